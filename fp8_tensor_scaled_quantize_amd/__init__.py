@@ -9,13 +9,16 @@ is missing, every call raises.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from ._lib import lib
 
 __all__ = ["E4M3", "E5M2", "F32", "F16", "BF16", "Fp8Error", "fp8_quantize", "fp8_quantize_dual", "fp8_quantize_dual_bias_grad",
            "fp8_quantize_dual_bias_grad_noalloc", "NOALLOC_SCRATCH_BYTES", "stream_reference",
-           "fp8_quantize_dynamic", "DYNAMIC_WORKSPACE_BYTES", "fp8_amax_fold", "fp8_mm", "fp8_mm_ex", "FP8_E4M3", "FP8_E5M2", "fp8_bias_grad", "fp8_bias_grad_workspace_bytes", "fp8_ring_seed", "new_ring", "ring_words", "version"]
+           "fp8_quantize_dynamic", "DYNAMIC_WORKSPACE_BYTES", "fp8_amax_fold", "fp8_mm", "fp8_mm_ex", "FP8_E4M3", "FP8_E5M2", "fp8_bias_grad", "fp8_bias_grad_workspace_bytes", "fp8_ring_seed", "new_ring", "ring_words", "version",
+           "fp8_rmsnorm", "fp8_rmsnorm_grad", "fp8_rmsnorm_grad_workspace_bytes"]
 
 E4M3, E5M2 = 0, 1
 F32, F16, BF16 = 0, 1, 2
@@ -504,3 +507,112 @@ def fp8_ring_seed(ring: torch.Tensor, amax: torch.Tensor, fmt) -> None:
     _scalar(amax, "amax")
     _on_device(ring, amax)
     _check(lib().fp8_ring_seed(rp, h, _ptr(amax), _fmt(fmt), _stream(ring)))
+
+
+def _rows2d(t: torch.Tensor, name: str):
+    """(rows, cols, leading dimension) of a 2-D tensor with unit column stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    rows, cols = t.shape
+    return rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
+    """Leading dimension of a matrix of x's shape and dtype."""
+    if t.dtype != x.dtype:
+        raise ValueError(f"{name} must be {x.dtype}, got {t.dtype}")
+    _matrix_out(t, x.shape, name)
+    return t.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _f32_vector(t: torch.Tensor, n: int, name: str) -> None:
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32, got {t.dtype}")
+    _vector(t, n, name)
+
+
+def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, fmt=E4M3, eps: float = 1e-6,
+                residual: torch.Tensor | None = None, out: torch.Tensor | None = None, row_scaled: bool = False,
+                scale: torch.Tensor | None = None, ring: torch.Tensor | None = None,
+                scale_inv_out: torch.Tensor | None = None, amax_out: torch.Tensor | None = None,
+                sum_out: torch.Tensor | None = None, rstd_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Root-mean-square norm of each row of x (+ residual), times weight, as
+    fp8 codes.  Exactly one of `scale`, `ring` and `row_scaled` picks the scale:
+    given, the ring's (which folds this call's amax), or measured per row --
+    then scale_inv_out [rows] receives the rows' dequantisation multipliers.
+    sum_out receives x + residual (it may be residual or x itself: in place),
+    rstd_out [rows] the 1 / rms values that fp8_rmsnorm_grad reads."""
+    rows, cols, ld_x = _rows2d(x, "x")
+    dt = _dt(x, "x")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+    out = _as_codes(out, "out")
+    _matrix_out(out, x.shape, "out")
+    wdt = 0
+    if weight is not None:
+        wdt = _dt(weight, "weight")
+        _vector(weight, cols, "weight")
+    ld_res = 0 if residual is None else _like(residual, x, "residual")
+    ld_sum = 0 if sum_out is None else _like(sum_out, x, "sum_out")
+    if row_scaled:
+        if scale is not None or ring is not None:
+            raise ValueError("row_scaled measures its scales: give neither scale nor ring")
+        if scale_inv_out is None:
+            raise ValueError("row_scaled needs scale_inv_out [rows]")
+        _f32_vector(scale_inv_out, rows, "scale_inv_out")
+        if amax_out is not None:
+            _f32_vector(amax_out, rows, "amax_out")
+    else:
+        _scalar(scale, "scale")
+        _scalar(scale_inv_out, "scale_inv_out")
+        _scalar(amax_out, "amax_out")
+    if rstd_out is not None:
+        _f32_vector(rstd_out, rows, "rstd_out")
+    rp, h = _ring_args(ring)
+    _on_device(x, weight, residual, out, scale, ring, scale_inv_out, amax_out, sum_out, rstd_out)
+    _check(lib().fp8_rmsnorm(x.data_ptr(), dt, rows, cols, ld_x, _ptr(residual), ld_res, _ptr(weight), wdt,
+                             ctypes.byref(ctypes.c_float(eps)), _fmt(fmt), out.data_ptr(),
+                             out.stride(0) if rows > 1 else cols, 1 if row_scaled else 0, _ptr(scale), rp, h,
+                             _ptr(scale_inv_out), _ptr(amax_out), _ptr(sum_out), ld_sum, _ptr(rstd_out), _stream(x)))
+    return out
+
+
+def fp8_rmsnorm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    """Device workspace fp8_rmsnorm_grad needs for its weight gradient."""
+    return int(lib().fp8_rmsnorm_grad_workspace_bytes(rows, cols))
+
+
+def fp8_rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
+                     dsum: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                     dweight: torch.Tensor | None = None, need_dweight: bool = True,
+                     workspace: torch.Tensor | None = None):
+    """Gradient of fp8_rmsnorm's normalised rows: returns (dx, dweight fp32 or
+    None).  h and rstd are the forward call's sum_out (or x) and rstd_out, dsum
+    the gradient that reaches h by the residual path (added into dx; dx may be
+    dsum or dy itself)."""
+    rows, cols, ld_dy = _rows2d(dy, "dy")
+    dt = _dt(dy, "dy")
+    ld_h = _like(h, dy, "h")
+    wdt = 0
+    if weight is not None:
+        wdt = _dt(weight, "weight")
+        _vector(weight, cols, "weight")
+    _f32_vector(rstd, rows, "rstd")
+    ld_ds = 0 if dsum is None else _like(dsum, dy, "dsum")
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
+    ld_dx = _like(dx, dy, "dx")
+    nbytes = 0
+    if need_dweight or dweight is not None:
+        if dweight is None:
+            dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        _f32_vector(dweight, cols, "dweight")
+        if workspace is None:
+            workspace = torch.empty(max(fp8_rmsnorm_grad_workspace_bytes(rows, cols), 4), dtype=torch.uint8,
+                                    device=dy.device)
+        nbytes = workspace.numel() * workspace.element_size()
+    _on_device(dy, h, weight, rstd, dsum, dx, dweight, workspace)
+    _check(lib().fp8_rmsnorm_grad(dy.data_ptr(), dt, rows, cols, ld_dy, h.data_ptr(), ld_h, _ptr(weight), wdt,
+                                  rstd.data_ptr(), _ptr(dsum), ld_ds, dx.data_ptr(), ld_dx, _ptr(dweight),
+                                  _ptr(workspace), nbytes, _stream(dy)))
+    return dx, dweight

@@ -53,6 +53,7 @@ int env_int_in(const char* name, int lo, int hi, int dflt) {
 }
 
 static_assert(kDynWorkspaceBytes == FP8MI_DYNAMIC_WORKSPACE_BYTES, "dynamic workspace size");
+static_assert(kNormMaxCols == FP8MI_NORM_MAX_COLS, "norm column limit");
 
 static bool valid_fmt(int f) { return f == FP8MI_E4M3 || f == FP8MI_E5M2; }
 static bool valid_dtype(int d) { return d == FP8MI_F32 || d == FP8MI_F16 || d == FP8MI_BF16; }
@@ -88,6 +89,36 @@ static fp8mi_status check_input(const void* x, int dt, int64_t rows, int64_t col
   if (reinterpret_cast<uintptr_t>(x) % dtype_bytes(dt)) return fail(FP8MI_ERR_ARG, "x not aligned to its element size");
   return FP8MI_OK;
 }
+
+// A further matrix of the norm calls (dtype dt, [rows, cols]): required, or
+// NULL when it is optional.
+static fp8mi_status check_matrix(const char* name, const void* m, bool required, int dt, int64_t rows, int64_t cols,
+                                 int64_t ld) {
+  if (!m) {
+    if (required && rows > 0 && cols > 0) return fail(FP8MI_ERR_NULL, "%s is NULL", name);
+    return FP8MI_OK;
+  }
+  if (rows > 0 && ld < cols)
+    return fail(FP8MI_ERR_SHAPE, "leading dimension %lld of %s < cols %lld", (long long)ld, name, (long long)cols);
+  if (!span_ok(rows, ld, dtype_bytes(dt)))
+    return fail(FP8MI_ERR_SHAPE, "%s: rows %lld x ld %lld beyond 2^62 bytes", name, (long long)rows, (long long)ld);
+  if (reinterpret_cast<uintptr_t>(m) % dtype_bytes(dt))
+    return fail(FP8MI_ERR_ARG, "%s not aligned to its element size", name);
+  return FP8MI_OK;
+}
+
+static fp8mi_status check_norm_weight(const void* weight, int dt, int64_t cols) {
+  if (cols > kNormMaxCols)
+    return fail(FP8MI_ERR_UNSUPPORTED, "cols %lld above FP8MI_NORM_MAX_COLS %lld", (long long)cols,
+                (long long)kNormMaxCols);
+  if (!weight) return FP8MI_OK;
+  if (!valid_dtype(dt)) return fail(FP8MI_ERR_ENUM, "weight_dtype %d is not FP8MI_F32/F16/BF16", dt);
+  if (reinterpret_cast<uintptr_t>(weight) % dtype_bytes(dt))
+    return fail(FP8MI_ERR_ARG, "weight not aligned to its element size");
+  return FP8MI_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static fp8mi_status check_outputs(int mode, int64_t rows, int64_t cols, const uint8_t* out_row, int64_t ld_row,
                                   const uint8_t* out_t, int64_t ld_t, const float* scale_inv_out,
@@ -408,6 +439,81 @@ fp8mi_status fp8_bias_grad(const void* dy, int dy_dtype, int64_t rows, int64_t c
   return from_hip(launch_grad_bias(dy, dy_dtype, rows, cols, ld, static_cast<uint16_t*>(out), workspace,
                                    static_cast<hipStream_t>(stream)),
                   "bias grad launch");
+}
+
+fp8mi_status fp8_rmsnorm(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                         int64_t ld_res, const void* weight, int weight_dtype, const float* eps, int fmt, uint8_t* out,
+                         int64_t ld_out, int scaling, const float* scale, uint32_t* ring, int32_t hist_len,
+                         float* scale_inv_out, float* amax_out, void* sum_out, int64_t ld_sum, float* rstd_out,
+                         void* stream) {
+  fp8mi_status s = check_input(x, x_dtype, rows, cols, ld_x);
+  if (s != FP8MI_OK) return s;
+  if (!valid_fmt(fmt)) return fail(FP8MI_ERR_ENUM, "fmt %d is not FP8MI_E4M3/FP8MI_E5M2", fmt);
+  s = check_norm_weight(weight, weight_dtype, cols);
+  if (s != FP8MI_OK) return s;
+  if (!eps) return fail(FP8MI_ERR_NULL, "eps is NULL");
+  if (!(*eps >= 0.0f)) return fail(FP8MI_ERR_ARG, "eps %g is not a number >= 0", (double)*eps);
+  if (scaling == FP8MI_SCALE_TENSOR) {
+    s = check_scale_ring(scale, ring, hist_len);
+    if (s != FP8MI_OK) return s;
+    if (!aligned4(scale)) return fail(FP8MI_ERR_ARG, "fp32 scalars must be 4-byte aligned");
+  } else if (scaling == FP8MI_SCALE_ROW) {
+    if (scale || ring) return fail(FP8MI_ERR_ARG, "row scaling measures its scales: give neither scale nor ring");
+    if (rows > 0 && !scale_inv_out) return fail(FP8MI_ERR_NULL, "row scaling needs scale_inv_out [rows]");
+  } else {
+    return fail(FP8MI_ERR_ENUM, "scaling %d is not FP8MI_SCALE_TENSOR/FP8MI_SCALE_ROW", scaling);
+  }
+  s = check_outputs(0, rows, cols, out, ld_out, nullptr, 0, scale_inv_out, amax_out);
+  if (s != FP8MI_OK) return s;
+  s = check_matrix("residual", residual, false, x_dtype, rows, cols, ld_res);
+  if (s != FP8MI_OK) return s;
+  s = check_matrix("sum_out", sum_out, false, x_dtype, rows, cols, ld_sum);
+  if (s != FP8MI_OK) return s;
+  if (!aligned4(rstd_out)) return fail(FP8MI_ERR_ARG, "rstd_out must be 4-byte aligned");
+  NormArgs p;
+  p.x = x; p.res = residual; p.weight = weight; p.weight_dt = weight_dtype;
+  p.rows = rows; p.cols = cols; p.ld_x = ld_x; p.ld_res = ld_res;
+  p.eps = *eps; p.n_cols = cols > 0 ? (float)cols : 1.0f;
+  p.out = out; p.ld_out = ld_out;
+  p.row_scaled = scaling == FP8MI_SCALE_ROW; p.scale = scale; p.ring = ring; p.H = hist_len;
+  p.scale_inv_out = scale_inv_out; p.amax_out = amax_out;
+  p.sum_out = sum_out; p.ld_sum = ld_sum; p.rstd_out = rstd_out;
+  return from_hip(launch_rmsnorm(p, x_dtype, fmt, static_cast<hipStream_t>(stream)), "rmsnorm launch");
+}
+
+size_t fp8_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols) {
+  return (size_t)fp8mi::rmsnorm_grad_workspace_bytes(rows, cols);
+}
+
+fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t cols, int64_t ld_dy, const void* h,
+                              int64_t ld_h, const void* weight, int weight_dtype, const float* rstd, const void* dsum,
+                              int64_t ld_dsum, void* dx, int64_t ld_dx, float* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  fp8mi_status s = check_input(dy, dtype, rows, cols, ld_dy);
+  if (s != FP8MI_OK) return s;
+  s = check_norm_weight(weight, weight_dtype, cols);
+  if (s != FP8MI_OK) return s;
+  s = check_matrix("h", h, true, dtype, rows, cols, ld_h);
+  if (s != FP8MI_OK) return s;
+  s = check_matrix("dsum", dsum, false, dtype, rows, cols, ld_dsum);
+  if (s != FP8MI_OK) return s;
+  s = check_matrix("dx", dx, true, dtype, rows, cols, ld_dx);
+  if (s != FP8MI_OK) return s;
+  if (rows > 0 && cols > 0 && !rstd) return fail(FP8MI_ERR_NULL, "rstd is NULL");
+  if (!aligned4(rstd) || !aligned4(dweight)) return fail(FP8MI_ERR_ARG, "rstd and dweight must be 4-byte aligned");
+  if (dweight) {
+    const size_t need = (size_t)rmsnorm_grad_workspace_bytes(rows, cols);
+    if (need > 0 && !workspace) return fail(FP8MI_ERR_NULL, "workspace is NULL (%zu bytes needed)", need);
+    if (workspace_bytes < need)
+      return fail(FP8MI_ERR_ARG, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+    if (!aligned4(workspace)) return fail(FP8MI_ERR_ARG, "workspace must be 4-byte aligned");
+  }
+  NormGradArgs p;
+  p.dy = dy; p.h = h; p.weight = weight; p.weight_dt = weight_dtype; p.rstd = rstd; p.dsum = dsum; p.dx = dx;
+  p.rows = rows; p.cols = cols; p.ld_dy = ld_dy; p.ld_h = ld_h; p.ld_dsum = ld_dsum; p.ld_dx = ld_dx;
+  p.n_cols = cols > 0 ? (float)cols : 1.0f;
+  return from_hip(launch_rmsnorm_grad(p, dtype, dweight, workspace, static_cast<hipStream_t>(stream)),
+                  "rmsnorm gradient launch");
 }
 
 fp8mi_status fp8_ring_seed(uint32_t* ring, int32_t hist_len, const float* amax, int fmt, void* stream) {

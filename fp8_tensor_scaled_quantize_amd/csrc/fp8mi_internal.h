@@ -90,6 +90,45 @@ hipError_t launch_grad_bias(const void* dy, int dt, int64_t rows, int64_t cols, 
                             void* workspace, hipStream_t st);
 // Second half of the bias gradient: adds the per-chunk sums in chunk order, one bf16 rounding.
 hipError_t launch_grad_bias_finalize(const double* ws, int64_t rows, int64_t cols, uint16_t* out, hipStream_t st);
+// Root-mean-square norm (rmsnorm.hip).  Rows of at most kNormMaxCols columns:
+// a row is held in one workgroup's registers.
+constexpr int64_t kNormMaxCols = 32768;
+struct NormArgs {
+  const void* x = nullptr;
+  const void* res = nullptr;      // residual, x's type, or null
+  const void* weight = nullptr;   // [cols], or null (ones)
+  int weight_dt = 0;
+  int64_t rows = 0, cols = 0, ld_x = 0, ld_res = 0;
+  float eps = 0.0f, n_cols = 1.0f;  // n_cols: cols as fp32 (1 when there are none)
+  uint8_t* out = nullptr;
+  int64_t ld_out = 0;
+  int row_scaled = 0;             // one scale per row, measured; else scale / ring
+  const float* scale = nullptr;
+  uint32_t* ring = nullptr;
+  int H = 0;
+  float* scale_inv_out = nullptr;  // one word, or [rows] with row_scaled
+  float* amax_out = nullptr;
+  void* sum_out = nullptr;        // x + res in x's type, or null
+  int64_t ld_sum = 0;
+  float* rstd_out = nullptr;      // [rows], or null
+};
+hipError_t launch_rmsnorm(const NormArgs& p, int dt, int fmt, hipStream_t st);
+
+struct NormGradArgs {
+  const void* dy = nullptr;
+  const void* h = nullptr;
+  const void* weight = nullptr;
+  int weight_dt = 0;
+  const float* rstd = nullptr;
+  const void* dsum = nullptr;     // gradient that reaches h by the residual path, or null
+  void* dx = nullptr;
+  int64_t rows = 0, cols = 0, ld_dy = 0, ld_h = 0, ld_dsum = 0, ld_dx = 0;
+  float n_cols = 1.0f;
+  float* parts = nullptr;         // set by the launch: one fp32 row per workgroup, or null
+};
+int64_t rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_grad(const NormGradArgs& p, int dt, float* dweight, void* workspace, hipStream_t st);
+
 hipError_t launch_ring_seed(uint32_t* ring, int H, const float* amax, int fmt, hipStream_t st);
 // Measurement aid (stream.hip): read src_bytes, write dst_bytes (= src_bytes or its half).
 hipError_t launch_stream(const void* src, int64_t src_bytes, void* dst, int64_t dst_bytes, hipStream_t st);

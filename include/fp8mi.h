@@ -327,6 +327,73 @@ FP8MI_API fp8mi_status fp8_bias_grad(const void* dy, int dy_dtype, int64_t rows,
 FP8MI_API size_t fp8_bias_grad_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
+ * fp8_rmsnorm -- root-mean-square norm of each row, with the residual's
+ * addition and an fp8 output (the input of a linear layer's fp8_mm):
+ *   h(i,j) = x(i,j) + residual(i,j)               (fp32; x alone without a residual)
+ *   rstd_i = 1 / sqrt(sum_j h(i,j)^2 / cols + eps)
+ *   y(i,j) = fl32(fl32(h(i,j) * rstd_i) * weight_j)
+ *   out(i,j) = enc(fl32(y(i,j) * s)), all sums in fp32.
+ *   x          device, element (i, j) at x[i * ld_x + j], dtype FP8MI_F32 / F16 /
+ *              BF16; any element-aligned base, ld_x >= cols.
+ *   residual   device, x's dtype, ld_res >= cols; NULL for none.
+ *   weight     device [cols] of weight_dtype FP8MI_F32 / F16 / BF16; NULL for ones.
+ *   eps        HOST pointer to one fp32 >= 0, read before the call returns.
+ *   out        device codes, ld_out >= cols; bytes outside them are not written.
+ *   scaling    FP8MI_SCALE_TENSOR: exactly one of scale / ring, as fp8_quantize
+ *              (the ring folds amax = max |y|, NaN ignored); scale_inv_out and
+ *              amax_out are optional fp32 words.
+ *              FP8MI_SCALE_ROW: one scale per row, measured: s_i = fmt_max /
+ *              max_j |y(i,j)| (1.0 in the cases fp8_quantize_dynamic names);
+ *              scale and ring are NULL, scale_inv_out is [rows] (required: the
+ *              row multipliers fp8_mm_act takes), amax_out [rows] or NULL.
+ *   sum_out    optional device, x's dtype, ld_sum >= cols: h rounded once.  It may
+ *              be the residual itself or x itself (same pointer and leading
+ *              dimension): the residual stream is then updated in place.
+ *   rstd_out   optional device fp32 [rows] (for fp8_rmsnorm_grad).
+ * cols is at most FP8MI_NORM_MAX_COLS (else FP8MI_ERR_UNSUPPORTED): a row is
+ * held in one workgroup's registers.  rows == 0 writes no codes; a ring still
+ * folds amax 0.  A row of zeros with eps = 0 has rstd = inf and NaN codes, as
+ * the formula says.  One launch (two with an explicit scale and amax_out).
+ */
+#define FP8MI_NORM_MAX_COLS 32768
+typedef enum { FP8MI_SCALE_TENSOR = 0, FP8MI_SCALE_ROW = 1 } fp8mi_scaling;
+FP8MI_API fp8mi_status fp8_rmsnorm(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                                   const void* residual, int64_t ld_res, const void* weight, int weight_dtype,
+                                   const float* eps, int fmt, uint8_t* out, int64_t ld_out, int scaling,
+                                   const float* scale, uint32_t* ring, int32_t hist_len, float* scale_inv_out,
+                                   float* amax_out, void* sum_out, int64_t ld_sum, float* rstd_out, void* stream);
+
+/*
+ * fp8_rmsnorm_grad -- gradient of fp8_rmsnorm's y with respect to h (so to x
+ * and to the residual alike) and to the weight:
+ *   g(i,j)  = dy(i,j) * weight_j
+ *   dx(i,j) = rstd_i g(i,j) - rstd_i^3 (sum_j g(i,j) h(i,j) / cols) h(i,j) + dsum(i,j)
+ *   dweight_j = sum_i dy(i,j) h(i,j) rstd_i
+ *   dy         device, dtype FP8MI_F32 / F16 / BF16, ld_dy >= cols.
+ *   h          device, dy's dtype: the forward call's sum_out (or x).
+ *   rstd       device fp32 [rows]: the forward call's rstd_out.
+ *   dsum       device, dy's dtype: the gradient that reaches h by the residual
+ *              path (h's other use); NULL for none.
+ *   dx         device, dy's dtype, rounded once from fp32; may be dsum or dy
+ *              itself (same pointer and leading dimension).
+ *   dweight    device fp32 [cols], or NULL when it is not wanted.  fp32 sums per
+ *              workgroup, added in fp64 in a fixed order: the same every call.
+ *   workspace  device scratch of fp8_rmsnorm_grad_workspace_bytes(rows, cols)
+ *              bytes, 4-byte aligned, caller-owned, no initialisation; not
+ *              needed without dweight.  Calls in flight on one workspace race.
+ * rows == 0 writes zeros to dweight; cols == 0 is a no-op.  Limits of cols as
+ * fp8_rmsnorm.  Two launches (one without dweight).
+ */
+FP8MI_API fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t cols, int64_t ld_dy,
+                                        const void* h, int64_t ld_h, const void* weight, int weight_dtype,
+                                        const float* rstd, const void* dsum, int64_t ld_dsum, void* dx,
+                                        int64_t ld_dx, float* dweight, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Device workspace of fp8_rmsnorm_grad for [rows, cols]; pure host function. */
+FP8MI_API size_t fp8_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
  * fp8_ring_seed -- (re)initialise a ring on the device: history, ticket and
  * scratch set to 0, slot 0, and current scale = the scale a fold of *amax
  * into an empty window would publish (fmt_max / amax, or 1.0 when amax is 0
