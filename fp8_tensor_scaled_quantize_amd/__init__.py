@@ -18,12 +18,18 @@ from ._lib import lib
 __all__ = ["E4M3", "E5M2", "F32", "F16", "BF16", "Fp8Error", "fp8_quantize", "fp8_quantize_dual", "fp8_quantize_dual_bias_grad",
            "fp8_quantize_dual_bias_grad_noalloc", "NOALLOC_SCRATCH_BYTES", "stream_reference",
            "fp8_quantize_dynamic", "DYNAMIC_WORKSPACE_BYTES", "fp8_amax_fold", "fp8_mm", "fp8_mm_ex", "FP8_E4M3", "FP8_E5M2", "fp8_bias_grad", "fp8_bias_grad_workspace_bytes", "fp8_ring_seed", "new_ring", "ring_words", "version",
-           "fp8_rmsnorm", "fp8_rmsnorm_grad", "fp8_rmsnorm_grad_workspace_bytes"]
+           "fp8_rmsnorm", "fp8_rmsnorm_grad", "fp8_rmsnorm_grad_workspace_bytes", "fp8_mm_act", "fp8_act_grad",
+           "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_SILU", "interleave_gated"]
 
 E4M3, E5M2 = 0, 1
 F32, F16, BF16 = 0, 1, 2
 FP8_E4M3, FP8_E5M2 = 3, 4  # fp8 storage types (fp8 bias / fp8 GEMM output of fp8_mm_ex)
 
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3  # activations of fp8_mm_act (gelu: the tanh form)
+_ACT_GATED = 16
+
+_ACT = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "silu": ACT_SILU, None: ACT_NONE,
+        ACT_NONE: ACT_NONE, ACT_RELU: ACT_RELU, ACT_GELU: ACT_GELU, ACT_SILU: ACT_SILU}
 _FMT = {"e4m3": E4M3, "e5m2": E5M2, E4M3: E4M3, E5M2: E5M2}
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 RING_SCRATCH_WORDS = 1024  # FP8MI_RING_SCRATCH_WORDS
@@ -616,3 +622,134 @@ def fp8_rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | N
                                   rstd.data_ptr(), _ptr(dsum), ld_ds, dx.data_ptr(), ld_dx, _ptr(dweight),
                                   _ptr(workspace), nbytes, _stream(dy)))
     return dx, dweight
+
+
+def _act(act, gated: bool) -> int:
+    try:
+        return _ACT[act] | (_ACT_GATED if gated else 0)
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {act!r}") from None
+
+
+def interleave_gated(gate: torch.Tensor, value: torch.Tensor) -> torch.Tensor:
+    """The weight (or bias, or its codes) of a gated product from its two
+    halves: rows 2j and 2j + 1 are row j of gate and of value."""
+    if gate.shape != value.shape or gate.dtype != value.dtype:
+        raise ValueError(f"gate {tuple(gate.shape)} {gate.dtype} and value {tuple(value.shape)} {value.dtype} differ")
+    return torch.stack((gate, value), dim=1).flatten(0, 1)
+
+
+def _row_scales(t, n: int, name: str) -> int:
+    """1 where t holds one multiplier per row, 0 for one per tensor (or none)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.numel() not in (1, n):
+        raise ValueError(f"{name} must be a float32 tensor of 1 or {n} elements")
+    if n > 1 and t.numel() == n:
+        _vector(t, n, name)
+        return 1
+    return 0
+
+
+def fp8_mm_act(a: torch.Tensor, b: torch.Tensor, a_scale_inv: torch.Tensor | None = None,
+               b_scale_inv: torch.Tensor | None = None, bias: torch.Tensor | None = None, act=ACT_NONE,
+               gated: bool = False, residual: torch.Tensor | None = None, z_out: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, out_fmt=None, out_scale: torch.Tensor | None = None,
+               out_ring: torch.Tensor | None = None, out_scale_inv: torch.Tensor | None = None,
+               out_amax: torch.Tensor | None = None) -> torch.Tensor:
+    """E4M3 codes A [M, K] and B [N, K]: f(A B^T sa sb + bias) + residual as
+    bf16, or with out_fmt=E4M3 as codes quantized with out_scale or out_ring.
+    The scale multipliers hold one word, or one per row of their operand.
+    gated: B's rows alternate gate and value (interleave_gated) and the output
+    is f(gate) * value + residual, [M, N / 2].  z_out (bf16 [M, N]) receives
+    the values before the activation, for fp8_act_grad.  A bf16 residual may be
+    `out` itself."""
+    a, b = _as_codes(a, "a"), _as_codes(b, "b")
+    M, K, lda = _rows2d(a, "a")
+    N, Kb, ldb = _rows2d(b, "b")
+    if K != Kb:
+        raise ValueError(f"K mismatch: {tuple(a.shape)} vs {tuple(b.shape)}")
+    code = _act(act, gated)
+    if gated and N % 2:
+        raise ValueError(f"a gated product needs an even number of rows in b, got {N}")
+    No = N // 2 if gated else N
+    fp8_out = out_fmt is not None
+    if fp8_out and _fmt(out_fmt) != E4M3:
+        raise ValueError("fp8_mm_act's fp8 output is E4M3")
+    if out is None:
+        out = torch.empty((M, No), dtype=torch.uint8 if fp8_out else torch.bfloat16, device=a.device)
+    if fp8_out:
+        out = _as_codes(out, "out")
+    elif out.dtype != torch.bfloat16:
+        raise ValueError(f"out must be bfloat16, got {out.dtype}")
+    _matrix_out(out, (M, No), "out")
+    rows = _row_scales(a_scale_inv, M, "a_scale_inv") | (_row_scales(b_scale_inv, N, "b_scale_inv") << 1)
+    bias_dt = res_dt = 0
+    ld_res = ld_z = 0
+    if bias is not None:
+        bias_dt = _dt(bias, "bias")
+        _vector(bias, N, "bias")
+    if residual is not None:
+        res_dt = _dt(residual, "residual")
+        _matrix_out(residual, (M, No), "residual")
+        ld_res = residual.stride(0) if M > 1 else No
+    if z_out is not None:
+        if z_out.dtype != torch.bfloat16:
+            raise ValueError(f"z_out must be bfloat16, got {z_out.dtype}")
+        _matrix_out(z_out, (M, N), "z_out")
+        ld_z = z_out.stride(0) if M > 1 else N
+    if fp8_out:
+        for t, name in ((out_scale, "out_scale"), (out_scale_inv, "out_scale_inv"), (out_amax, "out_amax")):
+            _scalar(t, name)
+    rp, h = _ring_args(out_ring)
+    _on_device(a, b, a_scale_inv, b_scale_inv, bias, residual, z_out, out, out_scale, out_ring, out_scale_inv, out_amax)
+    _check(lib().fp8_mm_act(a.data_ptr(), lda, b.data_ptr(), ldb, M, N, K, _ptr(a_scale_inv), _ptr(b_scale_inv), rows,
+                            _ptr(bias), bias_dt, code, _ptr(residual), res_dt, ld_res, _ptr(z_out), ld_z,
+                            out.data_ptr(), FP8_E4M3 if fp8_out else BF16, out.stride(0) if M > 1 else No,
+                            _ptr(out_scale), rp, h, _ptr(out_scale_inv), _ptr(out_amax), _stream(a)))
+    return out
+
+
+def fp8_act_grad(dy: torch.Tensor, z: torch.Tensor, act, gated: bool = False, fmt=E5M2,
+                 out_row: torch.Tensor | None = None, out_t: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None, ring: torch.Tensor | None = None,
+                 scale_inv_out: torch.Tensor | None = None, amax_out: torch.Tensor | None = None,
+                 need_bias_grad: bool = False, bias_grad_out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None):
+    """Gradient dz of fp8_mm_act's pre-activations (z, its z_out) from the
+    gradient dy of its output, quantized with `scale` or `ring`: returns
+    (codes [rows, cols], codes_t [cols, rows], bias gradient bf16 or None)."""
+    drows, dcols, ld_dy = _rows2d(dy, "dy")
+    rows, cols, ld_z = _rows2d(z, "z")
+    if z.dtype != torch.bfloat16:
+        raise ValueError(f"z must be bfloat16, got {z.dtype}")
+    if (drows, dcols * (2 if gated else 1)) != (rows, cols):
+        raise ValueError(f"dy {tuple(dy.shape)} does not fit z {tuple(z.shape)}" + (" (gated)" if gated else ""))
+    dt, code, f = _dt(dy, "dy"), _act(act, gated), _fmt(fmt)
+    if out_row is None:
+        out_row = torch.empty((rows, cols), dtype=torch.uint8, device=dy.device)
+    if out_t is None:
+        out_t = torch.empty((cols, rows), dtype=torch.uint8, device=dy.device)
+    out_row, out_t = _as_codes(out_row, "out_row"), _as_codes(out_t, "out_t")
+    _matrix_out(out_row, (rows, cols), "out_row")
+    _matrix_out(out_t, (cols, rows), "out_t")
+    for t, name in ((scale, "scale"), (scale_inv_out, "scale_inv_out"), (amax_out, "amax_out")):
+        _scalar(t, name)
+    nbytes = 0
+    if need_bias_grad or bias_grad_out is not None:
+        if bias_grad_out is None:
+            bias_grad_out = torch.empty(cols, dtype=torch.bfloat16, device=dy.device)
+        _vector(bias_grad_out, cols, "bias_grad_out")
+        if bias_grad_out.dtype != torch.bfloat16:
+            raise ValueError("bias_grad_out must be bfloat16")
+        if workspace is None:
+            workspace = torch.empty(max(fp8_bias_grad_workspace_bytes(rows, cols), 8), dtype=torch.uint8,
+                                    device=dy.device)
+        nbytes = workspace.numel() * workspace.element_size()
+    rp, h = _ring_args(ring)
+    _on_device(dy, z, out_row, out_t, scale, ring, scale_inv_out, amax_out, bias_grad_out, workspace)
+    _check(lib().fp8_act_grad(dy.data_ptr(), dt, rows, cols, ld_dy, z.data_ptr(), ld_z, code, f, out_row.data_ptr(),
+                              out_row.stride(0) if rows > 1 else cols, out_t.data_ptr(),
+                              out_t.stride(0) if cols > 1 else rows, _ptr(scale), rp, h, _ptr(scale_inv_out),
+                              _ptr(amax_out), _ptr(bias_grad_out), _ptr(workspace), nbytes, _stream(dy)))
+    return out_row, out_t, bias_grad_out

@@ -25,6 +25,10 @@ SIGNATURES = {
                             _P, _I, _I64, _I64, _P, _P, _I32, _P, _P, _P]),
     "fp8_bias_grad": (C.c_int, [_P, _I, _I64, _I64, _I64, _P, _P, C.c_size_t, _P]),
     "fp8_bias_grad_workspace_bytes": (C.c_size_t, [_I64, _I64]),
+    "fp8_mm_act": (C.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _I, _I, _P, _I, _I64, _P, _I64, _P,
+                             _I, _I64, _P, _P, _I32, _P, _P, _P]),
+    "fp8_act_grad": (C.c_int, [_P, _I, _I64, _I64, _I64, _P, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P, _I32, _P, _P, _P,
+                               _P, C.c_size_t, _P]),
     "fp8_rmsnorm": (C.c_int, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, _P, _I, _P, _I64, _I, _P, _P, _I32, _P, _P,
                               _P, _I64, _P, _P]),
     "fp8_rmsnorm_grad": (C.c_int, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, _P, _P, _I64, _P, _I64, _P, _P,

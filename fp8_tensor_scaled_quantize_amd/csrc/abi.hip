@@ -118,6 +118,14 @@ static fp8mi_status check_norm_weight(const void* weight, int dt, int64_t cols) 
   return FP8MI_OK;
 }
 
+// act: an activation, optionally gated.
+static fp8mi_status check_act(int act, int* kind, bool* gated) {
+  *gated = act >= 0 && (act & FP8MI_ACT_GATED) != 0;
+  *kind = act & ~FP8MI_ACT_GATED;
+  if (act < 0 || *kind > FP8MI_ACT_SILU) return fail(FP8MI_ERR_ENUM, "act %d is not an FP8MI_ACT value", act);
+  return FP8MI_OK;
+}
+
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static fp8mi_status check_outputs(int mode, int64_t rows, int64_t cols, const uint8_t* out_row, int64_t ld_row,
@@ -479,6 +487,122 @@ fp8mi_status fp8_rmsnorm(const void* x, int x_dtype, int64_t rows, int64_t cols,
   p.scale_inv_out = scale_inv_out; p.amax_out = amax_out;
   p.sum_out = sum_out; p.ld_sum = ld_sum; p.rstd_out = rstd_out;
   return from_hip(launch_rmsnorm(p, x_dtype, fmt, static_cast<hipStream_t>(stream)), "rmsnorm launch");
+}
+
+fp8mi_status fp8_mm_act(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                        const float* a_scale_inv, const float* b_scale_inv, int scale_rows, const void* bias,
+                        int bias_dtype, int act, const void* residual, int residual_dtype, int64_t ld_res, void* z_out,
+                        int64_t ld_z, void* c, int c_dtype, int64_t ldc, const float* c_scale, uint32_t* c_ring,
+                        int32_t c_hist_len, float* c_scale_inv_out, float* c_amax_out, void* stream) {
+  int kind;
+  bool gated;
+  fp8mi_status s = check_act(act, &kind, &gated);
+  if (s != FP8MI_OK) return s;
+  if (scale_rows < 0 || scale_rows > 3)
+    return fail(FP8MI_ERR_ENUM, "scale_rows %d is not a combination of FP8MI_A_ROW_SCALES / FP8MI_B_ROW_SCALES", scale_rows);
+  if (((scale_rows & FP8MI_A_ROW_SCALES) && !a_scale_inv) || ((scale_rows & FP8MI_B_ROW_SCALES) && !b_scale_inv))
+    return fail(FP8MI_ERR_NULL, "row scales are announced but their array is NULL");
+  if (bias && !valid_dtype(bias_dtype)) return fail(FP8MI_ERR_ENUM, "bias_dtype %d is not F32/F16/BF16", bias_dtype);
+  if (residual && !valid_dtype(residual_dtype))
+    return fail(FP8MI_ERR_ENUM, "residual_dtype %d is not F32/F16/BF16", residual_dtype);
+  const bool fp8_out = c_dtype == FP8MI_FP8_E4M3;
+  if (c_dtype == FP8MI_FP8_E5M2) return fail(FP8MI_ERR_UNSUPPORTED, "fp8_mm_act's fp8 output is E4M3");
+  if (c_dtype != FP8MI_BF16 && !fp8_out) return fail(FP8MI_ERR_ENUM, "c_dtype %d is not BF16/FP8_E4M3", c_dtype);
+  if (fp8_out) {
+    s = check_scale_ring(c_scale, c_ring, c_hist_len);
+    if (s != FP8MI_OK) return s;
+  } else if (c_scale || c_ring || c_scale_inv_out || c_amax_out) {
+    return fail(FP8MI_ERR_ARG, "output scale, ring, scale_inv and amax are for an fp8 output only");
+  }
+  if (M < 0 || N < 0 || K < 0)
+    return fail(FP8MI_ERR_SHAPE, "negative size M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+  if (gated && (N & 1)) return fail(FP8MI_ERR_SHAPE, "a gated product needs an even N, got %lld", (long long)N);
+  const int64_t No = gated ? N / 2 : N;
+  if (!aligned4(a_scale_inv) || !aligned4(b_scale_inv) || !aligned4(c_scale) || !aligned4(c_scale_inv_out) ||
+      !aligned4(c_amax_out))
+    return fail(FP8MI_ERR_ARG, "fp32 scales must be 4-byte aligned");
+  if (M > 0 && N > 0) {
+    if (!c) return fail(FP8MI_ERR_NULL, "c is NULL");
+    if (K > 0 && (!a || !b)) return fail(FP8MI_ERR_NULL, "a or b is NULL");
+    if (ldc < No) return fail(FP8MI_ERR_SHAPE, "ldc %lld < outputs %lld", (long long)ldc, (long long)No);
+    if (K > 0 && (lda < K || ldb < K))
+      return fail(FP8MI_ERR_SHAPE, "lda %lld / ldb %lld < K %lld", (long long)lda, (long long)ldb, (long long)K);
+    if ((K > 0 && (!span_ok(M, lda, 1) || !span_ok(N, ldb, 1))) || !span_ok(M, ldc, fp8_out ? 1 : 2))
+      return fail(FP8MI_ERR_SHAPE, "an operand or output extent is beyond 2^62 bytes");
+    s = check_matrix("z_out", z_out, false, FP8MI_BF16, M, N, ld_z);
+    if (s != FP8MI_OK) return s;
+    if (residual) {
+      s = check_matrix("residual", residual, false, residual_dtype, M, No, ld_res);
+      if (s != FP8MI_OK) return s;
+    }
+    if (!fp8_out && (reinterpret_cast<uintptr_t>(c) & 1u)) return fail(FP8MI_ERR_ARG, "c must be 2-byte aligned");
+    if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_bytes(bias_dtype))
+      return fail(FP8MI_ERR_ARG, "bias not aligned to its element size");
+    if (K > 0) {
+      if ((K % 16) || (lda % 16) || (ldb % 16))
+        return fail(FP8MI_ERR_UNSUPPORTED, "K, lda and ldb must be multiples of 16 (K=%lld lda=%lld ldb=%lld)",
+                    (long long)K, (long long)lda, (long long)ldb);
+      if ((reinterpret_cast<uintptr_t>(a) & 15u) || (reinterpret_cast<uintptr_t>(b) & 15u))
+        return fail(FP8MI_ERR_UNSUPPORTED, "a and b must be 16-byte aligned");
+    }
+    if ((M + 63) / 64 > 65535 || (N + 31) / 32 > 0x1FFFFFFF / ((M + 63) / 64))
+      return fail(FP8MI_ERR_UNSUPPORTED, "M=%lld N=%lld beyond the launch grid", (long long)M, (long long)N);
+  }
+  MmActArgs p;
+  p.a = a; p.b = b; p.lda = lda; p.ldb = ldb; p.M = M; p.N = N; p.K = K; p.batch = 1;
+  p.a_scale_inv = a_scale_inv; p.b_scale_inv = b_scale_inv;
+  p.a_rows = (scale_rows & FP8MI_A_ROW_SCALES) != 0; p.b_rows = (scale_rows & FP8MI_B_ROW_SCALES) != 0;
+  p.bias = bias; p.bias_dtype = bias ? bias_dtype : -1;
+  p.act = kind; p.res = residual; p.res_dt = residual_dtype; p.ld_res = ld_res;
+  p.z = static_cast<uint16_t*>(z_out); p.ld_z = ld_z;
+  p.c = c; p.ldc = ldc; p.out_fmt = fp8_out ? (int)FP8MI_E4M3 : -1;
+  p.c_scale = c_scale; p.c_ring = c_ring; p.c_H = c_hist_len;
+  p.c_scale_inv_out = c_scale_inv_out; p.c_amax_out = c_amax_out;
+  if (M > 0 && N > 0 &&
+      !(p.a_extent_from(0) < (1ll << 31) && p.b_extent_from(0) < (1ll << 31) && K < (1ll << 30)))
+    return fail(FP8MI_ERR_UNSUPPORTED, "fp8_mm_act needs operand extents below 2^31 bytes");
+  return from_hip(launch_mm_act(p, gated, static_cast<hipStream_t>(stream)), "mm_act launch");
+}
+
+fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, int64_t cols, int64_t ld_dy, const void* z,
+                          int64_t ld_z, int act, int fmt, uint8_t* out_row, int64_t ld_row, uint8_t* out_t,
+                          int64_t ld_t, const float* scale, uint32_t* ring, int32_t hist_len, float* scale_inv_out,
+                          float* amax_out, void* bias_grad_out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int kind;
+  bool gated;
+  fp8mi_status s = check_act(act, &kind, &gated);
+  if (s != FP8MI_OK) return s;
+  if (kind == FP8MI_ACT_NONE && !gated)
+    return fail(FP8MI_ERR_ARG, "without an activation dz is dy: use fp8_quantize_dual");
+  if (gated && (cols & 1)) return fail(FP8MI_ERR_SHAPE, "a gated gradient needs an even cols, got %lld", (long long)cols);
+  s = check_input(dy, dy_dtype, rows, gated ? cols / 2 : cols, ld_dy);
+  if (s != FP8MI_OK) return s;
+  if (dy_dtype == FP8MI_F32) return fail(FP8MI_ERR_UNSUPPORTED, "fp8_act_grad takes bf16 or fp16 gradients");
+  s = check_matrix("z", z, true, FP8MI_BF16, rows, cols, ld_z);
+  if (s != FP8MI_OK) return s;
+  if (!valid_fmt(fmt)) return fail(FP8MI_ERR_ENUM, "fmt %d is not FP8MI_E4M3/FP8MI_E5M2", fmt);
+  s = check_scale_ring(scale, ring, hist_len);
+  if (s != FP8MI_OK) return s;
+  if (!aligned4(scale)) return fail(FP8MI_ERR_ARG, "fp32 scalars must be 4-byte aligned");
+  s = check_outputs(2, rows, cols, out_row, ld_row, out_t, ld_t, scale_inv_out, amax_out);
+  if (s != FP8MI_OK) return s;
+  if ((rows + 127) / 128 > 0 && (cols + 63) / 64 > 0x7FFFFFFF / ((rows + 127) / 128))
+    return fail(FP8MI_ERR_UNSUPPORTED, "rows=%lld cols=%lld beyond the launch grid", (long long)rows, (long long)cols);
+  if (bias_grad_out) {
+    s = check_bias_grad(dy_dtype, rows, cols, bias_grad_out, workspace, workspace_bytes);
+    if (s != FP8MI_OK) return s;
+  }
+  ActGradArgs p;
+  p.dy = dy; p.z = static_cast<const uint16_t*>(z); p.rows = rows; p.cols = cols; p.ld_dy = ld_dy; p.ld_z = ld_z;
+  p.out_row = out_row; p.ld_row = ld_row; p.out_t = out_t; p.ld_t = ld_t;
+  p.scale = scale; p.ring = ring; p.H = hist_len; p.scale_inv_out = scale_inv_out; p.amax_out = amax_out;
+  p.bias_ws = bias_grad_out ? static_cast<double*>(workspace) : nullptr;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  s = from_hip(launch_act_grad(p, dy_dtype, fmt, kind, gated, st), "activation gradient launch");
+  if (s != FP8MI_OK || !bias_grad_out || cols == 0) return s;
+  return from_hip(launch_grad_bias_finalize(p.bias_ws, rows, cols, static_cast<uint16_t*>(bias_grad_out), st),
+                  "bias grad finalize launch");
 }
 
 size_t fp8_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols) {

@@ -1,0 +1,54 @@
+// The activations of the fused epilogue and of its gradient, in fp32.  With
+// p(t) = 1 / (1 + exp(-q(t))):
+//   silu(t) = t p(t),  q = t
+//   gelu(t) = t p(t),  q = 2 sqrt(2 / pi) (t + 0.044715 t^3)   (the tanh form:
+//             (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)))
+//   slope   = p + t p (1 - p) q'(t)
+// exp is the hardware's exp2 of q log2(e), the quotient its reciprocal: each
+// within about 1 ulp, so p is within 2^-24 (|q| + 4) of exact -- far below the
+// bf16 or fp8 rounding that follows.  exp(-q) = inf gives p = 0 and exp(-q) = 0
+// gives p = 1, so large |t| needs no branch.
+#pragma once
+#include "fp8mi_device.h"
+
+namespace fp8mi {
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kGelu2c = 1.59576912160573071f;  // 2 sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+template <int ACT> __device__ __forceinline__ float act_p(float t) {
+  const float q = ACT == kActGelu ? kGelu2c * fmaf(kGeluA * t, t * t, t) : t;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * q));
+}
+
+// relu keeps a NaN.
+__device__ __forceinline__ float relu(float t) { return t > 0.0f || t != t ? t : 0.0f; }
+
+template <int ACT> __device__ __forceinline__ float act_value(float t) {
+  if constexpr (ACT == kActNone) return t;
+  else if constexpr (ACT == kActRelu) return relu(t);
+  else return t * act_p<ACT>(t);
+}
+
+// Value and slope.  Where p is 0 or 1 the slope's second term is 0: without
+// the test, a t whose cube or square overflows would make it inf * 0.
+template <int ACT> __device__ __forceinline__ void act_value_slope(float t, float& value, float& slope) {
+  if constexpr (ACT == kActNone) {
+    value = t;
+    slope = 1.0f;
+  } else if constexpr (ACT == kActRelu) {
+    value = relu(t);
+    slope = t > 0.0f ? 1.0f : 0.0f;
+  } else {
+    const float p = act_p<ACT>(t);
+    const float dq = ACT == kActGelu ? kGelu2c * fmaf(3.0f * kGeluA * t, t, 1.0f) : 1.0f;
+    const float pq = p * (1.0f - p);
+    value = t * p;
+    slope = pq == 0.0f ? p : fmaf(t * pq, dq, p);
+  }
+}
+
+}  // namespace fp8mi

@@ -32,6 +32,7 @@ hipError_t launch_quantize_dynamic(const void* x, int dt, int64_t rows, int64_t 
 hipError_t launch_amax_fold(uint32_t* ring, int H, const float* amax, int fmt, hipStream_t st);
 
 struct MmArgs {
+  static constexpr bool kAct = false;  // the plain epilogue
   const uint8_t* a = nullptr;
   const uint8_t* b = nullptr;
   int64_t lda = 0, ldb = 0, stride_a = 0, stride_b = 0;
@@ -83,6 +84,45 @@ hipError_t launch_mm_prec_q8(const MmArgs& p, int fmt_a, int fmt_b, hipStream_t 
 hipError_t launch_mm_prec_km_q8(const MmArgs& p, int fmt_a, int fmt_b, hipStream_t st);
 // One fp32 word set to 0 on the stream (a fill kernel, capturable).
 hipError_t launch_zero_word(float* p, hipStream_t st);
+
+// GEMM with bias, activation (optionally gated) and residual in its epilogue
+// (mm_act_kernel.h): E4M3 operands, NT, one batch, operand extents below 2^31
+// bytes.  Gated: weight rows 2j / 2j + 1 give the gate and the value of output
+// column j.
+struct MmActArgs : MmArgs {
+  static constexpr bool kAct = true;
+  int a_rows = 0, b_rows = 0;       // a_scale_inv is [M] / b_scale_inv is [N], else one word each
+  int act = 0;                      // Act
+  const void* res = nullptr;        // [M, output columns], or null
+  int res_dt = 0;
+  int64_t ld_res = 0;
+  uint16_t* z = nullptr;            // pre-activations, bf16 [M, N], or null
+  int64_t ld_z = 0;
+};
+hipError_t launch_mm_act(const MmActArgs& p, bool gated, hipStream_t st);
+// one output type and gating each
+hipError_t launch_mm_act_bf16(const MmActArgs& p, hipStream_t st);
+hipError_t launch_mm_act_bf16_gated(const MmActArgs& p, hipStream_t st);
+hipError_t launch_mm_act_q8(const MmActArgs& p, hipStream_t st);
+hipError_t launch_mm_act_q8_gated(const MmActArgs& p, hipStream_t st);
+
+// Gradient through the activation, quantized in both layouts (act_grad.hip).
+struct ActGradArgs {
+  const void* dy = nullptr;         // [rows, cols], or [rows, cols / 2] gated
+  const uint16_t* z = nullptr;      // bf16 [rows, cols]
+  int64_t rows = 0, cols = 0, ld_dy = 0, ld_z = 0;
+  uint8_t* out_row = nullptr;
+  int64_t ld_row = 0;
+  uint8_t* out_t = nullptr;
+  int64_t ld_t = 0;
+  const float* scale = nullptr;
+  uint32_t* ring = nullptr;
+  int H = 0;
+  float* scale_inv_out = nullptr;
+  float* amax_out = nullptr;
+  double* bias_ws = nullptr;        // fp64 column sums per 128-row tile, or null
+};
+hipError_t launch_act_grad(const ActGradArgs& p, int dt, int fmt, int act, bool gated, hipStream_t st);
 
 // Bytes of fp64 workspace the bias gradient needs (per-chunk column sums).
 int64_t grad_bias_workspace_bytes(int64_t rows, int64_t cols);

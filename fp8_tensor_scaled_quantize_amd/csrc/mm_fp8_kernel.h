@@ -279,12 +279,20 @@ template <int BM, int BN, int NWAVES, int DEEP> struct TileLds {
   static constexpr int kBias = kSmem;           // BN floats
   static constexpr int kRed = kBias + 4 * BN;   // NWAVES + 1 words
   static constexpr int kBytes = kRed + 4 * (NWAVES + 1);
+  // the fused epilogue (mm_act_kernel.h) also keeps the tile's column scales
+  static constexpr int kCol = (kBytes + 15) / 16 * 16;  // BN floats
+  static constexpr int kActBytes = kCol + 4 * BN;
 };
+
+// The fused epilogue of fp8_mm_act (mm_act_kernel.h).
+template <int BM, int BN, int WAVES_M, int WAVES_N, int DEEP, int OUT, int TI, int TJ, class P>
+__device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uint8_t* pool, const int64_t m0,
+                                             const int64_t n0);
 
 // One BM x BN output tile at (m0, n0) of batch bz, with `pool` the
 // workgroup's TileLds bytes.
-template <int FA, int FB, int BM, int BN, int WAVES_M, int WAVES_N, int OUT, int LAY, bool PREC, int DEEP>
-__device__ __forceinline__ void mm_tile(const MmArgs& p, const int64_t m0, const int64_t n0, const int64_t bz,
+template <int FA, int FB, int BM, int BN, int WAVES_M, int WAVES_N, int OUT, int LAY, bool PREC, int DEEP, class P>
+__device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int64_t n0, const int64_t bz,
                                         uint8_t* pool) {
   constexpr bool KMA = (LAY & 1) != 0, KMB = (LAY & 2) != 0;
   constexpr int NWAVES = WAVES_M * WAVES_N;
@@ -344,7 +352,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, const int64_t m0, const
   float* const bias_s = reinterpret_cast<float*>(pool + Lds::kBias);
   const bool bias_col = p.bias != nullptr && tid < BN && n0 + tid < p.N;
   const uint32_t bias_bits = bias_col ? load_bias_bits(p, n0 + tid) : 0u;
+  float col_scale = 1.0f;  // fused epilogue: column n0 + t's dequantisation multiplier
+  if constexpr (P::kAct) {
+    if (p.b_scale_inv && tid < BN) col_scale = p.b_scale_inv[p.b_rows ? (n0 + tid < p.N ? n0 + tid : n0) : 0];
+  }
   auto park_bias = [&]() {
+    if constexpr (P::kAct) {
+      if (tid < BN) reinterpret_cast<float*>(pool + Lds::kCol)[tid] = col_scale;
+    }
     if (tid < BN) bias_s[tid] = bias_col ? decode_bias(p, bias_bits, p.bias_scale ? *p.bias_scale : 1.0f) : 0.0f;
   };
 
@@ -553,6 +568,10 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, const int64_t m0, const
   __syncthreads();
   }
 
+  if constexpr (P::kAct) {
+    act_epilogue<BM, BN, WAVES_M, WAVES_N, DEEP, OUT>(p, acc, pool, m0, n0);
+    return;
+  } else {
   // Epilogue: y = acc * fl32(sa * sb) + bias[j] in fp32, then one bf16
   // rounding (OUT < 0) or the output quantization (OUT = E4M3 / E5M2).
   const float sa = p.a_scale_inv ? *p.a_scale_inv : 1.0f;
@@ -747,13 +766,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& p, const int64_t m0, const
       }
     }
   }
+  }
 }
 
 template <int FA, int FB, int BM, int BN, int WAVES_M, int WAVES_N, int MIN_BLOCKS, int OUT, int LAY, bool PREC,
-          int DEEP = 0>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, MIN_BLOCKS) mm_fp8_dma(MmArgs p, int64_t tiles_m,
+          int DEEP = 0, class P = MmArgs>
+__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, MIN_BLOCKS) mm_fp8_dma(P p, int64_t tiles_m,
                                                                                  int64_t tiles_n, int group_m) {
-  __shared__ __align__(16) uint8_t pool[TileLds<BM, BN, WAVES_M * WAVES_N, DEEP>::kBytes];
+  using Lds = TileLds<BM, BN, WAVES_M * WAVES_N, DEEP>;
+  __shared__ __align__(16) uint8_t pool[P::kAct ? Lds::kActBytes : Lds::kBytes];
   int64_t tm, tn, bz = 0, wg = blockIdx.x;
   if (gridDim.z > 1) batch_tile(wg, bz);
   tile_coords(wg, tiles_m, tiles_n, group_m, tm, tn);
@@ -766,13 +787,14 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, MIN_BLOCKS) mm_fp8_dma
 // the band [n_band, N), which start as CUs come free and take about half a
 // big tile's time.  Both shapes sum every output's K in the same MFMA
 // order, so the result equals the all-256 x 256 launch bit for bit.
-template <int FA, int FB, int OUT, int LAY>
-__global__ void __launch_bounds__(512, 1) mm_fp8_mixed(MmArgs p, int64_t tiles_m, int64_t tiles_n,
+template <int FA, int FB, int OUT, int LAY, class P = MmArgs>
+__global__ void __launch_bounds__(512, 1) mm_fp8_mixed(P p, int64_t tiles_m, int64_t tiles_n,
                                                        int64_t band_tiles_m, int64_t band_tiles_n, int64_t n_band,
                                                        int group_m) {
   using Big = TileLds<256, 256, 8, 0>;
   using Band = TileLds<128, 256, 8, 0>;
-  __shared__ __align__(16) uint8_t pool[Big::kBytes > Band::kBytes ? Big::kBytes : Band::kBytes];
+  static_assert(Big::kBytes >= Band::kBytes && Big::kActBytes >= Band::kActBytes, "the big tile's LDS is the larger");
+  __shared__ __align__(16) uint8_t pool[P::kAct ? Big::kActBytes : Big::kBytes];
   const int64_t nbig = tiles_m * tiles_n;
   int64_t tm, tn;
   if ((int64_t)blockIdx.x < nbig) {

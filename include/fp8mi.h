@@ -394,6 +394,79 @@ FP8MI_API fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows,
 FP8MI_API size_t fp8_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
+ * fp8_mm_act -- fp8_mm of one batch with the whole of a feed-forward linear's
+ * elementwise work in its epilogue: bias, activation (plain or gated) and
+ * residual, in fp32, then one bf16 rounding or the output quantization.
+ *   t(i,j) = fl32(sum_k dec(A(i,k)) dec(B(j,k))) * fl32(sa_i * sb_j) + bias_j
+ *   y(i,j) = f(t(i,j)) + residual(i,j)                       [M, N] outputs, or with
+ *            FP8MI_ACT_GATED f(t(i,2j)) * t(i,2j+1) + residual(i,j)   [M, N / 2]
+ *   f:       FP8MI_ACT_NONE; _RELU max(t, 0); _SILU t / (1 + exp(-t));
+ *            _GELU t / (1 + exp(-2 sqrt(2 / pi) (t + 0.044715 t^3))), the tanh form.
+ *   a, b     device E4M3 codes, A(i,k) = a[i * lda + k], B(j,k) = b[j * ldb + k]
+ *            (NT; gated: rows 2j / 2j + 1 of B are the gate and the value of
+ *            output column j, N even).  Requirements as fp8_mm_ex with an fp8
+ *            output (16-byte alignment, K, lda, ldb multiples of 16, operand
+ *            extents below 2^31 bytes).
+ *   a_scale_inv, b_scale_inv  device fp32, NULL meaning 1.0: one word each, or
+ *            [M] / [N] words where scale_rows has FP8MI_A_ROW_SCALES /
+ *            FP8MI_B_ROW_SCALES (the row multipliers of fp8_rmsnorm; a weight
+ *            quantized per output channel).
+ *   bias     device [N] of bias_dtype FP8MI_F32 / F16 / BF16, or NULL.
+ *   act      FP8MI_ACT_*, optionally | FP8MI_ACT_GATED.
+ *   residual device, [M, outputs] of residual_dtype FP8MI_F32 / F16 / BF16,
+ *            ld_res >= outputs, or NULL.  A bf16 residual may be c itself (same
+ *            pointer and leading dimension).
+ *   z_out    optional device bf16 [M, N], ld_z >= N: t rounded once, for
+ *            fp8_act_grad.
+ *   c_dtype  FP8MI_BF16, or FP8MI_FP8_E4M3 with c_scale / c_ring / c_scale_inv_out /
+ *            c_amax_out as fp8_mm_ex (FP8MI_FP8_E5M2, the gradients' format,
+ *            returns FP8MI_ERR_UNSUPPORTED).  ldc in elements, >= outputs.
+ * M or N 0 writes nothing (an fp8 output still folds amax 0); K == 0 gives
+ * t = bias.  One launch (two with c_scale and c_amax_out).
+ */
+typedef enum {
+  FP8MI_ACT_NONE = 0,
+  FP8MI_ACT_RELU = 1,
+  FP8MI_ACT_GELU = 2,
+  FP8MI_ACT_SILU = 3,
+  FP8MI_ACT_GATED = 16 /* or-ed in */
+} fp8mi_activation;
+#define FP8MI_A_ROW_SCALES 1
+#define FP8MI_B_ROW_SCALES 2
+FP8MI_API fp8mi_status fp8_mm_act(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M, int64_t N,
+                                  int64_t K, const float* a_scale_inv, const float* b_scale_inv, int scale_rows,
+                                  const void* bias, int bias_dtype, int act, const void* residual,
+                                  int residual_dtype, int64_t ld_res, void* z_out, int64_t ld_z, void* c, int c_dtype,
+                                  int64_t ldc, const float* c_scale, uint32_t* c_ring, int32_t c_hist_len,
+                                  float* c_scale_inv_out, float* c_amax_out, void* stream);
+
+/*
+ * fp8_act_grad -- the gradient through fp8_mm_act's activation, quantized for
+ * the backward products, in one pass:
+ *   dz(i,j) = dy(i,j) f'(z(i,j)), or with FP8MI_ACT_GATED
+ *   dz(i,2j) = dy(i,j) f'(z(i,2j)) z(i,2j+1),  dz(i,2j+1) = dy(i,j) f(z(i,2j))
+ *   dy       device, FP8MI_BF16 or FP8MI_F16 (FP8MI_F32 returns
+ *            FP8MI_ERR_UNSUPPORTED), [rows, cols], gated [rows, cols / 2]; ld_dy.
+ *   z        device bf16 [rows, cols]: fp8_mm_act's z_out; ld_z >= cols.
+ *   act      as fp8_mm_act (FP8MI_ACT_NONE without FP8MI_ACT_GATED returns
+ *            FP8MI_ERR_ARG: dz is dy, fp8_quantize_dual takes it).  relu' is 0
+ *            at 0.
+ *   fmt, out_row, out_t, scale / ring, scale_inv_out, amax_out
+ *            as fp8_quantize_dual, quantizing dz [rows, cols] (fp32).
+ *   bias_grad_out  optional device bf16 [cols]: sum_i dz(i,j) (4-row sums in
+ *            fp32, then fp64, in a fixed order; one rounding).  Then workspace
+ *            is needed: fp8_bias_grad_workspace_bytes(rows, cols) bytes, 8-byte
+ *            aligned, caller-owned, no initialisation.
+ * rows or cols 0 writes no codes (a ring folds amax 0, bias gradients are 0).
+ * One launch, a second for the bias gradient, one more with scale and amax_out.
+ */
+FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, int64_t cols, int64_t ld_dy,
+                                    const void* z, int64_t ld_z, int act, int fmt, uint8_t* out_row, int64_t ld_row,
+                                    uint8_t* out_t, int64_t ld_t, const float* scale, uint32_t* ring,
+                                    int32_t hist_len, float* scale_inv_out, float* amax_out, void* bias_grad_out,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fp8_ring_seed -- (re)initialise a ring on the device: history, ticket and
  * scratch set to 0, slot 0, and current scale = the scale a fold of *amax
  * into an empty window would publish (fmt_max / amax, or 1.0 when amax is 0

@@ -107,3 +107,100 @@ def test_binding_checks_norm_arguments():
         fp8mi.fp8_rmsnorm_grad(x, x, w, torch.ones(5))
     with pytest.raises(ValueError, match="dweight"):
         fp8mi.fp8_rmsnorm_grad(x, x, w, torch.ones(4), dweight=torch.ones(8, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=4), ENUM), (dict(act=-1), ENUM), (dict(act=32), ENUM), (dict(rows=4), ENUM), (dict(bdt=3), ENUM),
+    (dict(rdt=3), ENUM), (dict(cdt=0), ENUM), (dict(cdt=4, cs=FAKE), UNSUP),
+    (dict(M=-1), SHAPE), (dict(K=-16), SHAPE), (dict(N=33, act=19, ldc=40, ldz=40), SHAPE), (dict(ldc=31), SHAPE),
+    (dict(lda=48), SHAPE), (dict(ldb=48), SHAPE), (dict(ldr=31), SHAPE), (dict(ldz=31), SHAPE), (dict(ldz=1 << 61), SHAPE),
+    (dict(ldc=1 << 62), SHAPE), (dict(lda=1 << 60), SHAPE),
+    (dict(a=None), NULL), (dict(b=None), NULL), (dict(c=None), NULL), (dict(rows=1, sa=None), NULL),
+    (dict(rows=2, sb=None), NULL),
+    (dict(cs=FAKE), ARG), (dict(cdt=3), ARG), (dict(cdt=3, cs=FAKE, ring=FAKE, h=4), ARG),
+    (dict(cdt=3, ring=FAKE, h=0), SHAPE), (dict(c=FAKE + 1), ARG), (dict(z=FAKE + 1), ARG), (dict(res=FAKE + 1), ARG),
+    (dict(bias=FAKE + 1), ARG), (dict(sa=FAKE + 2), ARG), (dict(sb=FAKE + 2), ARG),
+    (dict(K=40), UNSUP), (dict(lda=72), UNSUP), (dict(a=FAKE + 8), UNSUP), (dict(b=FAKE + 8), UNSUP),
+    (dict(M=1 << 23), UNSUP), (dict(M=1 << 20, lda=4096), UNSUP),
+])
+def test_mm_act_rejects(L, kw, status):
+    a = dict(a=FAKE, lda=64, b=FAKE, ldb=64, M=32, N=32, K=64, sa=FAKE, sb=FAKE, rows=0, bias=FAKE, bdt=2, act=2,
+             res=FAKE, rdt=2, ldr=32, z=FAKE, ldz=32, c=FAKE, cdt=2, ldc=32, cs=None, ring=None, h=0, csi=None, cam=None)
+    a.update(kw)
+    assert L.fp8_mm_act(*a.values(), None) == status
+    assert L.fp8mi_last_error()
+
+
+def test_mm_act_empty_is_noop(L):
+    z = [None, 64, None, 64, 0, 32, 64, None, None, 0, None, 0, 2, None, 0, 0, None, 0, None, 2, 32, None, None, 0, None,
+         None, None]
+    assert L.fp8_mm_act(*z) == OK
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=0), ARG), (dict(act=4), ENUM), (dict(act=-3), ENUM), (dict(dt=0), UNSUP), (dict(dt=5), ENUM),
+    (dict(fmt=2), ENUM), (dict(act=18, cols=9), SHAPE), (dict(rows=-1), SHAPE), (dict(ld=7), SHAPE), (dict(ldz=7), SHAPE),
+    (dict(ldr=7), SHAPE), (dict(ldt=3), SHAPE), (dict(ldz=1 << 62), SHAPE), (dict(dy=None), NULL), (dict(z=None), NULL),
+    (dict(o=None), NULL), (dict(ot=None), NULL), (dict(ws=None), NULL), (dict(wsb=63), ARG), (dict(ws=FAKE + 4), ARG),
+    (dict(db=FAKE + 1), ARG), (dict(s=None), ARG), (dict(ring=FAKE, h=4), ARG), (dict(s=FAKE + 2), ARG),
+    (dict(dy=FAKE + 1), ARG), (dict(z=FAKE + 1), ARG), (dict(am=FAKE + 2), ARG),
+])
+def test_act_grad_rejects(L, kw, status):
+    assert L.fp8_bias_grad_workspace_bytes(4, 8) == 64
+    a = dict(dy=FAKE, dt=2, rows=4, cols=8, ld=8, z=FAKE, ldz=8, act=2, fmt=1, o=FAKE, ldr=8, ot=FAKE, ldt=4, s=FAKE,
+             ring=None, h=0, si=None, am=None, db=FAKE, ws=FAKE, wsb=64)
+    a.update(kw)
+    assert L.fp8_act_grad(*a.values(), None) == status
+    assert L.fp8mi_last_error()
+
+
+def test_binding_checks_mm_act_arguments():
+    a, b = torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(6, 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="device"):
+        fp8mi.fp8_mm_act(a, b)
+    with pytest.raises(ValueError, match="K mismatch"):
+        fp8mi.fp8_mm_act(a, b[:, :8])
+    with pytest.raises(ValueError, match="activation"):
+        fp8mi.fp8_mm_act(a, b, act="tanh")
+    with pytest.raises(ValueError, match="even"):
+        fp8mi.fp8_mm_act(a, b[:5], gated=True)
+    with pytest.raises(ValueError, match="a_scale_inv"):
+        fp8mi.fp8_mm_act(a, b, a_scale_inv=torch.ones(3))
+    with pytest.raises(ValueError, match="b_scale_inv"):
+        fp8mi.fp8_mm_act(a, b, b_scale_inv=torch.ones(6, dtype=torch.float64))
+    with pytest.raises(ValueError, match="bias"):
+        fp8mi.fp8_mm_act(a, b, bias=torch.ones(4))
+    with pytest.raises(ValueError, match="residual"):
+        fp8mi.fp8_mm_act(a, b, gated=True, residual=torch.zeros(4, 6))
+    with pytest.raises(ValueError, match="z_out"):
+        fp8mi.fp8_mm_act(a, b, z_out=torch.zeros(4, 6))
+    with pytest.raises(ValueError, match="E4M3"):
+        fp8mi.fp8_mm_act(a, b, out_fmt=fp8mi.E5M2)
+    with pytest.raises(ValueError, match="out must be bfloat16"):
+        fp8mi.fp8_mm_act(a, b, out=torch.zeros(4, 6))
+    with pytest.raises(ValueError, match="1-byte"):
+        fp8mi.fp8_mm_act(a.float(), b)
+
+
+def test_binding_checks_act_grad_arguments():
+    dy, z = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
+    one = torch.ones(1)
+    with pytest.raises(ValueError, match="device"):
+        fp8mi.fp8_act_grad(dy, z, "gelu", scale=one)
+    with pytest.raises(ValueError, match="does not fit"):
+        fp8mi.fp8_act_grad(dy, z, "gelu", gated=True, scale=one)
+    with pytest.raises(ValueError, match="z must be bfloat16"):
+        fp8mi.fp8_act_grad(dy, z.float(), "gelu", scale=one)
+    with pytest.raises(ValueError, match="out_t"):
+        fp8mi.fp8_act_grad(dy, z, "gelu", scale=one, out_t=torch.zeros(4, 8, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="bias_grad_out"):
+        fp8mi.fp8_act_grad(dy, z, "gelu", scale=one, bias_grad_out=torch.zeros(7, dtype=torch.bfloat16))
+
+
+def test_interleave_gated():
+    g, v = torch.arange(6).reshape(3, 2), torch.arange(10, 16).reshape(3, 2)
+    w = fp8mi.interleave_gated(g, v)
+    assert torch.equal(w[0::2], g) and torch.equal(w[1::2], v)
+    assert torch.equal(fp8mi.interleave_gated(g[:, 0], v[:, 0]), torch.tensor([0, 10, 2, 12, 4, 14]))
+    with pytest.raises(ValueError):
+        fp8mi.interleave_gated(g, v[:2])
