@@ -55,14 +55,14 @@ struct MmArgs {
   int early_loads = 0;                // set by the launch: big tiles issue a K step's loads early
 
   // Bytes of one batch's A (B) from row r on: the last row ends at K.
-  __host__ __device__ int64_t a_extent_from(int64_t r) const { return r < M ? (M - 1 - r) * lda + K : 0; }
-  __host__ __device__ int64_t b_extent_from(int64_t r) const { return r < N ? (N - 1 - r) * ldb + K : 0; }
+  __host__ __device__ __forceinline__ int64_t a_extent_from(int64_t r) const { return r < M ? (M - 1 - r) * lda + K : 0; }
+  __host__ __device__ __forceinline__ int64_t b_extent_from(int64_t r) const { return r < N ? (N - 1 - r) * ldb + K : 0; }
   // K-major operands ([K, ld] arrays of K full rows): bytes from column r of
   // row 0 to the end of row K - 1 including its padding, so the extent ends
   // on a 16-byte chunk boundary (lda % 16 == 0, r % 16 == 0): the raw-buffer
   // range check zeroes a straddling 16-byte access as a whole.
-  __host__ __device__ int64_t a_extent_km(int64_t r) const { return (r < M && K > 0) ? K * lda - r : 0; }
-  __host__ __device__ int64_t b_extent_km(int64_t r) const { return (r < N && K > 0) ? K * ldb - r : 0; }
+  __host__ __device__ __forceinline__ int64_t a_extent_km(int64_t r) const { return (r < M && K > 0) ? K * lda - r : 0; }
+  __host__ __device__ __forceinline__ int64_t b_extent_km(int64_t r) const { return (r < N && K > 0) ? K * ldb - r : 0; }
 };
 
 hipError_t launch_mm(const MmArgs& p, int fmt_a, int fmt_b, hipStream_t st);

@@ -4,8 +4,7 @@
 //
 //   t_ij = acc_ij fl32(sa_i sb_j) + bias_j                 (z_out = bf16(t))
 //   y_ij = act(t_ij) + res_ij, or gated y_ij = act(t_i,2j) t_i,2j+1 + res_ij
-// in fp32 throughout.  A lane holds 4 consecutive columns of a row, so a gated
-// pair is always in one lane.
+// in fp32 throughout.  A gated pair is always in one lane.
 #pragma once
 #include "activation.h"
 #include "mm_fp8_kernel.h"
@@ -13,87 +12,322 @@
 
 namespace fp8mi {
 
-// Rows of a tile staged in LDS (PITCH bytes apart, ROWB bytes each) to global
-// memory at dst, ld bytes apart: 16 bytes per lane and step, whole rows by
-// consecutive lanes; rows_in x cols_in_b bytes of the tile lie inside the
-// matrix, EB bytes per element.
-template <int ROWB, int PITCH, int EB, int NT>
-__device__ __forceinline__ void store_rows(const uint8_t* S, uint8_t* dst, int64_t ld, int rows_in, int cols_in_b,
-                                           int tid) {
-  constexpr int PPR = ROWB / 16;
-  static_assert(ROWB % 16 == 0 && PITCH % 16 == 0, "16-byte pieces");
-  for (int q = tid; q < rows_in * PPR; q += NT) {
-    const int r = q / PPR, c = 16 * (q % PPR);
-    if (c >= cols_in_b) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(S + r * PITCH + c);
-    uint8_t* g = dst + r * ld + c;
-    if (c + 16 <= cols_in_b) {
-      if constexpr (EB == 2) *reinterpret_cast<u32x4_any*>(g) = u32x4_any{v.x, v.y, v.z, v.w};
-      else *reinterpret_cast<u32x4_byte*>(g) = u32x4_byte{v.x, v.y, v.z, v.w};
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The accumulators of one 16-row strip, regrouped so that a lane holds
+// consecutive columns of its row.  Lane l = 16 g + r of an MFMA tile holds
+// columns 4g .. 4g + 3 of row r; tiles are taken in pairs (32 columns), and one
+// v_permlane16_swap per value pair exchanges the odd 16-lane rows of the
+// first tile's register with the even ones of the second's: lane group g ends
+// with columns 8 (g / 2) .. + 7 of tile g & 1.  No LDS and no barrier: each wave
+// reads and writes its own rows, 64 contiguous bytes (of bf16) of a row per
+// four lanes and instruction.  (Staged through LDS with 8-column stores of
+// whole rows, the epilogue held 128 + 128 values live and spilled: 8192 x 6912
+// x 1536 without activation 171 us, regrouped 92 us, the plain GEMM 87 us.)
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+// Columns per lane and pair, pairs per strip (a strip of one tile is taken as
+// it is, 4 columns per lane; the last of three tiles pairs with nothing).
+constexpr int pair_cols(int tj) { return tj == 1 ? 4 : 8; }
+constexpr int strip_pairs(int tj) { return (tj + 1) / 2; }
+template <int TJ> __device__ __forceinline__ void lane_columns(const v4f (&acc)[TJ], int c, float (&t)[pair_cols(TJ)]) {
 #pragma unroll
-      for (int e = 0; e < 16 / EB - 1; ++e) {
-        if (c + (e + 1) * EB > cols_in_b) break;
-        if constexpr (EB == 2) reinterpret_cast<uint16_t*>(g)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-        else g[e] = (uint8_t)(w[e / 4] >> (8 * (e & 3)));
+  for (int r = 0; r < 4; ++r) {
+    if constexpr (TJ == 1) {
+      t[r] = acc[0][r];
+    } else {
+      t[r] = acc[2 * c][r];
+      t[4 + r] = 2 * c + 1 < TJ ? acc[2 * c + 1 < TJ ? 2 * c + 1 : 0][r] : 0.0f;
+      swap16(t[r], t[4 + r]);
+    }
+  }
+}
+template <int TJ> __device__ __forceinline__ int lane_column(int g, int c) {
+  return TJ == 1 ? 4 * g : 32 * c + 16 * (g & 1) + 8 * (g >> 1);
+}
+
+// Brings the residual of a BM-row tile into the L2 while the last K steps run:
+// one dword per 128-byte line, straight to a spare KiB of LDS (no register
+// waits for it).  Called by `waves` waves (w-th of them here) that load nothing
+// else; the resource's base is 4-byte aligned, rows and bytes past `extent` are
+// not fetched.
+template <int BM> __device__ __forceinline__ void warm_res(v4i rsrc, int64_t ld_bytes, int row_bytes, int extent, uint32_t lds,
+                                                           int w, int waves) {
+  const int lane = threadIdx.x & 63;
+  const int lines = (row_bytes + 127) / 128;  // per row, a power of two or less
+  const int lpr = lines <= 1 ? 1 : (lines <= 2 ? 2 : (lines <= 4 ? 4 : 8));
+  const int rpi = 64 / lpr;                   // rows per instruction
+  const int line = lane % lpr;
+  for (int r = w * rpi + lane / lpr; r - lane / lpr < BM; r += waves * rpi) {
+    const int64_t off = (r * ld_bytes + 128 * line) & ~int64_t{3};  // whole dwords
+    const int voff = (line < lines && off < extent) ? (int)off : extent;
+    int saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "buffer_load_dword %2, %3, 0 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc)
+        : "memory");
+  }
+}
+
+// W words to element-aligned memory (EB bytes per element), n of the W * 4 / EB
+// elements; W = 1, 2, 4 or 8.
+template <int W, int EB> __device__ __forceinline__ void store_words(uint8_t* g, const uint32_t (&w)[W], int n) {
+  if (n >= W * 4 / EB) {
+    if constexpr (W >= 4) {
+#pragma unroll
+      for (int c = 0; c < W / 4; ++c) {
+        const u32x4_byte v = {w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
+        reinterpret_cast<u32x4_byte*>(g)[c] = v;
       }
+    } else if constexpr (W == 2) {
+      *reinterpret_cast<u32x2_byte*>(g) = u32x2_byte{w[0], w[1]};
+    } else {
+      typedef uint32_t u32_byte __attribute__((aligned(1)));
+      *reinterpret_cast<u32_byte*>(g) = w[0];
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < W * 4 / EB - 1; ++e) {
+    if (e < n) {
+      if constexpr (EB == 2) reinterpret_cast<uint16_t*>(g)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+      else g[e] = (uint8_t)(w[e / 4] >> (8 * (e & 3)));
     }
   }
 }
 
-// W consecutive residual values of one row starting at column c, n of them
-// inside the matrix.
-template <int W> __device__ __forceinline__ void load_res(float (&f)[W], const MmActArgs& p, int64_t row, int64_t c, int n) {
-#pragma unroll
-  for (int e = 0; e < W; ++e) f[e] = 0.0f;
-  const int64_t at = row * p.ld_res + c;
+// C consecutive residual values as stored: words 0 .. C - 1 (fp32), or packed
+// in words 0 .. C / 2 - 1; n of them lie inside the matrix.  (A vector, not an
+// array: the two types' stores into one array would be merged through a
+// pointer, which puts it into memory.)
+template <int C> struct ResWords {
+  typedef uint32_t V __attribute__((ext_vector_type(C)));
+  V w;
+};
+template <int C> __device__ __forceinline__ ResWords<C> load_res(const MmActArgs& p, int64_t row, int64_t col, int n) {
+  ResWords<C> o;
+  o.w = 0u;
+  const int64_t at = row * p.ld_res + col;
   if (p.res_dt == kF32) {
-    const float* q = static_cast<const float*>(p.res) + at;
+    const uint32_t* q = static_cast<const uint32_t*>(p.res) + at;
+    if (n >= C) {
+      if constexpr (C >= 4) {
 #pragma unroll
-    for (int e = 0; e < W; ++e)
-      if (e < n) f[e] = q[e];
-    return;
+        for (int c = 0; c < C / 4; ++c) {
+          const u32x4_any v = reinterpret_cast<const u32x4_any*>(q)[c];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.w[4 * c + e] = v[e];
+        }
+      } else {
+        const u32x2_any v = *reinterpret_cast<const u32x2_any*>(q);
+        o.w[0] = v[0];
+        o.w[1] = v[1];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < C - 1; ++e)
+        if (e < n) o.w[e] = q[e];
+    }
+    return o;
   }
-  uint32_t w[W / 2];
   const uint16_t* q = static_cast<const uint16_t*>(p.res) + at;
-  if (n >= W) {
-    if constexpr (W == 4) {
+  if (n >= C) {
+    if constexpr (C == 8) {
+      const u32x4_any v = *reinterpret_cast<const u32x4_any*>(q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.w[e] = v[e];
+    } else if constexpr (C == 4) {
       const u32x2_any v = *reinterpret_cast<const u32x2_any*>(q);
-      w[0] = v[0];
-      w[1] = v[1];
+      o.w[0] = v[0];
+      o.w[1] = v[1];
     } else {
       typedef uint32_t u32_any __attribute__((aligned(2)));
-      w[0] = *reinterpret_cast<const u32_any*>(q);
+      o.w[0] = *reinterpret_cast<const u32_any*>(q);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < W / 2; ++e) w[e] = 0u;
-#pragma unroll
-    for (int e = 0; e < W; ++e)
-      if (e < n) w[e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
+    for (int e = 0; e < C - 1; ++e)
+      if (e < n) o.w[e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
   }
+  return o;
+}
+template <int C> __device__ __forceinline__ void add_res(float (&y)[C], const ResWords<C>& r, int dt) {
+  if (dt == kF32) {
 #pragma unroll
-  for (int e = 0; e < W / 2; ++e) {
-    if (p.res_dt == kBF16) widen2<kBF16>(w[e], f[2 * e], f[2 * e + 1]);
-    else widen2<kF16>(w[e], f[2 * e], f[2 * e + 1]);
+    for (int e = 0; e < C; ++e) y[e] += __uint_as_float(r.w[e]);
+  } else if (dt == kBF16) {
+#pragma unroll
+    for (int e = 0; e < C; e += 2) {
+      float a, b;
+      widen2<kBF16>(r.w[e / 2], a, b);
+      y[e] += a;
+      y[e + 1] += b;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < C; e += 2) {
+      float a, b;
+      widen2<kF16>(r.w[e / 2], a, b);
+      y[e] += a;
+      y[e + 1] += b;
+    }
   }
 }
 
-// y in place of t: acc[..][0 .. W - 1] hold the lane's W output columns.
-template <int ACT, bool GATED, int TI, int TJ> __device__ __forceinline__ void apply_act(v4f (&acc)[TI][TJ]) {
+template <int C> __device__ __forceinline__ void pack_bf16(uint32_t (&w)[C / 2], const float (&f)[C]) {
 #pragma unroll
-  for (int i = 0; i < TI; ++i)
+  for (int e = 0; e < C; e += 2) {
+    const f32x2 v = {f[e], f[e + 1]};
+    w[e / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  }
+}
+
+// Everything of one wave's strips for one activation.  Returns the largest |y|
+// inside the matrix, NaN left out (0 for a bf16 output).
+template <int ACT, int OUT, bool GATED, int TI, int TJ>
+__device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)[TI][TJ], const float* bias_s,
+                                            const float* col_s, int64_t row0, int64_t col0, int rows_in, int cols_in,
+                                            float s_c) {
+  constexpr int G = GATED ? 2 : 1;  // t columns per output column
+  constexpr int C = pair_cols(TJ), CO = C / G, NP = strip_pairs(TJ);
+  // packed words of a lane's outputs per pair; two pairs' narrow outputs are
+  // joined by v_permlane32_swap, so that a lane stores 16 consecutive t columns
+  constexpr int WO = OUT < 0 ? CO / 2 : (CO + 3) / 4, EB = OUT < 0 ? 2 : 1;
+  constexpr bool JOIN = NP == 2 && WO < 4;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+  const auto clip = [](int v, int most) { return v < 0 ? 0 : (v < most ? v : most); };
+  int n[NP];  // the lane's columns inside the matrix
+  int64_t col[NP];
+  float bias[NP][C], cs[NP][C];
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      if constexpr (GATED) {
-        acc[i][j][0] = act_value<ACT>(acc[i][j][0]) * acc[i][j][1];
-        acc[i][j][1] = act_value<ACT>(acc[i][j][2]) * acc[i][j][3];
-      } else {
+  for (int c = 0; c < NP; ++c) {
+    const int at = lane_column<TJ>(g, c);
+    const bool idle = at >= 16 * TJ;  // three tiles: the absent fourth's lanes
+    n[c] = idle ? 0 : clip(cols_in - at, C);
+    col[c] = col0 + at;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = act_value<ACT>(acc[i][j][r]);
+    for (int e = 0; e < C; e += 4) {
+      const float4 b4 = *reinterpret_cast<const float4*>(bias_s + (idle ? 0 : at) + e);
+      const float4 c4 = *reinterpret_cast<const float4*>(col_s + (idle ? 0 : at) + e);
+      bias[c][e] = idle ? 0.0f : b4.x;
+      bias[c][e + 1] = idle ? 0.0f : b4.y;
+      bias[c][e + 2] = idle ? 0.0f : b4.z;
+      bias[c][e + 3] = idle ? 0.0f : b4.w;
+      cs[c][e] = c4.x; cs[c][e + 1] = c4.y; cs[c][e + 2] = c4.z; cs[c][e + 3] = c4.w;
+    }
+  }
+  const float sa = p.a_scale_inv && !p.a_rows ? *p.a_scale_inv : 1.0f;
+  const bool sreg = OUT >= 0 && scale_regular(s_c);
+  float amax = 0.0f;
+  // residual of strip i + 1 in flight while strip i is finished
+  ResWords<CO> raw[NP], next[NP];
+  if (p.res) {
+#pragma unroll
+    for (int c = 0; c < NP; ++c) raw[c] = load_res<CO>(p, row0 + r16, col[c] / G, r16 < rows_in ? n[c] / G : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int lr = 16 * i + r16;
+    const bool in = lr < rows_in;
+    const int64_t row = row0 + lr;
+    if (p.res && i + 1 < TI) {
+#pragma unroll
+      for (int c = 0; c < NP; ++c)
+        next[c] = load_res<CO>(p, row + 16, col[c] / G, lr + 16 < rows_in ? n[c] / G : 0);
+    }
+    const float ra = p.a_rows ? p.a_scale_inv[in ? row : row0] : sa;
+    float y[NP][CO];
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+      float t[C];
+      lane_columns<TJ>(acc[i], c, t);
+#pragma unroll
+      for (int e = 0; e < C; ++e) t[e] = fmaf(t[e], ra * cs[c][e], bias[c][e]);
+      if (p.z && in) {
+        uint32_t w[C / 2];
+        pack_bf16<C>(w, t);
+        store_words<C / 2, 2>(reinterpret_cast<uint8_t*>(p.z + row * p.ld_z + col[c]), w, n[c]);
+      }
+#pragma unroll
+      for (int e = 0; e < CO; ++e)
+        y[c][e] = GATED ? act_value<ACT>(t[G * e]) * t[G * e + G - 1] : act_value<ACT>(t[e]);
+      if (p.res) {
+        add_res<CO>(y[c], raw[c], p.res_dt);
+        raw[c] = next[c];
       }
     }
+    uint32_t w[NP][WO];
+    if constexpr (OUT < 0) {
+#pragma unroll
+      for (int c = 0; c < NP; ++c) pack_bf16<CO>(w[c], y[c]);
+    } else {
+      // columns past the edge hold y = 0 (zero weights, no bias, no residual);
+      // rows past it hold the bias's values: left out lane by lane
+      float m = 0.0f;  // a NaN kept: it picks the exact encoder
+#pragma unroll
+      for (int c = 0; c < NP; ++c)
+#pragma unroll
+        for (int e = 0; e < CO; ++e) m = __builtin_elementwise_maximum(m, fabsf(y[c][e]));
+      const bool nan = m != m;
+      if (nan) {
+        m = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+          for (int e = 0; e < CO; ++e)
+            if (e < n[c] / G) m = fmaxf(m, fabsf(y[c][e]));
+      }
+      if (!in) m = 0.0f;
+      amax = fmaxf(amax, m);
+      auto encode = [&](auto enc) {
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+          for (int e = 0; e < CO; e += 4) {
+            const float y2 = CO > 2 ? y[c][(e + 2) % CO] : 0.0f, y3 = CO > 2 ? y[c][(e + 3) % CO] : 0.0f;
+            w[c][e / 4] = enc(y[c][e] * s_c, y[c][e + 1] * s_c, y2 * s_c, y3 * s_c);
+          }
+      };
+      if (!__any(nan) && sreg) {
+        // no clamp where fl32(max |y| |s|), the largest of them, is in range
+        if (!__any(m * fabsf(s_c) > FmtTraits<OUT>::kMax))
+          encode([](float a, float b, float c, float d) { return cvt4_inrange<OUT>(a, b, c, d); });
+        else
+          encode([](float a, float b, float c, float d) { return cvt4<OUT>(a, b, c, d); });
+      } else {
+        encode([](float a, float b, float c, float d) { return enc4_exact<OUT>(a, b, c, d); });
+      }
+    }
+    const int64_t at = row * p.ldc;
+    if constexpr (JOIN) {
+      uint32_t o[2 * WO];
+#pragma unroll
+      for (int k = 0; k < WO; ++k) {
+        swap32(w[0][k], w[1][k]);
+        o[k] = w[0][k];
+        o[WO + k] = w[1][k];
+      }
+      if (in)
+        store_words<2 * WO, EB>(static_cast<uint8_t*>(p.c) + (at + (col0 + 16 * g) / G) * EB, o,
+                                16 * g >= 16 * TJ ? 0 : clip(cols_in - 16 * g, 16) / G);
+    } else if (in) {
+#pragma unroll
+      for (int c = 0; c < NP; ++c)  // two codes alone (gated, one tile a wave) fill half their word
+        store_words<WO, EB>(static_cast<uint8_t*>(p.c) + (at + col[c] / G) * EB, w[c], n[c] / G);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // one strip's registers at a time
+  }
+  return amax;
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int DEEP, int OUT, int TI, int TJ, class P>
@@ -102,141 +336,46 @@ __device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uin
   constexpr bool GATED = P::kGated;
   constexpr int NWAVES = WAVES_M * WAVES_N, NT = 64 * NWAVES;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
-  constexpr int G = GATED ? 2 : 1;     // t columns per output column
-  constexpr int W = 4 / G, BNO = BN / G;  // output columns per lane and MFMA tile / per tile
   using Lds = TileLds<BM, BN, NWAVES, DEEP>;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / WAVES_N, wn = wid % WAVES_N;
-  const int r16 = lane & 15, ng = lane >> 4;
-  const int64_t No = p.N / G, o0 = n0 / G;
-  const int rows_in = p.M - m0 < BM ? (int)(p.M - m0) : BM;  // the tile's part inside the matrices
-  const int cols_in = p.N - n0 < BN ? (int)(p.N - n0) : BN;
-  const int outs_in = cols_in / G;
-  const float* const bias_s = reinterpret_cast<const float*>(pool + Lds::kBias);
-  const float* const col_s = reinterpret_cast<const float*>(pool + Lds::kCol);
-
-  // t, in place
-  const float sa = p.a_scale_inv && !p.a_rows ? *p.a_scale_inv : 1.0f;
-#pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int lm = wm * WM + 16 * i + r16;
-    float ra = sa;
-    if (p.a_rows) ra = p.a_scale_inv[m0 + (lm < rows_in ? lm : 0)];
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const float4 b4 = *reinterpret_cast<const float4*>(&bias_s[wn * WN + 16 * j + 4 * ng]);
-      const float4 c4 = *reinterpret_cast<const float4*>(&col_s[wn * WN + 16 * j + 4 * ng]);
-      acc[i][j][0] = fmaf(acc[i][j][0], ra * c4.x, b4.x);
-      acc[i][j][1] = fmaf(acc[i][j][1], ra * c4.y, b4.y);
-      acc[i][j][2] = fmaf(acc[i][j][2], ra * c4.z, b4.z);
-      acc[i][j][3] = fmaf(acc[i][j][3], ra * c4.w, b4.w);
+  const float* const bias_s = reinterpret_cast<const float*>(pool + Lds::kBias) + wn * WN;
+  const float* const col_s = reinterpret_cast<const float*>(pool + Lds::kCol) + wn * WN;
+  const int64_t row0 = m0 + wm * WM, col0 = n0 + wn * WN;
+  const int64_t rl = p.M - row0, cl = p.N - col0;
+  const int rows_in = rl < WM ? (int)rl : WM, cols_in = cl < WN ? (int)cl : WN;  // negative: none
+  // the scale is read before this workgroup's amax can be folded
+  const float s_c = OUT < 0 ? 1.0f : (p.c_ring ? __uint_as_float(p.c_ring[p.c_H]) : *p.c_scale);
+  float amax = 0.0f;
+  if (rows_in > 0) {
+    switch (p.act) {
+      case kActRelu:
+        amax = act_strips<kActRelu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+        break;
+      case kActGelu:
+        amax = act_strips<kActGelu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+        break;
+      case kActSilu:
+        amax = act_strips<kActSilu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+        break;
+      default:
+        amax = act_strips<kActNone, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+        break;
     }
   }
-  if (p.z) {
-    constexpr int PITCH = 2 * (BN + 8);
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        *reinterpret_cast<uint2*>(pool + (wm * WM + 16 * i + r16) * PITCH + 2 * (wn * WN + 16 * j + 4 * ng)) =
-            bf16x4_rne(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-    __syncthreads();
-    store_rows<2 * BN, PITCH, 2, NT>(pool, reinterpret_cast<uint8_t*>(p.z + m0 * p.ld_z + n0), 2 * p.ld_z, rows_in,
-                                     2 * cols_in, tid);
-    __syncthreads();
-  }
-  switch (p.act) {
-    case kActRelu: apply_act<kActRelu, GATED>(acc); break;
-    case kActGelu: apply_act<kActGelu, GATED>(acc); break;
-    case kActSilu: apply_act<kActSilu, GATED>(acc); break;
-    default:
-      if constexpr (GATED) apply_act<kActNone, true>(acc);
-      break;
-  }
-  if (p.res) {
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int lm = wm * WM + 16 * i + r16;
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int lo = (wn * WN + 16 * j + 4 * ng) / G;
-        float f[W];
-        load_res<W>(f, p, m0 + lm, o0 + lo, lm < rows_in ? outs_in - lo : 0);
-#pragma unroll
-        for (int r = 0; r < W; ++r) acc[i][j][r] += f[r];
-      }
-    }
-  }
-  if constexpr (OUT < 0) {
-    constexpr int PITCH = 2 * (BNO + 8);
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        uint8_t* q = pool + (wm * WM + 16 * i + r16) * PITCH + 2 * ((wn * WN + 16 * j + 4 * ng) / G);
-        const uint2 v = bf16x4_rne(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-        if constexpr (GATED) *reinterpret_cast<uint32_t*>(q) = v.x;
-        else *reinterpret_cast<uint2*>(q) = v;
-      }
-    __syncthreads();
-    uint16_t* C = static_cast<uint16_t*>(p.c) + m0 * p.ldc + o0;
-    store_rows<2 * BNO, PITCH, 2, NT>(pool, reinterpret_cast<uint8_t*>(C), 2 * p.ldc, rows_in, 2 * outs_in, tid);
-    return;
-  } else {
-    // quantized like an fp32 tensor; the workgroup's amax is published before
-    // any code is stored (see mm_tile's quantizing epilogue)
-    constexpr int PITCH = BNO + 16;
-    float* const red = reinterpret_cast<float*>(pool + Lds::kRed);
-    const float s_c = p.c_ring ? __uint_as_float(p.c_ring[p.c_H]) : *p.c_scale;
-    auto tile_max = [&](auto maxop) {
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const bool row_in = wm * WM + 16 * i + r16 < rows_in;
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          const int lo = (wn * WN + 16 * j + 4 * ng) / G;
-#pragma unroll
-          for (int r = 0; r < W; ++r)
-            if (row_in && lo + r < outs_in) m = maxop(m, fabsf(acc[i][j][r]));
-        }
-      }
-      return m;
-    };
-    float amax = tile_max([](float a, float b) { return __builtin_elementwise_maximum(a, b); });
-    const bool fast = !__any(amax != amax) && scale_regular(s_c);
-    if (!fast) amax = tile_max([](float a, float b) { return fmaxf(a, b); });
-    uint32_t pub = __builtin_nondeterministic_value(0u);  // read by thread 0 only
-    if (p.c_ring) {
+  if constexpr (OUT >= 0) {
+    if (p.c_ring || p.c_amax_out) {
+      float* const red = reinterpret_cast<float*>(pool + Lds::kRed);
       const float bmax = block_max<NT>(amax, red);
-      if (tid == 0) pub = ring_publish(p.c_ring, p.c_H, bmax);
-    }
-    auto encode = [&](auto enc) {
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          const v4f y = acc[i][j];
-          uint8_t* q = pool + (wm * WM + 16 * i + r16) * PITCH + (wn * WN + 16 * j + 4 * ng) / G;
-          if constexpr (GATED) *reinterpret_cast<uint16_t*>(q) = (uint16_t)enc(y[0] * s_c, y[1] * s_c, 0.0f, 0.0f);
-          else *reinterpret_cast<uint32_t*>(q) = enc(y[0] * s_c, y[1] * s_c, y[2] * s_c, y[3] * s_c);
-        }
-    };
-    if (fast) encode([](float a, float b, float c, float d) { return cvt4<OUT>(a, b, c, d); });
-    else encode([](float a, float b, float c, float d) { return enc4_exact<OUT>(a, b, c, d); });
-    __syncthreads();
-    store_rows<BNO, PITCH, 1, NT>(pool, static_cast<uint8_t*>(p.c) + m0 * p.ldc + o0, p.ldc, rows_in, outs_in, tid);
-    if (p.c_ring) {
-      ring_block_finish<OUT>(p.c_ring, p.c_H, pub, s_c, p.c_scale_inv_out, p.c_amax_out,
+      if (p.c_ring) {
+        ring_block_done<OUT>(p.c_ring, p.c_H, bmax, s_c, p.c_scale_inv_out, p.c_amax_out,
                              reinterpret_cast<uint32_t*>(red + NWAVES));
-    } else {
-      if (p.c_amax_out) {
-        const float bmax = block_max<NT>(amax, red);
-        if (tid == 0) publish_max(reinterpret_cast<uint32_t*>(p.c_amax_out), bmax);
+        return;
       }
-      if (tid == 0 && p.c_scale_inv_out && blockIdx.x == 0) *p.c_scale_inv_out = 1.0f / s_c;
+      if (tid == 0) publish_max(reinterpret_cast<uint32_t*>(p.c_amax_out), bmax);
     }
+    if (tid == 0 && p.c_scale_inv_out && blockIdx.x == 0) *p.c_scale_inv_out = 1.0f / s_c;
   }
 }
 
