@@ -5,8 +5,9 @@
 //             (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)))
 //   slope   = p + t p (1 - p) q'(t)
 // exp is the hardware's exp2 of q log2(e), the quotient its reciprocal: each
-// within about 1 ulp, so p is within 2^-24 (|q| + 4) of exact -- far below the
-// bf16 or fp8 rounding that follows.  exp(-q) = inf gives p = 0 and exp(-q) = 0
+// within about 1 ulp, so p is within 2^-24 ((1 - p) (|q| + 2) + 2) of exact,
+// far below the bf16 or fp8 rounding that follows.  Every instruction counts:
+// one more per output value is 1.7 us at 8192 x 6912 outputs.  exp(-q) = inf gives p = 0 and exp(-q) = 0
 // gives p = 1, so large |t| needs no branch.
 #pragma once
 #include "fp8mi_device.h"
@@ -20,12 +21,14 @@ constexpr float kGelu2c = 1.59576912160573071f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
 template <int ACT> __device__ __forceinline__ float act_p(float t) {
-  const float q = ACT == kActGelu ? kGelu2c * fmaf(kGeluA * t, t * t, t) : t;
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * q));
+  // -q(t) log2(e), the constants multiplied out
+  constexpr float a = -kLog2e * kGelu2c, b = -kLog2e * kGelu2c * kGeluA;
+  const float w = ACT == kActGelu ? t * fmaf(t * t, b, a) : -kLog2e * t;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(w));
 }
 
-// relu keeps a NaN.
-__device__ __forceinline__ float relu(float t) { return t > 0.0f || t != t ? t : 0.0f; }
+// Keeps a NaN.
+__device__ __forceinline__ float relu(float t) { return __builtin_elementwise_maximum(t, 0.0f); }
 
 template <int ACT> __device__ __forceinline__ float act_value(float t) {
   if constexpr (ACT == kActNone) return t;

@@ -206,64 +206,98 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
   constexpr bool JOIN = NP == 2 && WO < 4;
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
   const auto clip = [](int v, int most) { return v < 0 ? 0 : (v < most ? v : most); };
+  const float sa = p.a_scale_inv && !p.a_rows ? *p.a_scale_inv : 1.0f;
+  // Three pairs (the 128 x 192 tile): bias and scales are read from LDS strip
+  // by strip and the residual where it is added -- the registers would not
+  // suffice, and there the CU's other workgroup covers the latency.
+  constexpr bool LEAN = NP > 2;
   int n[NP];  // the lane's columns inside the matrix
   int64_t col[NP];
   float bias[NP][C], cs[NP][C];
+  auto load_cols = [&]() {
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+      const int at = lane_column<TJ>(g, c);
+      const bool idle = at >= 16 * TJ;  // three tiles: the absent fourth's lanes
+#pragma unroll
+      for (int e = 0; e < C; e += 4) {
+        const float4 b4 = *reinterpret_cast<const float4*>(bias_s + (idle ? 0 : at) + e);
+        const float4 c4 = *reinterpret_cast<const float4*>(col_s + (idle ? 0 : at) + e);
+        bias[c][e] = idle ? 0.0f : b4.x;
+        bias[c][e + 1] = idle ? 0.0f : b4.y;
+        bias[c][e + 2] = idle ? 0.0f : b4.z;
+        bias[c][e + 3] = idle ? 0.0f : b4.w;
+        // fl32(sa sb); row scales of A are multiplied in strip by strip
+        cs[c][e] = sa * c4.x; cs[c][e + 1] = sa * c4.y; cs[c][e + 2] = sa * c4.z; cs[c][e + 3] = sa * c4.w;
+      }
+    }
+  };
 #pragma unroll
   for (int c = 0; c < NP; ++c) {
     const int at = lane_column<TJ>(g, c);
-    const bool idle = at >= 16 * TJ;  // three tiles: the absent fourth's lanes
-    n[c] = idle ? 0 : clip(cols_in - at, C);
+    n[c] = at >= 16 * TJ ? 0 : clip(cols_in - at, C);
     col[c] = col0 + at;
-#pragma unroll
-    for (int e = 0; e < C; e += 4) {
-      const float4 b4 = *reinterpret_cast<const float4*>(bias_s + (idle ? 0 : at) + e);
-      const float4 c4 = *reinterpret_cast<const float4*>(col_s + (idle ? 0 : at) + e);
-      bias[c][e] = idle ? 0.0f : b4.x;
-      bias[c][e + 1] = idle ? 0.0f : b4.y;
-      bias[c][e + 2] = idle ? 0.0f : b4.z;
-      bias[c][e + 3] = idle ? 0.0f : b4.w;
-      cs[c][e] = c4.x; cs[c][e + 1] = c4.y; cs[c][e + 2] = c4.z; cs[c][e + 3] = c4.w;
-    }
   }
-  const float sa = p.a_scale_inv && !p.a_rows ? *p.a_scale_inv : 1.0f;
+  if constexpr (!LEAN) load_cols();
   const bool sreg = OUT >= 0 && scale_regular(s_c);
   float amax = 0.0f;
   // residual of strip i + 1 in flight while strip i is finished
-  ResWords<CO> raw[NP], next[NP];
-  if (p.res) {
+  ResWords<CO> raw[LEAN ? 1 : NP], next[LEAN ? 1 : NP];
+  if (!LEAN && p.res) {
 #pragma unroll
-    for (int c = 0; c < NP; ++c) raw[c] = load_res<CO>(p, row0 + r16, col[c] / G, r16 < rows_in ? n[c] / G : 0);
+    for (int c = 0; c < (LEAN ? 0 : NP); ++c)
+      raw[c] = load_res<CO>(p, row0 + r16, col[c] / G, r16 < rows_in ? n[c] / G : 0);
   }
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int lr = 16 * i + r16;
     const bool in = lr < rows_in;
     const int64_t row = row0 + lr;
-    if (p.res && i + 1 < TI) {
+    if (!LEAN && p.res && i + 1 < TI) {
 #pragma unroll
-      for (int c = 0; c < NP; ++c)
+      for (int c = 0; c < (LEAN ? 0 : NP); ++c)
         next[c] = load_res<CO>(p, row + 16, col[c] / G, lr + 16 < rows_in ? n[c] / G : 0);
     }
-    const float ra = p.a_rows ? p.a_scale_inv[in ? row : row0] : sa;
-    float y[NP][CO];
+    const float ra = p.a_rows ? p.a_scale_inv[in ? row : row0] : 1.0f;
+    // step by step over the whole strip: few, long basic blocks, so that the
+    // chains of exp2 and reciprocal of different values overlap
+    float t[NP][C], y[NP][CO];
+    if constexpr (LEAN) load_cols();
 #pragma unroll
-    for (int c = 0; c < NP; ++c) {
-      float t[C];
-      lane_columns<TJ>(acc[i], c, t);
+    for (int c = 0; c < NP; ++c) lane_columns<TJ>(acc[i], c, t[c]);
+    if (p.a_rows) {
 #pragma unroll
-      for (int e = 0; e < C; ++e) t[e] = fmaf(t[e], ra * cs[c][e], bias[c][e]);
-      if (p.z && in) {
+      for (int c = 0; c < NP; ++c)
+#pragma unroll
+        for (int e = 0; e < C; ++e) t[c][e] = fmaf(t[c][e], ra * cs[c][e], bias[c][e]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NP; ++c)
+#pragma unroll
+        for (int e = 0; e < C; ++e) t[c][e] = fmaf(t[c][e], cs[c][e], bias[c][e]);
+    }
+    if (p.z && in) {
+#pragma unroll
+      for (int c = 0; c < NP; ++c) {
         uint32_t w[C / 2];
-        pack_bf16<C>(w, t);
+        pack_bf16<C>(w, t[c]);
         store_words<C / 2, 2>(reinterpret_cast<uint8_t*>(p.z + row * p.ld_z + col[c]), w, n[c]);
       }
+    }
+#pragma unroll
+    for (int c = 0; c < NP; ++c)
 #pragma unroll
       for (int e = 0; e < CO; ++e)
-        y[c][e] = GATED ? act_value<ACT>(t[G * e]) * t[G * e + G - 1] : act_value<ACT>(t[e]);
-      if (p.res) {
-        add_res<CO>(y[c], raw[c], p.res_dt);
-        raw[c] = next[c];
+        y[c][e] = GATED ? act_value<ACT>(t[c][G * e]) * t[c][G * e + G - 1] : act_value<ACT>(t[c][e]);
+    if (p.res) {
+#pragma unroll
+      for (int c = 0; c < NP; ++c) {
+        if constexpr (LEAN) {
+          add_res<CO>(y[c], load_res<CO>(p, row, col[c] / G, in ? n[c] / G : 0), p.res_dt);
+        } else {
+          add_res<CO>(y[c], raw[c], p.res_dt);
+          raw[c] = next[c];
+        }
       }
     }
     uint32_t w[NP][WO];
@@ -340,8 +374,8 @@ __device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uin
   const int tid = threadIdx.x;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / WAVES_N, wn = wid % WAVES_N;
-  const float* const bias_s = reinterpret_cast<const float*>(pool + Lds::kBias) + wn * WN;
-  const float* const col_s = reinterpret_cast<const float*>(pool + Lds::kCol) + wn * WN;
+  const float* const bias_s = reinterpret_cast<const float*>(pool + Lds::kActBias) + wn * WN;
+  const float* const col_s = reinterpret_cast<const float*>(pool + Lds::kActCol) + wn * WN;
   const int64_t row0 = m0 + wm * WM, col0 = n0 + wn * WN;
   const int64_t rl = p.M - row0, cl = p.N - col0;
   const int rows_in = rl < WM ? (int)rl : WM, cols_in = cl < WN ? (int)cl : WN;  // negative: none
@@ -366,7 +400,7 @@ __device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uin
   }
   if constexpr (OUT >= 0) {
     if (p.c_ring || p.c_amax_out) {
-      float* const red = reinterpret_cast<float*>(pool + Lds::kRed);
+      float* const red = reinterpret_cast<float*>(pool + Lds::kActRed);
       const float bmax = block_max<NT>(amax, red);
       if (p.c_ring) {
         ring_block_done<OUT>(p.c_ring, p.c_H, bmax, s_c, p.c_scale_inv_out, p.c_amax_out,
@@ -390,16 +424,43 @@ static hipError_t launch_act_tile(const P& p0, hipStream_t st) {
   P p = p0;
   p.early_loads = tiles_m * tiles_n > (int64_t)device_cu_count();  // more than one round
   hipLaunchKernelGGL((mm_fp8_dma<kE4M3, kE4M3, BM, BN, WM_, WN_, MINB, OUT, 0, PREC, DEEP, P>),
-                     dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WM_ * WN_), 0, st, p, tiles_m, tiles_n, 4);
+                     dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WM_ * WN_), 0, st, p, tiles_m, tiles_n, BM == 128 ? 8 : 4);
   return hipGetLastError();
 }
 
-// The tile rule of the plain GEMM (pick_tile): the K loop dominates both.
+// The plain GEMM's tile (pick_tile), or 4: 128 x 192 tiles of four waves, two
+// workgroups per CU, so that one's epilogue passes under the other's K loop.
+// Costs are in 1/256 of a round of 256 x 256 tiles: a round of 256 x 192 takes
+// 230, one of two 128 x 192 tiles per CU 202 (a last round at most half full
+// 0.6 of it, its workgroups having a CU each), 15% more where K is long and
+// the smaller tile's L2 traffic counts.  The mixed grid's band costs 150 in
+// place of a last round, but not with plain fp8 outputs, where it measured
+// slower than its count.  Both sides measured (us, others -> this tile):
+// 8192 x 6912 x 1536 gelu to fp8 117 -> 100, with pre-activations 122 -> 108;
+// 6144 x 6144 x 1536 gelu 75 -> 70, to fp8 88 -> 68; 2048 x 10240 x 1024 gated
+// to fp8 35 -> 33; and where the rule keeps the others: 8192 x 6912 x 1536
+// without activation 94 against 97, 4096^3 52 against 69, 8192 x 1536 x 6912
+// 72 against 74, 8192^3 392 against 473.
+static inline int pick_act_tile(const MmActArgs& p, bool plain_q8, int ncu) {
+  static const int forced = env_int_in("FP8MI_MM_TILE", 0, 8, -1);
+  if (forced >= 0) return forced;
+  const int base = pick_tile(p, ncu);
+  if (base != 0 && base != 3 && base != 7) return base;
+  const int64_t tm = (p.M + 255) / 256;
+  const int64_t r256 = (tm * ((p.N + 255) / 256) + ncu - 1) / ncu, r192 = (tm * ((p.N + 191) / 192) + ncu - 1) / ncu;
+  const int64_t cost = base == 3 ? r192 * 230 : (base == 7 && !plain_q8 ? (r256 - 1) * 256 + 150 : r256 * 256);
+  const int64_t t = ((p.M + 127) / 128) * ((p.N + 191) / 192), full = t / (2 * ncu), rest = t % (2 * ncu);
+  int64_t own = full * 202 + (rest == 0 ? 0 : (rest <= ncu ? 121 : 202));
+  if (p.K > 2048) own += own * 15 / 100;
+  return own < cost ? 4 : base;
+}
+
 template <int OUT, bool GATED> static hipError_t launch_act_family(const MmActArgs& args, hipStream_t st) {
   using P = MmActTyped<GATED>;
   P p;
   static_cast<MmActArgs&>(p) = args;
-  const int tile = pick_tile(p, device_cu_count());
+  const int tile = mm_precise(p) ? pick_tile(p, device_cu_count())
+                                 : pick_act_tile(p, OUT >= 0 && !GATED, device_cu_count());
   if (mm_precise(p)) {
     switch (tile) {
       case 5: return launch_act_tile<64, 64, 1, 4, 2, OUT, P, true>(p, st);
@@ -411,6 +472,7 @@ template <int OUT, bool GATED> static hipError_t launch_act_family(const MmActAr
     case 0: return launch_act_tile<256, 256, 2, 4, 1, OUT, P>(p, st);
     case 3: return launch_act_tile<256, 192, 2, 4, 1, OUT, P>(p, st);
     case 1: return launch_act_tile<128, 128, 2, 2, 2, OUT, P>(p, st);
+    case 4: return launch_act_tile<128, 192, 2, 2, 2, OUT, P>(p, st);
     case 5: return launch_act_tile<64, 64, 1, 4, 2, OUT, P>(p, st);
     case 6: return launch_act_tile<64, 64, 1, 4, 1, OUT, P, false, 8>(p, st);
     case 8: return launch_act_tile<64, 32, 4, 1, 1, OUT, P, false, 8>(p, st);

@@ -280,11 +280,16 @@ template <int BM, int BN, int NWAVES, int DEEP> struct TileLds {
   static constexpr int kBias = kSmem;           // BN floats
   static constexpr int kRed = kBias + 4 * BN;   // NWAVES + 1 words
   static constexpr int kBytes = kRed + 4 * (NWAVES + 1);
-  // the fused epilogue (mm_act_kernel.h) also keeps the tile's column scales
-  static constexpr int kCol = (kBytes + 15) / 16 * 16;  // BN floats
-  // ... and a KiB that takes what is read ahead only to be in the L2
-  static constexpr int kSpare = kCol + 4 * BN;
-  static constexpr int kActBytes = kSpare + 1024;
+  // The fused epilogue (mm_act_kernel.h) also keeps the tile's column scales,
+  // and a KiB that takes what is read ahead only to be in the L2.  The 128 x
+  // 192 tile, whose stages are half a CU's LDS, keeps all this in a stage that
+  // the K loop has left.
+  static constexpr bool kActInStage = BM * BN == 128 * 192;
+  static constexpr int kActBias = kActInStage ? 0 : kBias;
+  static constexpr int kActRed = kActInStage ? 8 * BN : kRed;
+  static constexpr int kActCol = kActInStage ? 4 * BN : (kBytes + 15) / 16 * 16;  // BN floats
+  static constexpr int kSpare = kActCol + 4 * BN;
+  static constexpr int kActBytes = kActInStage ? kStages * kStage : kSpare + 1024;
 };
 
 // The fused epilogue of fp8_mm_act (mm_act_kernel.h).
@@ -354,7 +359,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   // latency showed once per tile, and once per element for 16- and 8-bit
   // biases: +4.5 µs (fp32) and +8.5 µs (bf16) at 8192 x 6912 x 1536.)
   static_assert(BN <= 64 * NWAVES, "one bias column per thread");
-  float* const bias_s = reinterpret_cast<float*>(pool + Lds::kBias);
+  float* const bias_s = reinterpret_cast<float*>(pool + (P::kAct ? Lds::kActBias : Lds::kBias));
   const bool bias_col = p.bias != nullptr && tid < BN && n0 + tid < p.N;
   const uint32_t bias_bits = bias_col ? load_bias_bits(p, n0 + tid) : 0u;
   float col_scale = 1.0f;  // fused epilogue: column n0 + t's dequantisation multiplier
@@ -363,7 +368,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   }
   auto park_bias = [&]() {
     if constexpr (P::kAct) {
-      if (tid < BN) reinterpret_cast<float*>(pool + Lds::kCol)[tid] = col_scale;
+      if (tid < BN) reinterpret_cast<float*>(pool + Lds::kActCol)[tid] = col_scale;
     }
     if (tid < BN) bias_s[tid] = bias_col ? decode_bias(p, bias_bits, p.bias_scale ? *p.bias_scale : 1.0f) : 0.0f;
   };
@@ -552,6 +557,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     // epilogue overwrites: wait for the idle-stage reads of the last step too
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if constexpr (kWarm) wait_vmem();  // LDS writes of the read-ahead end before the workgroup can
+    if constexpr (P::kAct && Lds::kActInStage) __syncthreads();  // every wave's last reads of the stages are over
     park_bias();
     __syncthreads();
   } else {
