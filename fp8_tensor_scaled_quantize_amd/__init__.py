@@ -515,26 +515,46 @@ def fp8_ring_seed(ring: torch.Tensor, amax: torch.Tensor, fmt) -> None:
     _check(lib().fp8_ring_seed(rp, h, _ptr(amax), _fmt(fmt), _stream(ring)))
 
 
+# A serving step calls the operators below once per token, when the host's
+# share of a call is longer than the kernel: their checks read each tensor's
+# shape and strides once and call as little as they can.
+
 def _rows2d(t: torch.Tensor, name: str):
-    """(rows, cols, leading dimension) of a 2-D tensor with unit column stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """(shape, rows, cols, leading dimension) of a 2-D tensor with unit column
+    stride."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    rows, cols = t.shape
-    return rows, cols, t.stride(0) if rows > 1 else cols
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return shape, rows, cols, ld if rows > 1 else cols
 
 
-def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
-    """Leading dimension of a matrix of x's shape and dtype."""
-    if t.dtype != x.dtype:
-        raise ValueError(f"{name} must be {x.dtype}, got {t.dtype}")
-    _matrix_out(t, x.shape, name)
-    return t.stride(0) if x.shape[0] > 1 else x.shape[1]
+def _ld(t: torch.Tensor, shape, dtype, name: str) -> int:
+    """Leading dimension of a matrix of exactly this shape and dtype."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {str(dtype)[6:]}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} needs unit stride along its rows")
+    return ld if shape[0] > 1 else shape[1]
 
 
-def _f32_vector(t: torch.Tensor, n: int, name: str) -> None:
-    if t.dtype != torch.float32:
-        raise ValueError(f"{name} must be float32, got {t.dtype}")
-    _vector(t, n, name)
+def _typed_vector(t: torch.Tensor, n: int, name: str, dtypes=_DT) -> int:
+    """Type code of a contiguous 1-D tensor of n elements."""
+    dt = dtypes.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be " + " or ".join(str(d)[6:] for d in dtypes) + f", got {t.dtype}")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous 1-D tensor of {n} elements, got {tuple(t.shape)}")
+    return dt
+
+
+_F32_ONLY, _BF16_ONLY = {torch.float32: F32}, {torch.bfloat16: BF16}
 
 
 def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, fmt=E4M3, eps: float = 1e-6,
@@ -548,38 +568,42 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, fmt=E4M3, eps: flo
     then scale_inv_out [rows] receives the rows' dequantisation multipliers.
     sum_out receives x + residual (it may be residual or x itself: in place),
     rstd_out [rows] the 1 / rms values that fp8_rmsnorm_grad reads."""
-    rows, cols, ld_x = _rows2d(x, "x")
+    shape, rows, cols, ld_x = _rows2d(x, "x")
+    dtype = x.dtype
     dt = _dt(x, "x")
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    out = _as_codes(out, "out")
-    _matrix_out(out, x.shape, "out")
-    wdt = 0
-    if weight is not None:
-        wdt = _dt(weight, "weight")
-        _vector(weight, cols, "weight")
-    ld_res = 0 if residual is None else _like(residual, x, "residual")
-    ld_sum = 0 if sum_out is None else _like(sum_out, x, "sum_out")
+        out = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    elif out.dtype is not torch.uint8:
+        out = _as_codes(out, "out")
+    ld_out = _ld(out, shape, torch.uint8, "out")
+    wdt = 0 if weight is None else _typed_vector(weight, cols, "weight")
+    ld_res = 0 if residual is None else _ld(residual, shape, dtype, "residual")
+    ld_sum = 0 if sum_out is None else _ld(sum_out, shape, dtype, "sum_out")
     if row_scaled:
         if scale is not None or ring is not None:
             raise ValueError("row_scaled measures its scales: give neither scale nor ring")
         if scale_inv_out is None:
             raise ValueError("row_scaled needs scale_inv_out [rows]")
-        _f32_vector(scale_inv_out, rows, "scale_inv_out")
+        _typed_vector(scale_inv_out, rows, "scale_inv_out", _F32_ONLY)
         if amax_out is not None:
-            _f32_vector(amax_out, rows, "amax_out")
+            _typed_vector(amax_out, rows, "amax_out", _F32_ONLY)
     else:
         _scalar(scale, "scale")
         _scalar(scale_inv_out, "scale_inv_out")
         _scalar(amax_out, "amax_out")
     if rstd_out is not None:
-        _f32_vector(rstd_out, rows, "rstd_out")
-    rp, h = _ring_args(ring)
+        _typed_vector(rstd_out, rows, "rstd_out", _F32_ONLY)
+    rp, h = (None, 0) if ring is None else _ring_args(ring)
     _on_device(x, weight, residual, out, scale, ring, scale_inv_out, amax_out, sum_out, rstd_out)
-    _check(lib().fp8_rmsnorm(x.data_ptr(), dt, rows, cols, ld_x, _ptr(residual), ld_res, _ptr(weight), wdt,
-                             ctypes.byref(ctypes.c_float(eps)), _fmt(fmt), out.data_ptr(),
-                             out.stride(0) if rows > 1 else cols, 1 if row_scaled else 0, _ptr(scale), rp, h,
-                             _ptr(scale_inv_out), _ptr(amax_out), _ptr(sum_out), ld_sum, _ptr(rstd_out), _stream(x)))
+    status = lib().fp8_rmsnorm(
+        x.data_ptr(), dt, rows, cols, ld_x, None if residual is None else residual.data_ptr(), ld_res,
+        None if weight is None else weight.data_ptr(), wdt, ctypes.byref(ctypes.c_float(eps)), _fmt(fmt),
+        out.data_ptr(), ld_out, 1 if row_scaled else 0, None if scale is None else scale.data_ptr(), rp, h,
+        None if scale_inv_out is None else scale_inv_out.data_ptr(), None if amax_out is None else amax_out.data_ptr(),
+        None if sum_out is None else sum_out.data_ptr(), ld_sum, None if rstd_out is None else rstd_out.data_ptr(),
+        _stream(x))
+    if status:
+        _check(status)
     return out
 
 
@@ -596,31 +620,33 @@ def fp8_rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | N
     None).  h and rstd are the forward call's sum_out (or x) and rstd_out, dsum
     the gradient that reaches h by the residual path (added into dx; dx may be
     dsum or dy itself)."""
-    rows, cols, ld_dy = _rows2d(dy, "dy")
+    shape, rows, cols, ld_dy = _rows2d(dy, "dy")
+    dtype = dy.dtype
     dt = _dt(dy, "dy")
-    ld_h = _like(h, dy, "h")
-    wdt = 0
-    if weight is not None:
-        wdt = _dt(weight, "weight")
-        _vector(weight, cols, "weight")
-    _f32_vector(rstd, rows, "rstd")
-    ld_ds = 0 if dsum is None else _like(dsum, dy, "dsum")
+    ld_h = _ld(h, shape, dtype, "h")
+    wdt = 0 if weight is None else _typed_vector(weight, cols, "weight")
+    _typed_vector(rstd, rows, "rstd", _F32_ONLY)
+    ld_ds = 0 if dsum is None else _ld(dsum, shape, dtype, "dsum")
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
-    ld_dx = _like(dx, dy, "dx")
+        dx = torch.empty(shape, dtype=dtype, device=dy.device)
+    ld_dx = _ld(dx, shape, dtype, "dx")
     nbytes = 0
     if need_dweight or dweight is not None:
         if dweight is None:
             dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
-        _f32_vector(dweight, cols, "dweight")
+        _typed_vector(dweight, cols, "dweight", _F32_ONLY)
         if workspace is None:
             workspace = torch.empty(max(fp8_rmsnorm_grad_workspace_bytes(rows, cols), 4), dtype=torch.uint8,
                                     device=dy.device)
         nbytes = workspace.numel() * workspace.element_size()
     _on_device(dy, h, weight, rstd, dsum, dx, dweight, workspace)
-    _check(lib().fp8_rmsnorm_grad(dy.data_ptr(), dt, rows, cols, ld_dy, h.data_ptr(), ld_h, _ptr(weight), wdt,
-                                  rstd.data_ptr(), _ptr(dsum), ld_ds, dx.data_ptr(), ld_dx, _ptr(dweight),
-                                  _ptr(workspace), nbytes, _stream(dy)))
+    status = lib().fp8_rmsnorm_grad(
+        dy.data_ptr(), dt, rows, cols, ld_dy, h.data_ptr(), ld_h, None if weight is None else weight.data_ptr(), wdt,
+        rstd.data_ptr(), None if dsum is None else dsum.data_ptr(), ld_ds, dx.data_ptr(), ld_dx,
+        None if dweight is None else dweight.data_ptr(), None if workspace is None else workspace.data_ptr(), nbytes,
+        _stream(dy))
+    if status:
+        _check(status)
     return dx, dweight
 
 
@@ -643,10 +669,11 @@ def _row_scales(t, n: int, name: str) -> int:
     """1 where t holds one multiplier per row, 0 for one per tensor (or none)."""
     if t is None:
         return 0
-    if t.dtype != torch.float32 or t.numel() not in (1, n):
+    k = t.numel()
+    if t.dtype is not torch.float32 or (k != 1 and k != n):
         raise ValueError(f"{name} must be a float32 tensor of 1 or {n} elements")
-    if n > 1 and t.numel() == n:
-        _vector(t, n, name)
+    if k > 1:
+        _typed_vector(t, n, name, _F32_ONLY)
         return 1
     return 0
 
@@ -664,49 +691,50 @@ def fp8_mm_act(a: torch.Tensor, b: torch.Tensor, a_scale_inv: torch.Tensor | Non
     is f(gate) * value + residual, [M, N / 2].  z_out (bf16 [M, N]) receives
     the values before the activation, for fp8_act_grad.  A bf16 residual may be
     `out` itself."""
-    a, b = _as_codes(a, "a"), _as_codes(b, "b")
-    M, K, lda = _rows2d(a, "a")
-    N, Kb, ldb = _rows2d(b, "b")
+    if a.dtype is not torch.uint8:
+        a = _as_codes(a, "a")
+    if b.dtype is not torch.uint8:
+        b = _as_codes(b, "b")
+    _, M, K, lda = _rows2d(a, "a")
+    _, N, Kb, ldb = _rows2d(b, "b")
     if K != Kb:
         raise ValueError(f"K mismatch: {tuple(a.shape)} vs {tuple(b.shape)}")
     code = _act(act, gated)
     if gated and N % 2:
         raise ValueError(f"a gated product needs an even number of rows in b, got {N}")
-    No = N // 2 if gated else N
+    shape = (M, N // 2 if gated else N)
     fp8_out = out_fmt is not None
-    if fp8_out and _fmt(out_fmt) != E4M3:
-        raise ValueError("fp8_mm_act's fp8 output is E4M3")
-    if out is None:
-        out = torch.empty((M, No), dtype=torch.uint8 if fp8_out else torch.bfloat16, device=a.device)
     if fp8_out:
+        if _fmt(out_fmt) != E4M3:
+            raise ValueError("fp8_mm_act's fp8 output is E4M3")
+        for t, name in ((out_scale, "out_scale"), (out_scale_inv, "out_scale_inv"), (out_amax, "out_amax")):
+            if t is not None:
+                _scalar(t, name)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8 if fp8_out else torch.bfloat16, device=a.device)
+    elif fp8_out and out.dtype is not torch.uint8:
         out = _as_codes(out, "out")
-    elif out.dtype != torch.bfloat16:
-        raise ValueError(f"out must be bfloat16, got {out.dtype}")
-    _matrix_out(out, (M, No), "out")
+    ldc = _ld(out, shape, torch.uint8 if fp8_out else torch.bfloat16, "out")
     rows = _row_scales(a_scale_inv, M, "a_scale_inv") | (_row_scales(b_scale_inv, N, "b_scale_inv") << 1)
-    bias_dt = res_dt = 0
-    ld_res = ld_z = 0
-    if bias is not None:
-        bias_dt = _dt(bias, "bias")
-        _vector(bias, N, "bias")
+    bias_dt = 0 if bias is None else _typed_vector(bias, N, "bias")
+    res_dt = ld_res = ld_z = 0
     if residual is not None:
         res_dt = _dt(residual, "residual")
-        _matrix_out(residual, (M, No), "residual")
-        ld_res = residual.stride(0) if M > 1 else No
+        ld_res = _ld(residual, shape, residual.dtype, "residual")
     if z_out is not None:
-        if z_out.dtype != torch.bfloat16:
-            raise ValueError(f"z_out must be bfloat16, got {z_out.dtype}")
-        _matrix_out(z_out, (M, N), "z_out")
-        ld_z = z_out.stride(0) if M > 1 else N
-    if fp8_out:
-        for t, name in ((out_scale, "out_scale"), (out_scale_inv, "out_scale_inv"), (out_amax, "out_amax")):
-            _scalar(t, name)
-    rp, h = _ring_args(out_ring)
+        ld_z = _ld(z_out, (M, N), torch.bfloat16, "z_out")
+    rp, h = (None, 0) if out_ring is None else _ring_args(out_ring)
     _on_device(a, b, a_scale_inv, b_scale_inv, bias, residual, z_out, out, out_scale, out_ring, out_scale_inv, out_amax)
-    _check(lib().fp8_mm_act(a.data_ptr(), lda, b.data_ptr(), ldb, M, N, K, _ptr(a_scale_inv), _ptr(b_scale_inv), rows,
-                            _ptr(bias), bias_dt, code, _ptr(residual), res_dt, ld_res, _ptr(z_out), ld_z,
-                            out.data_ptr(), FP8_E4M3 if fp8_out else BF16, out.stride(0) if M > 1 else No,
-                            _ptr(out_scale), rp, h, _ptr(out_scale_inv), _ptr(out_amax), _stream(a)))
+    status = lib().fp8_mm_act(
+        a.data_ptr(), lda, b.data_ptr(), ldb, M, N, K, None if a_scale_inv is None else a_scale_inv.data_ptr(),
+        None if b_scale_inv is None else b_scale_inv.data_ptr(), rows, None if bias is None else bias.data_ptr(),
+        bias_dt, code, None if residual is None else residual.data_ptr(), res_dt, ld_res,
+        None if z_out is None else z_out.data_ptr(), ld_z, out.data_ptr(), FP8_E4M3 if fp8_out else BF16, ldc,
+        None if out_scale is None else out_scale.data_ptr(), rp, h,
+        None if out_scale_inv is None else out_scale_inv.data_ptr(), None if out_amax is None else out_amax.data_ptr(),
+        _stream(a))
+    if status:
+        _check(status)
     return out
 
 
@@ -719,37 +747,43 @@ def fp8_act_grad(dy: torch.Tensor, z: torch.Tensor, act, gated: bool = False, fm
     """Gradient dz of fp8_mm_act's pre-activations (z, its z_out) from the
     gradient dy of its output, quantized with `scale` or `ring`: returns
     (codes [rows, cols], codes_t [cols, rows], bias gradient bf16 or None)."""
-    drows, dcols, ld_dy = _rows2d(dy, "dy")
-    rows, cols, ld_z = _rows2d(z, "z")
-    if z.dtype != torch.bfloat16:
+    _, drows, dcols, ld_dy = _rows2d(dy, "dy")
+    shape, rows, cols, ld_z = _rows2d(z, "z")
+    if z.dtype is not torch.bfloat16:
         raise ValueError(f"z must be bfloat16, got {z.dtype}")
-    if (drows, dcols * (2 if gated else 1)) != (rows, cols):
+    if drows != rows or dcols * (2 if gated else 1) != cols:
         raise ValueError(f"dy {tuple(dy.shape)} does not fit z {tuple(z.shape)}" + (" (gated)" if gated else ""))
     dt, code, f = _dt(dy, "dy"), _act(act, gated), _fmt(fmt)
     if out_row is None:
-        out_row = torch.empty((rows, cols), dtype=torch.uint8, device=dy.device)
+        out_row = torch.empty(shape, dtype=torch.uint8, device=dy.device)
+    elif out_row.dtype is not torch.uint8:
+        out_row = _as_codes(out_row, "out_row")
     if out_t is None:
         out_t = torch.empty((cols, rows), dtype=torch.uint8, device=dy.device)
-    out_row, out_t = _as_codes(out_row, "out_row"), _as_codes(out_t, "out_t")
-    _matrix_out(out_row, (rows, cols), "out_row")
-    _matrix_out(out_t, (cols, rows), "out_t")
+    elif out_t.dtype is not torch.uint8:
+        out_t = _as_codes(out_t, "out_t")
+    ld_row = _ld(out_row, shape, torch.uint8, "out_row")
+    ld_t = _ld(out_t, (cols, rows), torch.uint8, "out_t")
     for t, name in ((scale, "scale"), (scale_inv_out, "scale_inv_out"), (amax_out, "amax_out")):
-        _scalar(t, name)
+        if t is not None:
+            _scalar(t, name)
     nbytes = 0
     if need_bias_grad or bias_grad_out is not None:
         if bias_grad_out is None:
             bias_grad_out = torch.empty(cols, dtype=torch.bfloat16, device=dy.device)
-        _vector(bias_grad_out, cols, "bias_grad_out")
-        if bias_grad_out.dtype != torch.bfloat16:
-            raise ValueError("bias_grad_out must be bfloat16")
+        _typed_vector(bias_grad_out, cols, "bias_grad_out", _BF16_ONLY)
         if workspace is None:
             workspace = torch.empty(max(fp8_bias_grad_workspace_bytes(rows, cols), 8), dtype=torch.uint8,
                                     device=dy.device)
         nbytes = workspace.numel() * workspace.element_size()
-    rp, h = _ring_args(ring)
+    rp, h = (None, 0) if ring is None else _ring_args(ring)
     _on_device(dy, z, out_row, out_t, scale, ring, scale_inv_out, amax_out, bias_grad_out, workspace)
-    _check(lib().fp8_act_grad(dy.data_ptr(), dt, rows, cols, ld_dy, z.data_ptr(), ld_z, code, f, out_row.data_ptr(),
-                              out_row.stride(0) if rows > 1 else cols, out_t.data_ptr(),
-                              out_t.stride(0) if cols > 1 else rows, _ptr(scale), rp, h, _ptr(scale_inv_out),
-                              _ptr(amax_out), _ptr(bias_grad_out), _ptr(workspace), nbytes, _stream(dy)))
+    status = lib().fp8_act_grad(
+        dy.data_ptr(), dt, rows, cols, ld_dy, z.data_ptr(), ld_z, code, f, out_row.data_ptr(), ld_row,
+        out_t.data_ptr(), ld_t, None if scale is None else scale.data_ptr(), rp, h,
+        None if scale_inv_out is None else scale_inv_out.data_ptr(), None if amax_out is None else amax_out.data_ptr(),
+        None if bias_grad_out is None else bias_grad_out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), nbytes, _stream(dy))
+    if status:
+        _check(status)
     return out_row, out_t, bias_grad_out

@@ -482,11 +482,11 @@ fp8mi_status fp8_rmsnorm(const void* x, int x_dtype, int64_t rows, int64_t cols,
   p.x = x; p.res = residual; p.weight = weight; p.weight_dt = weight_dtype;
   p.rows = rows; p.cols = cols; p.ld_x = ld_x; p.ld_res = ld_res;
   p.eps = *eps; p.n_cols = cols > 0 ? (float)cols : 1.0f;
-  p.out = out; p.ld_out = ld_out;
+  p.out = out; p.ld_out = ld_out; p.fmt = fmt;
   p.row_scaled = scaling == FP8MI_SCALE_ROW; p.scale = scale; p.ring = ring; p.H = hist_len;
   p.scale_inv_out = scale_inv_out; p.amax_out = amax_out;
   p.sum_out = sum_out; p.ld_sum = ld_sum; p.rstd_out = rstd_out;
-  return from_hip(launch_rmsnorm(p, x_dtype, fmt, static_cast<hipStream_t>(stream)), "rmsnorm launch");
+  return from_hip(launch_rmsnorm(p, x_dtype, static_cast<hipStream_t>(stream)), "rmsnorm launch");
 }
 
 fp8mi_status fp8_mm_act(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M, int64_t N, int64_t K,

@@ -18,7 +18,7 @@
 namespace fp8mi {
 
 template <int DT, int FMT, int ACT, bool GATED, bool BG>
-__global__ void __launch_bounds__(kTileThreads) act_grad_kernel(ActGradArgs p, int64_t tiles_c, int64_t ntiles) {
+__global__ void __launch_bounds__(kTileThreads, 6) act_grad_kernel(ActGradArgs p, int64_t tiles_c, int64_t ntiles) {
   __shared__ float red[kTileThreads / 64];
   __shared__ __align__(16) uint32_t lds_t[kTileC * 32];
   __shared__ float bg_part[BG ? kTileR / 4 * kTileC : 1];  // [row group][column], swizzled
@@ -94,7 +94,14 @@ __global__ void __launch_bounds__(kTileThreads) act_grad_kernel(ActGradArgs p, i
   if (p.ring && t == 0) pub = ring_publish(p.ring, p.H, bmax);
 
   uint32_t rw[4][2];
-  if (!nan && scale_regular(s)) {
+  if (!nan && scale_regular(s) && m * fabsf(s) <= FmtTraits<FMT>::kMax) {
+    // no clamp needed: fl32(|dz| |s|) <= fl32(m |s|)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        rw[i][h] = cvt4_inrange<FMT>(d[i][4 * h] * s, d[i][4 * h + 1] * s, d[i][4 * h + 2] * s, d[i][4 * h + 3] * s);
+  } else if (!nan && scale_regular(s)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -129,9 +136,9 @@ __global__ void __launch_bounds__(kTileThreads) act_grad_kernel(ActGradArgs p, i
   __syncthreads();
   if constexpr (BG) {
     if (t < kTileC && c0 + t < p.cols && ntiles > 0) {
-      double v = (double)bg_part[bg_index(0, t)];
-#pragma unroll
-      for (int g = 1; g < kTileR / 4; ++g) v += (double)bg_part[bg_index(g, t)];
+      double v = 0.0;
+#pragma unroll 8
+      for (int g = 0; g < kTileR / 4; ++g) v += (double)bg_part[bg_index(g, t)];
       p.bias_ws[(r0 / kTileR) * p.cols + c0 + t] = v;
     }
   }

@@ -36,8 +36,9 @@ template <int ACT> __device__ __forceinline__ float act_value(float t) {
   else return t * act_p<ACT>(t);
 }
 
-// Value and slope.  Where p is 0 or 1 the slope's second term is 0: without
-// the test, a t whose cube or square overflows would make it inf * 0.
+// Value and slope.  t is clamped to +-L, where p is exactly 0 or 1, so that its
+// cube stays finite (the clamps keep a NaN); a clamped value needs only the
+// lower one.
 template <int ACT> __device__ __forceinline__ void act_value_slope(float t, float& value, float& slope) {
   if constexpr (ACT == kActNone) {
     value = t;
@@ -46,11 +47,15 @@ template <int ACT> __device__ __forceinline__ void act_value_slope(float t, floa
     value = relu(t);
     slope = t > 0.0f ? 1.0f : 0.0f;
   } else {
-    const float p = act_p<ACT>(t);
-    const float dq = ACT == kActGelu ? kGelu2c * fmaf(3.0f * kGeluA * t, t, 1.0f) : 1.0f;
-    const float pq = p * (1.0f - p);
-    value = t * p;
-    slope = pq == 0.0f ? p : fmaf(t * pq, dq, p);
+    constexpr float L = ACT == kActGelu ? 12.0f : 128.0f;
+    const float lo = __builtin_elementwise_maximum(t, -L), tc = __builtin_elementwise_minimum(lo, L);
+    constexpr float a = -kLog2e * kGelu2c, b = -kLog2e * kGelu2c * kGeluA;
+    const float u = tc * tc;
+    const float w = ACT == kActGelu ? tc * fmaf(u, b, a) : -kLog2e * tc;
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(w));
+    const float tq = ACT == kActGelu ? tc * fmaf(u, 3.0f * kGelu2c * kGeluA, kGelu2c) : tc;  // t q'(t)
+    value = lo * p;
+    slope = fmaf(p * (1.0f - p), tq, p);
   }
 }
 

@@ -142,6 +142,7 @@ struct NormArgs {
   float eps = 0.0f, n_cols = 1.0f;  // n_cols: cols as fp32 (1 when there are none)
   uint8_t* out = nullptr;
   int64_t ld_out = 0;
+  int fmt = 0;
   int row_scaled = 0;             // one scale per row, measured; else scale / ring
   const float* scale = nullptr;
   uint32_t* ring = nullptr;
@@ -152,7 +153,7 @@ struct NormArgs {
   int64_t ld_sum = 0;
   float* rstd_out = nullptr;      // [rows], or null
 };
-hipError_t launch_rmsnorm(const NormArgs& p, int dt, int fmt, hipStream_t st);
+hipError_t launch_rmsnorm(const NormArgs& p, int dt, hipStream_t st);
 
 struct NormGradArgs {
   const void* dy = nullptr;
@@ -164,7 +165,11 @@ struct NormGradArgs {
   void* dx = nullptr;
   int64_t rows = 0, cols = 0, ld_dy = 0, ld_h = 0, ld_dsum = 0, ld_dx = 0;
   float n_cols = 1.0f;
-  float* parts = nullptr;         // set by the launch: one fp32 row per workgroup, or null
+  // set by the launch: workgroups that take rows; the weight gradient's
+  // partial rows, one per workgroup, or its own array (few rows), or neither
+  int64_t row_blocks = 0;
+  float* parts = nullptr;
+  float* dw_direct = nullptr;
 };
 int64_t rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_grad(const NormGradArgs& p, int dt, float* dweight, void* workspace, hipStream_t st);

@@ -55,8 +55,44 @@ template <int FMT> __device__ __forceinline__ uint2 encode8(const float (&y)[8],
                     enc4_exact<FMT>(y[4] * s, y[5] * s, y[6] * s, y[7] * s));
 }
 
-// A workgroup of NT threads holds NT / 64 / WPR rows.
-template <int DT, int FMT, int WPR, int NV, int NT>
+// A lane's NV vectors of one row: elements 8 (v 64 WPR + li) .. + 7, n[v] of
+// them inside the row; the others read as zero.
+template <int DT, int NV> struct RowRaw {
+  Raw8<DT> v[NV];
+};
+template <int DT, int WPR, int NV>
+__device__ __forceinline__ void load_row(RowRaw<DT, NV>& r, const void* base, int64_t at, int li, const int (&n)[NV]) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (n[v] == 8) load8(r.v[v], base, at + 8 * (v * 64 * WPR + li));
+    else load8_tail(r.v[v], base, at + 8 * (v * 64 * WPR + li), n[v]);
+  }
+}
+// Weights of the lane's columns: as stored (W32: fp32, else two bytes each).
+template <bool W32, int WPR, int NV>
+__device__ __forceinline__ void load_weight(RowRaw<W32 ? kF32 : kBF16, NV>& r, const void* w, int li, const int (&n)[NV]) {
+  if (w) {
+    load_row<W32 ? kF32 : kBF16, WPR, NV>(r, w, 0, li, n);
+  } else {  // ones (fp32: the launch picks W32)
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < Raw8<W32 ? kF32 : kBF16>::kWords; ++e) r.v[v].w[e] = 0x3F800000u;
+  }
+}
+template <bool W32> __device__ __forceinline__ void widen_weight(const Raw8<W32 ? kF32 : kBF16>& r, int dt, float (&f)[8]) {
+  if constexpr (W32) {
+    widen8(r, f);
+  } else if (dt == kBF16) {
+    widen8(r, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) widen2<kF16>(r.w[e], f[2 * e], f[2 * e + 1]);
+  }
+}
+
+// A workgroup of NT threads holds NT / 64 / WPR rows at a time.
+template <int DT, bool W32, int WPR, int NV, int NT>
 __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs p) {
   constexpr int RPB = NT / 64 / WPR;
   static_assert(RPB >= 1 && (WPR == 1 || RPB == 1), "a row of several waves takes the whole workgroup");
@@ -65,62 +101,69 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs p) {
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int wr = WPR == 1 ? 0 : wid;
   const int li = wr * 64 + lane;
+  int n[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int64_t c = 8 * (int64_t)(v * 64 * WPR + li);
+    n[v] = c >= p.cols ? 0 : (p.cols - c >= 8 ? 8 : (int)(p.cols - c));
+  }
   const float s_t = p.row_scaled ? 1.0f : (p.ring ? __uint_as_float(p.ring[p.H]) : *p.scale);
+  // one pass over the rows: the workgroup's amax is published as soon as it is
+  // known, its atomic's round trip passing under the encoding and the stores
+  const bool early = p.ring && !p.row_scaled && p.rows <= (int64_t)gridDim.x * RPB;
+  uint32_t pub = __builtin_nondeterministic_value(0u);  // read by thread 0 only
+  RowRaw<W32 ? kF32 : kBF16, NV> rw;
   float amax = 0.0f;
   int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += (int64_t)gridDim.x * RPB) {
-    const int64_t row = row0 + (WPR == 1 ? wid : 0);
-    if (row >= p.rows) break;  // one row per wave: no barrier inside the loop
-    Raw8<DT> rx[NV], rr[NV];
-    int n[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = 8 * (int64_t)(v * 64 * WPR + li);
-      n[v] = c >= p.cols ? 0 : (p.cols - c >= 8 ? 8 : (int)(p.cols - c));
-      if (n[v] == 8) load8(rx[v], p.x, row * p.ld_x + c);
-      else load8_tail(rx[v], p.x, row * p.ld_x + c, n[v]);
-      if (p.res) {
-        if (n[v] == 8) load8(rr[v], p.res, row * p.ld_res + c);
-        else load8_tail(rr[v], p.res, row * p.ld_res + c, n[v]);
-      }
-    }
+  int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? wid : 0);
+  // with early every wave takes the loop's first turn, rows or not (a barrier)
+  for (bool first = true; row < p.rows || (early && first); row += (int64_t)gridDim.x * RPB) {
+    const bool have = row < p.rows;
+    RowRaw<DT, NV> rx, rr;
     float f[NV][8];
     float ss = 0.0f;
+    if (have) {
+      load_row<DT, WPR, NV>(rx, p.x, row * p.ld_x, li, n);
+      if (p.res) load_row<DT, WPR, NV>(rr, p.res, row * p.ld_res, li, n);
+      if (first) load_weight<W32, WPR, NV>(rw, p.weight, li, n);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      widen8(rx[v], f[v]);
-      if (p.res) {
-        float r[8];
-        widen8(rr[v], r);
+      for (int v = 0; v < NV; ++v) {
+        widen8(rx.v[v], f[v]);
+        if (p.res) {
+          float r[8];
+          widen8(rr.v[v], r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[v][e] += r[e];
+          for (int e = 0; e < 8; ++e) f[v][e] += r[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
       }
+    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[v][e] = 0.0f;
     }
+    first = false;
     ss = row_sum<WPR>(ss, red[parity][0], wr, lane);
     const float rstd = 1.0f / sqrtf(ss / p.n_cols + p.eps);
     float m = 0.0f;  // max |y| with a NaN kept
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = 8 * (int64_t)(v * 64 * WPR + li);
-      if (p.sum_out && n[v] > 0) {  // h, before it is scaled in place
+      if (p.sum_out && n[v] > 0 && have) {  // h, before it is scaled in place
         Raw8<DT> o;
         narrow8(o, f[v]);
-        store8(p.sum_out, row * p.ld_sum + c, o, n[v]);
+        store8(p.sum_out, row * p.ld_sum + 8 * (v * 64 * WPR + li), o, n[v]);
       }
-      float w[8];
-      if (p.weight) {
-        load8_rt(w, p.weight, p.weight_dt, n[v] > 0 ? c : 0, n[v]);
-      } else {
+      if (have) {
+        float w[8];
+        widen_weight<W32>(rw.v[v], p.weight_dt, w);
+        // elements past the row's end are zeros, NaN only where rstd is inf
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f[v][e] = (f[v][e] * rstd) * w[e];
-        // lanes past the row's end hold zeros, which rstd = inf would make NaN
-        m = __builtin_elementwise_maximum(m, e < n[v] ? fabsf(f[v][e]) : 0.0f);
+        for (int e = 0; e < 8; ++e) {
+          f[v][e] = (f[v][e] * rstd) * w[e];
+          m = __builtin_elementwise_maximum(m, fabsf(f[v][e]));
+        }
       }
     }
     const bool nan = m != m;
@@ -135,7 +178,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs p) {
     float s = s_t;
     if (p.row_scaled) {
       const float rm = row_max<WPR>(m, red[parity][1], wr, lane);
-      s = scale_from_max<FMT>(rm);
+      s = p.fmt == kE4M3 ? scale_from_max<kE4M3>(rm) : scale_from_max<kE5M2>(rm);
       if (li == 0) {
         p.scale_inv_out[row] = 1.0f / s;
         if (p.amax_out) p.amax_out[row] = rm;
@@ -143,104 +186,157 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs p) {
     } else {
       amax = fmaxf(amax, m);
     }
-    if (p.rstd_out && li == 0) p.rstd_out[row] = rstd;
+    if (early) {  // uniform over the workgroup
+      const float bmax = block_max<NT>(amax, blk);
+      if (threadIdx.x == 0) pub = ring_publish(p.ring, p.H, bmax);
+    }
+    if (p.rstd_out && li == 0 && have) p.rstd_out[row] = rstd;
     const bool exact = nan || !scale_regular(s);
+    if (have) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (n[v] > 0) {
-        const uint2 q = encode8<FMT>(f[v], s, exact);
-        store_codes8(p.out + row * p.ld_out + 8 * (int64_t)(v * 64 * WPR + li), q.x, q.y, n[v]);
+      for (int v = 0; v < NV; ++v) {
+        if (n[v] > 0) {
+          const uint2 q = p.fmt == kE4M3 ? encode8<kE4M3>(f[v], s, exact) : encode8<kE5M2>(f[v], s, exact);
+          store_codes8(p.out + row * p.ld_out + 8 * (v * 64 * WPR + li), q.x, q.y, n[v]);
+        }
       }
     }
     parity ^= 1;
   }
   if (p.row_scaled) return;
-  const float bmax = block_max<NT>(amax, blk);
+  uint32_t* const flag = reinterpret_cast<uint32_t*>(blk);
   if (p.ring) {
-    ring_block_done<FMT>(p.ring, p.H, bmax, s_t, p.scale_inv_out, p.amax_out, reinterpret_cast<uint32_t*>(blk));
-  } else if (threadIdx.x == 0) {
-    if (p.amax_out) publish_max(reinterpret_cast<uint32_t*>(p.amax_out), bmax);
-    if (p.scale_inv_out && blockIdx.x == 0) *p.scale_inv_out = 1.0f / s_t;
+    if (!early) {
+      const float bmax = block_max<NT>(amax, blk);
+      if (threadIdx.x == 0) pub = ring_publish(p.ring, p.H, bmax);
+    }
+    if (p.fmt == kE4M3) ring_block_finish<kE4M3>(p.ring, p.H, pub, s_t, p.scale_inv_out, p.amax_out, flag);
+    else ring_block_finish<kE5M2>(p.ring, p.H, pub, s_t, p.scale_inv_out, p.amax_out, flag);
+    return;
+  }
+  if (p.amax_out) {
+    const float bmax = block_max<NT>(amax, blk);
+    if (threadIdx.x == 0) publish_max(reinterpret_cast<uint32_t*>(p.amax_out), bmax);
+  }
+  if (threadIdx.x == 0 && p.scale_inv_out && blockIdx.x == 0) *p.scale_inv_out = 1.0f / s_t;
+}
+
+// Gradient.  A wave (WPR = 1) or the workgroup walks over rows, the next row's
+// loads in flight while one is finished, and keeps the weights and the weight
+// gradient's sums of its columns in registers; each workgroup then writes one
+// fp32 partial row, and rmsnorm_dw adds those in a fixed order.
+// The weight gradient of few rows, straight from dy and h: workgroups past the
+// rows' own take 16 columns each, NT / 16 row lanes per column, so a second
+// launch is saved for a second read (from the L2).
+constexpr int kDirectCols = 16;
+template <int DT, int NT> __device__ __forceinline__ void dw_direct(const NormGradArgs& p, int64_t c0, float* red) {
+  constexpr int RL = NT / kDirectCols, U = 4;
+  const int c = threadIdx.x % kDirectCols, rl = threadIdx.x / kDirectCols;
+  const int64_t col = c0 + c;
+  float s = 0.0f;
+  if (col < p.cols) {
+    for (int64_t r = rl; r < p.rows; r += U * RL) {
+      float d[U], h[U], k[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t q = r + u * RL < p.rows ? r + u * RL : r;
+        d[u] = load1<DT>(p.dy, q * p.ld_dy + col);
+        h[u] = load1<DT>(p.h, q * p.ld_h + col);
+        k[u] = p.rstd[q];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r + u * RL < p.rows) s = fmaf(d[u], h[u] * k[u], s);
+    }
+  }
+  red[threadIdx.x] = s;
+  __syncthreads();
+  if (rl == 0 && col < p.cols) {
+    double v = (double)red[c];
+    for (int i = 1; i < RL; ++i) v += (double)red[i * kDirectCols + c];
+    p.dw_direct[col] = (float)v;
   }
 }
 
-// Gradient.  A wave (WPR = 1) or the workgroup walks over rows and keeps the
-// weight gradient's sums of its columns in registers; each workgroup then
-// writes one fp32 partial row, and rmsnorm_dw adds those in a fixed order.
-template <int DT, int WPR, int NV, int NT>
+template <int DT, bool W32, int WPR, int NV, int NT>
 __global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradArgs p) {
   constexpr int RPB = NT / 64 / WPR;
   static_assert(RPB >= 1 && (WPR == 1 || RPB == 1), "a row of several waves takes the whole workgroup");
   __shared__ float red[2][WPR];
-  __shared__ float part[WPR == 1 ? NV * 512 : 1];
+  __shared__ float part[WPR == 1 && NV * 512 > NT ? NV * 512 : NT];
+  if ((int64_t)blockIdx.x >= p.row_blocks) {
+    dw_direct<DT, NT>(p, ((int64_t)blockIdx.x - p.row_blocks) * kDirectCols, part);
+    return;
+  }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int wr = WPR == 1 ? 0 : wid;
   const int li = wr * 64 + lane;
+  int n[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int64_t c = 8 * (int64_t)(v * 64 * WPR + li);
+    n[v] = c >= p.cols ? 0 : (p.cols - c >= 8 ? 8 : (int)(p.cols - c));
+  }
+  RowRaw<W32 ? kF32 : kBF16, NV> rw;
+  load_weight<W32, WPR, NV>(rw, p.weight, li, n);
   float dw[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[v][e] = 0.0f;
+  const int64_t step = p.row_blocks * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? wid : 0);
+  RowRaw<DT, NV> rd, rh, rs;
+  float rstd = 0.0f;
+  auto load = [&](int64_t r) {
+    rstd = p.rstd[r];
+    load_row<DT, WPR, NV>(rd, p.dy, r * p.ld_dy, li, n);
+    load_row<DT, WPR, NV>(rh, p.h, r * p.ld_h, li, n);
+    if (p.dsum) load_row<DT, WPR, NV>(rs, p.dsum, r * p.ld_dsum, li, n);
+  };
+  // (a row of sixteen waves leaves no registers for the next one)
+  constexpr bool AHEAD = WPR < 16;
+  if (AHEAD && row < p.rows) load(row);
   int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += (int64_t)gridDim.x * RPB) {
-    const int64_t row = row0 + (WPR == 1 ? wid : 0);
-    if (row >= p.rows) break;  // one row per wave: no barrier inside the loop
-    Raw8<DT> rd[NV], rh[NV], rs[NV];
-    int n[NV];
-    const float rstd = p.rstd[row];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = 8 * (int64_t)(v * 64 * WPR + li);
-      n[v] = c >= p.cols ? 0 : (p.cols - c >= 8 ? 8 : (int)(p.cols - c));
-      if (n[v] == 8) {
-        load8(rd[v], p.dy, row * p.ld_dy + c);
-        load8(rh[v], p.h, row * p.ld_h + c);
-        if (p.dsum) load8(rs[v], p.dsum, row * p.ld_dsum + c);
-      } else {
-        load8_tail(rd[v], p.dy, row * p.ld_dy + c, n[v]);
-        load8_tail(rh[v], p.h, row * p.ld_h + c, n[v]);
-        if (p.dsum) load8_tail(rs[v], p.dsum, row * p.ld_dsum + c, n[v]);
-      }
-    }
-    float g[NV][8];
+  for (; row < p.rows; row += step) {
+    if (!AHEAD) load(row);
+    float g[NV][8], o[NV][8];
     float dot = 0.0f;
+    const float rk = rstd;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = 8 * (int64_t)(v * 64 * WPR + li);
-      float h[8], w[8];
-      widen8(rd[v], g[v]);
-      widen8(rh[v], h);
-      if (p.weight) {
-        load8_rt(w, p.weight, p.weight_dt, n[v] > 0 ? c : 0, n[v]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      }
+      float w[8], h[8];
+      widen8(rd.v[v], g[v]);
+      widen8(rh.v[v], h);
+      widen_weight<W32>(rw.v[v], p.weight_dt, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (e < n[v]) dw[v][e] = fmaf(g[v][e], h[e] * rstd, dw[v][e]);
+        dw[v][e] = fmaf(g[v][e], h[e] * rk, dw[v][e]);
         g[v][e] *= w[e];
         dot = fmaf(g[v][e], h[e], dot);
+        o[v][e] = h[e];
       }
     }
     dot = row_sum<WPR>(dot, red[parity], wr, lane);
-    const float k = -(rstd * rstd) * rstd * (dot / p.n_cols);
+    const float k = -(rk * rk) * rk * (dot / p.n_cols);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[v][e] = fmaf(k, o[v][e], rk * g[v][e]);
+      if (p.dsum) {
+        float t[8];
+        widen8(rs.v[v], t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[v][e] += t[e];
+      }
+    }
+    if (AHEAD && row + step < p.rows) load(row + step);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (n[v] == 0) continue;
-      float h[8], o[8];
-      widen8(rh[v], h);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(k, h[e], rstd * g[v][e]);
-      if (p.dsum) {
-        float t[8];
-        widen8(rs[v], t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += t[e];
-      }
       Raw8<DT> q;
-      narrow8(q, o);
-      store8(p.dx, row * p.ld_dx + 8 * (int64_t)(v * 64 * WPR + li), q, n[v]);
+      narrow8(q, o[v]);
+      store8(p.dx, row * p.ld_dx + 8 * (v * 64 * WPR + li), q, n[v]);
     }
     parity ^= 1;
   }
@@ -302,95 +398,111 @@ __global__ void __launch_bounds__(kDwCols * kDwSplit) rmsnorm_dw(const float* pa
 // ---------------------------------------------------------------------------
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int DT, int FMT, int WPR, int NV, int NT>
+template <int DT, bool W32, int WPR, int NV, int NT>
 static void launch_norm_one(const NormArgs& p, int64_t most_blocks, hipStream_t st) {
   constexpr int RPB = NT / 64 / WPR;
   int64_t blocks = cdiv(p.rows, RPB);
   if (blocks > most_blocks) blocks = most_blocks;
   if (blocks < 1) blocks = 1;
-  hipLaunchKernelGGL((rmsnorm_kernel<DT, FMT, WPR, NV, NT>), dim3((unsigned)blocks), dim3(NT), 0, st, p);
+  hipLaunchKernelGGL((rmsnorm_kernel<DT, W32, WPR, NV, NT>), dim3((unsigned)blocks), dim3(NT), 0, st, p);
 }
 
 // Waves per row: one while the rows alone give the chip its waves and a row
 // fits 6 vectors per lane; else four (rows of at most 8192 columns) or
 // sixteen (at most kNormMaxCols).
-template <int DT, int FMT> static hipError_t launch_norm(const NormArgs& p, hipStream_t st) {
+template <int DT, bool W32> static hipError_t launch_norm(const NormArgs& p, hipStream_t st) {
   const int64_t ncu = device_cu_count();
-  const int64_t most = 8 * ncu;
+  // an explicit scale with amax_out: every workgroup's maximum goes to the
+  // caller's one word and these atomics serialise (about 12 ns each), so few
+  // workgroups of several rows (1000 x 1535 fp16: 16 -> 9 us)
+  const bool word = !p.row_scaled && !p.ring && p.amax_out;
+  const int64_t most = word ? ncu : 8 * ncu;
   const int64_t v1 = cdiv(p.cols, 512), v4 = cdiv(p.cols, 2048), v16 = cdiv(p.cols, 8192);
-  if (v1 <= 1 || (v1 <= 6 && p.rows >= 4 * ncu)) {
+  if (v1 <= 1 || (v1 <= 6 && p.rows >= (word ? ncu / 2 : 4 * ncu))) {
     switch (v1) {
       case 0:
-      case 1: launch_norm_one<DT, FMT, 1, 1, 256>(p, most, st); break;
-      case 2: launch_norm_one<DT, FMT, 1, 2, 256>(p, most, st); break;
-      case 3: launch_norm_one<DT, FMT, 1, 3, 256>(p, most, st); break;
-      case 4: launch_norm_one<DT, FMT, 1, 4, 256>(p, most, st); break;
-      default: launch_norm_one<DT, FMT, 1, 6, 256>(p, most, st); break;
+      case 1: launch_norm_one<DT, W32, 1, 1, 256>(p, most, st); break;
+      case 2: launch_norm_one<DT, W32, 1, 2, 256>(p, most, st); break;
+      case 3: launch_norm_one<DT, W32, 1, 3, 256>(p, most, st); break;
+      case 4: launch_norm_one<DT, W32, 1, 4, 256>(p, most, st); break;
+      default: launch_norm_one<DT, W32, 1, 6, 256>(p, most, st); break;
     }
   } else if (v4 <= 4) {
     switch (v4) {
-      case 1: launch_norm_one<DT, FMT, 4, 1, 256>(p, most, st); break;
-      case 2: launch_norm_one<DT, FMT, 4, 2, 256>(p, most, st); break;
-      default: launch_norm_one<DT, FMT, 4, 4, 256>(p, most, st); break;
+      case 1: launch_norm_one<DT, W32, 4, 1, 256>(p, most, st); break;
+      case 2: launch_norm_one<DT, W32, 4, 2, 256>(p, most, st); break;
+      default: launch_norm_one<DT, W32, 4, 4, 256>(p, most, st); break;
     }
   } else {
-    if (v16 <= 2) launch_norm_one<DT, FMT, 16, 2, 1024>(p, most, st);
-    else launch_norm_one<DT, FMT, 16, 4, 1024>(p, most, st);
+    if (v16 <= 2) launch_norm_one<DT, W32, 16, 2, 1024>(p, most, st);
+    else launch_norm_one<DT, W32, 16, 4, 1024>(p, most, st);
   }
   return hipGetLastError();
 }
 
-template <int DT> static hipError_t launch_norm_dt(const NormArgs& p, int fmt, hipStream_t st) {
-  return fmt == kE4M3 ? launch_norm<DT, kE4M3>(p, st) : launch_norm<DT, kE5M2>(p, st);
-}
+// No weight reads as fp32 ones.
+static bool weight_32(const void* weight, int dt) { return !weight || dt == kF32; }
 
-hipError_t launch_rmsnorm(const NormArgs& p, int dt, int fmt, hipStream_t st) {
+hipError_t launch_rmsnorm(const NormArgs& p, int dt, hipStream_t st) {
   if (p.row_scaled && p.rows == 0) return hipSuccess;
   if (!p.row_scaled && !p.ring && p.amax_out) {
     const hipError_t e = launch_zero_word(p.amax_out, st);
     if (e != hipSuccess) return e;
   }
+  if (weight_32(p.weight, p.weight_dt)) {
+    switch (dt) {
+      case kF32: return launch_norm<kF32, true>(p, st);
+      case kF16: return launch_norm<kF16, true>(p, st);
+      default: return launch_norm<kBF16, true>(p, st);
+    }
+  }
   switch (dt) {
-    case kF32: return launch_norm_dt<kF32>(p, fmt, st);
-    case kF16: return launch_norm_dt<kF16>(p, fmt, st);
-    default: return launch_norm_dt<kBF16>(p, fmt, st);
+    case kF32: return launch_norm<kF32, false>(p, st);
+    case kF16: return launch_norm<kF16, false>(p, st);
+    default: return launch_norm<kBF16, false>(p, st);
   }
 }
 
 // Workgroups of the gradient's main pass (one partial row of the weight's
-// gradient each): one per row (or per 8 rows of one wave each) up to
-// kGradBlocks.
-constexpr int64_t kGradBlocks = 512;
+// gradient each).  One wave per row: 8 rows a workgroup, one workgroup per CU
+// (its registers allow no second).  Four waves: up to four workgroups per CU.
+// Sixteen: one.
+constexpr int64_t kGradBlocks1 = 256, kGradBlocks4 = 1024, kGradBlocks16 = 256;
 static bool grad_one_wave(int64_t rows, int64_t cols) { return cols <= 512 || (cols <= 2048 && rows >= 2048); }
 static int64_t grad_blocks(int64_t rows, int64_t cols) {
-  const int64_t b = grad_one_wave(rows, cols) ? cdiv(rows, 8) : rows;
-  return b > kGradBlocks ? kGradBlocks : b;
+  const bool one = grad_one_wave(rows, cols);
+  const int64_t b = one ? cdiv(rows, 8) : rows;
+  const int64_t most = one ? kGradBlocks1 : (cols <= 8192 ? kGradBlocks4 : kGradBlocks16);
+  return b > most ? most : b;
 }
+// Few rows: the weight gradient comes from the same launch (dw_direct).  A
+// second launch costs about 4.5 us, the second read of 512 rows less.
+constexpr int64_t kDirectRows = 512;
 
 int64_t rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
   return grad_blocks(rows, cols) * cols * (int64_t)sizeof(float);
 }
 
-template <int DT> static void launch_norm_grad(const NormGradArgs& p, unsigned nb, hipStream_t st) {
+template <int DT, bool W32> static void launch_norm_grad(const NormGradArgs& p, unsigned nb, hipStream_t st) {
   const int64_t v1 = cdiv(p.cols, 512), v4 = cdiv(p.cols, 2048), v16 = cdiv(p.cols, 8192);
   const dim3 g(nb);
   if (grad_one_wave(p.rows, p.cols)) {
     switch (v1) {
-      case 1: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 1, 1, 512>), g, dim3(512), 0, st, p); break;
-      case 2: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 1, 2, 512>), g, dim3(512), 0, st, p); break;
-      case 3: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 1, 3, 512>), g, dim3(512), 0, st, p); break;
-      default: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 1, 4, 512>), g, dim3(512), 0, st, p); break;
+      case 1: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 1, 1, 512>), g, dim3(512), 0, st, p); break;
+      case 2: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 1, 2, 512>), g, dim3(512), 0, st, p); break;
+      case 3: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 1, 3, 512>), g, dim3(512), 0, st, p); break;
+      default: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 1, 4, 512>), g, dim3(512), 0, st, p); break;
     }
   } else if (v4 <= 4) {
     switch (v4) {
-      case 1: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 4, 1, 256>), g, dim3(256), 0, st, p); break;
-      case 2: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 4, 2, 256>), g, dim3(256), 0, st, p); break;
-      default: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 4, 4, 256>), g, dim3(256), 0, st, p); break;
+      case 1: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 4, 1, 256>), g, dim3(256), 0, st, p); break;
+      case 2: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 4, 2, 256>), g, dim3(256), 0, st, p); break;
+      default: hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 4, 4, 256>), g, dim3(256), 0, st, p); break;
     }
   } else {
-    if (v16 <= 2) hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 16, 2, 1024>), g, dim3(1024), 0, st, p);
-    else hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, 16, 4, 1024>), g, dim3(1024), 0, st, p);
+    if (v16 <= 2) hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 16, 2, 1024>), g, dim3(1024), 0, st, p);
+    else hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, W32, 16, 4, 1024>), g, dim3(1024), 0, st, p);
   }
 }
 
@@ -398,18 +510,34 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& p0, int dt, float* dweight, v
   if (p0.cols == 0) return hipSuccess;
   const int64_t nb = p0.rows > 0 ? grad_blocks(p0.rows, p0.cols) : 0;
   NormGradArgs p = p0;
-  // one workgroup: its sums are the gradient
-  p.parts = !dweight ? nullptr : (nb == 1 ? dweight : static_cast<float*>(workspace));
-  if (nb > 0) {
+  const bool direct = dweight && nb > 0 && p0.rows <= kDirectRows;
+  p.dw_direct = direct ? dweight : nullptr;
+  p.parts = dweight && !direct ? static_cast<float*>(workspace) : nullptr;
+  const bool w32 = weight_32(p.weight, p.weight_dt);
+  auto launch = [&](int64_t row_blocks, int64_t dw_blocks) {
+    p.row_blocks = row_blocks;
+    const unsigned grid = (unsigned)(row_blocks + dw_blocks);
     switch (dt) {
-      case kF32: launch_norm_grad<kF32>(p, (unsigned)nb, st); break;
-      case kF16: launch_norm_grad<kF16>(p, (unsigned)nb, st); break;
-      default: launch_norm_grad<kBF16>(p, (unsigned)nb, st); break;
+      case kF32: w32 ? launch_norm_grad<kF32, true>(p, grid, st) : launch_norm_grad<kF32, false>(p, grid, st); break;
+      case kF16: w32 ? launch_norm_grad<kF16, true>(p, grid, st) : launch_norm_grad<kF16, false>(p, grid, st); break;
+      default: w32 ? launch_norm_grad<kBF16, true>(p, grid, st) : launch_norm_grad<kBF16, false>(p, grid, st); break;
     }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    return hipGetLastError();
+  };
+  hipError_t e = hipSuccess;
+  if (direct) {
+    const int64_t db = cdiv(p.cols, kDirectCols);
+    if (p.dx == p.dy || p.dx == p.h) {  // the rows' results overwrite what dw_direct reads: one after the other
+      e = launch(0, db);
+      if (e == hipSuccess) e = launch(nb, 0);
+    } else {
+      e = launch(nb, db);
+    }
+  } else if (nb > 0) {
+    e = launch(nb, 0);
   }
-  if (dweight && nb != 1)
+  if (e != hipSuccess) return e;
+  if (dweight && !direct)
     hipLaunchKernelGGL(rmsnorm_dw, dim3((unsigned)cdiv(p.cols, kDwCols)), dim3(kDwCols * kDwSplit), 0, st,
                        static_cast<const float*>(workspace), nb, p.cols, dweight);
   return hipGetLastError();

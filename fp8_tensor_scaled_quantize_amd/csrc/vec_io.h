@@ -108,27 +108,6 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, uint32_t lo, uint32_t h
     if (e < n) p[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
 }
 
-// Eight consecutive values of a vector whose type is known at run time (a
-// norm's weight), elements at or past n read as zero.
-__device__ __forceinline__ void load8_rt(float (&f)[8], const void* base, int dt, int64_t idx, int n) {
-  if (dt == kF32) {
-    Raw8<kF32> r;
-    if (n >= 8) load8(r, base, idx);
-    else load8_tail(r, base, idx, n);
-    widen8(r, f);
-  } else {
-    Raw8<kBF16> r;
-    if (n >= 8) load8(r, base, idx);
-    else load8_tail(r, base, idx, n);
-    if (dt == kBF16) {
-      widen8(r, f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) widen2<kF16>(r.w[e], f[2 * e], f[2 * e + 1]);
-    }
-  }
-}
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);

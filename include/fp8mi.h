@@ -382,7 +382,8 @@ FP8MI_API fp8mi_status fp8_rmsnorm(const void* x, int x_dtype, int64_t rows, int
  *              bytes, 4-byte aligned, caller-owned, no initialisation; not
  *              needed without dweight.  Calls in flight on one workspace race.
  * rows == 0 writes zeros to dweight; cols == 0 is a no-op.  Limits of cols as
- * fp8_rmsnorm.  Two launches (one without dweight).
+ * fp8_rmsnorm.  Two launches (one without dweight, or with at
+ * most 512 rows and dx apart from dy).
  */
 FP8MI_API fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t cols, int64_t ld_dy,
                                         const void* h, int64_t ld_h, const void* weight, int weight_dtype,
