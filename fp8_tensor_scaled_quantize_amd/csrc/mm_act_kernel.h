@@ -364,6 +364,42 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
   return amax;
 }
 
+// One wave's strips, the activation chosen once.
+template <int OUT, bool GATED, int TI, int TJ>
+__device__ __forceinline__ float act_strips_any(const MmActArgs& p, const v4f (&acc)[TI][TJ], const float* bias_s,
+                                                const float* col_s, int64_t row0, int64_t col0, int rows_in,
+                                                int cols_in, float s_c) {
+  switch (p.act) {
+    case kActRelu: return act_strips<kActRelu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+    case kActGelu: return act_strips<kActGelu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+    case kActSilu: return act_strips<kActSilu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+    default: return act_strips<kActNone, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+  }
+}
+
+// The output scale; read before this workgroup's amax can be folded.
+template <int OUT> __device__ __forceinline__ float act_out_scale(const MmActArgs& p) {
+  return OUT < 0 ? 1.0f : (p.c_ring ? __uint_as_float(p.c_ring[p.c_H]) : *p.c_scale);
+}
+
+// A workgroup's share of the output's amax and scale bookkeeping; every thread
+// calls it.  red: NT / 64 + 1 words of LDS.
+template <int OUT, int NT>
+__device__ __forceinline__ void act_finish(const MmActArgs& p, float amax, float s_c, float* red) {
+  if constexpr (OUT >= 0) {
+    if (p.c_ring || p.c_amax_out) {
+      const float bmax = block_max<NT>(amax, red);
+      if (p.c_ring) {
+        ring_block_done<OUT>(p.c_ring, p.c_H, bmax, s_c, p.c_scale_inv_out, p.c_amax_out,
+                             reinterpret_cast<uint32_t*>(red + NT / 64));
+        return;
+      }
+      if (threadIdx.x == 0) publish_max(reinterpret_cast<uint32_t*>(p.c_amax_out), bmax);
+    }
+    if (threadIdx.x == 0 && p.c_scale_inv_out && blockIdx.x == 0) *p.c_scale_inv_out = 1.0f / s_c;
+  }
+}
+
 template <int BM, int BN, int WAVES_M, int WAVES_N, int DEEP, int OUT, int TI, int TJ, class P>
 __device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uint8_t* pool, const int64_t m0,
                                              const int64_t n0) {
@@ -379,38 +415,11 @@ __device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uin
   const int64_t row0 = m0 + wm * WM, col0 = n0 + wn * WN;
   const int64_t rl = p.M - row0, cl = p.N - col0;
   const int rows_in = rl < WM ? (int)rl : WM, cols_in = cl < WN ? (int)cl : WN;  // negative: none
-  // the scale is read before this workgroup's amax can be folded
-  const float s_c = OUT < 0 ? 1.0f : (p.c_ring ? __uint_as_float(p.c_ring[p.c_H]) : *p.c_scale);
+  const float s_c = act_out_scale<OUT>(p);
   float amax = 0.0f;
-  if (rows_in > 0) {
-    switch (p.act) {
-      case kActRelu:
-        amax = act_strips<kActRelu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
-        break;
-      case kActGelu:
-        amax = act_strips<kActGelu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
-        break;
-      case kActSilu:
-        amax = act_strips<kActSilu, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
-        break;
-      default:
-        amax = act_strips<kActNone, OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
-        break;
-    }
-  }
-  if constexpr (OUT >= 0) {
-    if (p.c_ring || p.c_amax_out) {
-      float* const red = reinterpret_cast<float*>(pool + Lds::kActRed);
-      const float bmax = block_max<NT>(amax, red);
-      if (p.c_ring) {
-        ring_block_done<OUT>(p.c_ring, p.c_H, bmax, s_c, p.c_scale_inv_out, p.c_amax_out,
-                             reinterpret_cast<uint32_t*>(red + NWAVES));
-        return;
-      }
-      if (tid == 0) publish_max(reinterpret_cast<uint32_t*>(p.c_amax_out), bmax);
-    }
-    if (tid == 0 && p.c_scale_inv_out && blockIdx.x == 0) *p.c_scale_inv_out = 1.0f / s_c;
-  }
+  if (rows_in > 0)
+    amax = act_strips_any<OUT, GATED>(p, acc, bias_s, col_s, row0, col0, rows_in, cols_in, s_c);
+  act_finish<OUT, NT>(p, amax, s_c, reinterpret_cast<float*>(pool + Lds::kActRed));
 }
 
 // Gating fixed at compile time (it decides the output tile's shape).
@@ -426,6 +435,128 @@ static hipError_t launch_act_tile(const P& p0, hipStream_t st) {
   hipLaunchKernelGGL((mm_fp8_dma<kE4M3, kE4M3, BM, BN, WM_, WN_, MINB, OUT, 0, PREC, DEEP, P>),
                      dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WM_ * WN_), 0, st, p, tiles_m, tiles_n, BM == 128 ? 8 : 4);
   return hipGetLastError();
+}
+
+// ===========================================================================
+// Few rows (serving): bound by reading the weights once.  A workgroup takes 16
+// weight rows and all of A's (at most 16 TI), its NW waves every NW-th K step
+// of 128; fragments come straight from global memory into registers, U steps in
+// flight per wave, no LDS and no barrier before the end.  Lane group g of a
+// fragment takes k = 16 g .. + 15 and 64 + 16 g .. + 15 of the step instead of
+// 32 g .. + 31, A and B alike: the sums are over the same products, and each
+// load instruction reads 64 contiguous bytes of a row.  The waves'
+// sums meet in LDS, added in wave order, and the epilogue is that of one
+// 16-column strip per 16 rows.  (32 x 1536 x 6912 with residual, graph replay:
+// 16.7 us in 64 x 32 tiles, whose rows are half empty and whose 48 workgroups
+// leave most CUs idle.)
+// ===========================================================================
+template <int OUT, bool GATED, int TI, int NW>
+__global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
+  constexpr int NT = 64 * NW, U = 4;
+  static_assert(NW >= TI, "one wave per 16 rows finishes them");
+  __shared__ float4 part[NW][TI][64];
+  __shared__ float bias_s[16], col_s[16];
+  __shared__ float red[NW + 1];
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  // raw buffers: rows past an edge and chunks past K read as zero
+  const int ext_a = (int)p.a_extent_from(0), ext_b = (int)p.b_extent_from(n0);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a), 0, ext_a, 0x00020000);
+  const auto rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.b + n0 * p.ldb), 0, ext_b, 0x00020000);
+  const int K = (int)p.K, steps = (K + kBK - 1) / kBK;
+  const uint32_t ob = (uint32_t)r16 * (uint32_t)p.ldb + 16 * g;
+  uint32_t oa[TI];  // a row past M - 1 starts at or beyond the extent
+#pragma unroll
+  for (int i = 0; i < TI; ++i) oa[i] = 16 * i + r16 < p.M ? (uint32_t)(16 * i + r16) * (uint32_t)p.lda + 16 * g : (uint32_t)ext_a;
+  const bool b_in = n0 + r16 < p.N;
+  auto frag = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, int ext, int kt) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const int k = kt * kBK + 16 * g;
+    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(rs, k < K ? off + kt * kBK : ext, 0, 0);
+    const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(rs, k + 64 < K ? off + kt * kBK + 64 : ext, 0, 0);
+    v8i r;
+    r[0] = (int)lo[0]; r[1] = (int)lo[1]; r[2] = (int)lo[2]; r[3] = (int)lo[3];
+    r[4] = (int)hi[0]; r[5] = (int)hi[1]; r[6] = (int)hi[2]; r[7] = (int)hi[3];
+    return r;
+  };
+  v4f acc[TI];
+#pragma unroll
+  for (int i = 0; i < TI; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  v8i bf[U], af[U][TI];
+  auto load = [&](int kt) {  // a step past the end reads nothing (k >= K)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bf[u] = frag(rsb, b_in ? ob : (uint32_t)ext_b, ext_b, kt + u * NW);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) af[u][i] = frag(rsa, oa[i], ext_a, kt + u * NW);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all in flight before anything waits
+  };
+  load(wid);
+  // bias and column scales: read behind the first steps' loads, parked after the K loop
+  const int64_t pc = n0 + (lane & 15);
+  const bool col_in = tid < 16 && pc < p.N;
+  const uint32_t bias_bits = p.bias && col_in ? load_bias_bits(p, pc) : 0u;
+  float col_scale = 1.0f;
+  if (p.b_scale_inv) col_scale = p.b_scale_inv[p.b_rows ? (pc < p.N ? pc : n0) : 0];
+  for (int kt = wid; kt < steps;) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < TI; ++i) acc[i] = mfma_nt<kE4M3, kE4M3>(bf[u], af[u][i], acc[i]);
+    kt += U * NW;
+    if (kt < steps) load(kt);
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i) part[wid][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  if (tid < 16) {
+    bias_s[tid] = col_in && p.bias ? decode_bias(p, bias_bits, 1.0f) : 0.0f;
+    col_s[tid] = col_scale;
+  }
+  const float s_c = act_out_scale<OUT>(p);
+  __syncthreads();
+  float amax = 0.0f;
+  const int64_t row0 = 16 * wid;
+  if (wid < TI && row0 < p.M) {
+    v4f sum[1][1];
+    const float4 f = part[0][wid][lane];
+    sum[0][0] = v4f{f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const float4 q = part[w][wid][lane];
+      sum[0][0][0] += q.x; sum[0][0][1] += q.y; sum[0][0][2] += q.z; sum[0][0][3] += q.w;
+    }
+    const int rows_in = p.M - row0 < 16 ? (int)(p.M - row0) : 16;
+    const int cols_in = p.N - n0 < 16 ? (int)(p.N - n0) : 16;
+    amax = act_strips_any<OUT, GATED>(p, sum, bias_s, col_s, row0, n0, rows_in, cols_in, s_c);
+  }
+  act_finish<OUT, NT>(p, amax, s_c, red);
+}
+
+template <int OUT, bool GATED, int TI> static hipError_t launch_act_rows_ti(const MmActArgs& p, hipStream_t st) {
+  const unsigned wgs = (unsigned)((p.N + 15) / 16);
+  // waves per workgroup: enough of them over the chip, no more than K steps
+  const int64_t steps = (p.K + kBK - 1) / kBK;
+  if (wgs >= 768 || steps <= 8) hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 4>), dim3(wgs), dim3(256), 0, st, p);
+  else if (wgs >= 384 || steps <= 16) hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 8>), dim3(wgs), dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 16>), dim3(wgs), dim3(1024), 0, st, p);
+  return hipGetLastError();
+}
+template <int OUT, bool GATED> static hipError_t launch_act_rows(const MmActArgs& p, hipStream_t st) {
+  return p.M <= 16 ? launch_act_rows_ti<OUT, GATED, 1>(p, st) : launch_act_rows_ti<OUT, GATED, 2>(p, st);
+}
+// Every workgroup reads all of A, which the tiles share through LDS: taken for
+// at most 8 rows, for 16 while the weights are small, for 32 while there is
+// at most one workgroup per CU.  Graph replay, tiles -> this (us): 1 x 13824 x
+// 1536 9.6 -> 7.5, 8 x 4096 x 4096 11.4 -> 7.7, 16 x 1536 x 6912 16.0 -> 9.6,
+// 32 x 1536 x 6912 16.1 -> 12.8, 32 x 4096 x 4096 11.4 -> 10.8; and where the
+// tiles stay: 16 x 28672 x 8192 50 against 59, 32 x 8192 x 2048 8.3 against
+// 10.6, 64 x 1536 x 6912 16.2 against 19.6.
+static inline bool act_few_rows(const MmActArgs& p) {
+  if (p.M <= 8) return true;
+  if (p.M <= 16) return p.N * p.K <= (int64_t)32 << 20;
+  return p.M <= 32 && p.N <= 16 * (int64_t)device_cu_count();
 }
 
 // The plain GEMM's tile (pick_tile), or 4: 128 x 192 tiles of four waves, two
@@ -457,6 +588,7 @@ static inline int pick_act_tile(const MmActArgs& p, bool plain_q8, int ncu) {
 
 template <int OUT, bool GATED> static hipError_t launch_act_family(const MmActArgs& args, hipStream_t st) {
   using P = MmActTyped<GATED>;
+  if (!mm_precise(args) && act_few_rows(args)) return launch_act_rows<OUT, GATED>(args, st);
   P p;
   static_cast<MmActArgs&>(p) = args;
   const int tile = mm_precise(p) ? pick_tile(p, device_cu_count())
