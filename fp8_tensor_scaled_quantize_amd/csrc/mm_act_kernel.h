@@ -33,17 +33,18 @@ __device__ __forceinline__ void swap16(float& a, float& b) {
   b = __uint_as_float(r[1]);
 }
 // Columns per lane and pair, pairs per strip (a strip of one tile is taken as
-// it is, 4 columns per lane; the last of three tiles pairs with nothing).
+// it is, 4 columns per lane).
 constexpr int pair_cols(int tj) { return tj == 1 ? 4 : 8; }
 constexpr int strip_pairs(int tj) { return (tj + 1) / 2; }
 template <int TJ> __device__ __forceinline__ void lane_columns(const v4f (&acc)[TJ], int c, float (&t)[pair_cols(TJ)]) {
+  static_assert(TJ == 1 || TJ % 2 == 0, "whole pairs");
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if constexpr (TJ == 1) {
       t[r] = acc[0][r];
     } else {
       t[r] = acc[2 * c][r];
-      t[4 + r] = 2 * c + 1 < TJ ? acc[2 * c + 1 < TJ ? 2 * c + 1 : 0][r] : 0.0f;
+      t[4 + r] = acc[2 * c + 1][r];
       swap16(t[r], t[4 + r]);
     }
   }
@@ -80,17 +81,19 @@ template <int BM> __device__ __forceinline__ void warm_res(v4i rsrc, int64_t ld_
 }
 
 // W words to element-aligned memory (EB bytes per element), n of the W * 4 / EB
-// elements; W = 1, 2, 4 or 8.
-template <int W, int EB> __device__ __forceinline__ void store_words(uint8_t* g, const uint32_t (&w)[W], int n) {
+// elements; W = 1, 2, 4 or 8.  STREAM: non-temporal.
+template <int W, int EB, bool STREAM = false> __device__ __forceinline__ void store_words(uint8_t* g, const uint32_t (&w)[W], int n) {
   if (n >= W * 4 / EB) {
     if constexpr (W >= 4) {
 #pragma unroll
       for (int c = 0; c < W / 4; ++c) {
         const u32x4_byte v = {w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
-        reinterpret_cast<u32x4_byte*>(g)[c] = v;
+        if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_byte*>(g) + c);
+        else reinterpret_cast<u32x4_byte*>(g)[c] = v;
       }
     } else if constexpr (W == 2) {
-      *reinterpret_cast<u32x2_byte*>(g) = u32x2_byte{w[0], w[1]};
+      if constexpr (STREAM) __builtin_nontemporal_store(u32x2_byte{w[0], w[1]}, reinterpret_cast<u32x2_byte*>(g));
+      else *reinterpret_cast<u32x2_byte*>(g) = u32x2_byte{w[0], w[1]};
     } else {
       typedef uint32_t u32_byte __attribute__((aligned(1)));
       *reinterpret_cast<u32_byte*>(g) = w[0];
@@ -204,6 +207,12 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
   // joined by v_permlane32_swap, so that a lane stores 16 consecutive t columns
   constexpr int WO = OUT < 0 ? CO / 2 : (CO + 3) / 4, EB = OUT < 0 ? 2 : 1;
   constexpr bool JOIN = NP == 2 && WO < 4;
+  // The big tiles' 16-byte stores of pre-activations and bf16 outputs bypass
+  // the L2's keeping (their sizes pass it by far, the operand panels stay):
+  // 8192 x 6912 x 1536 gelu to fp8 with pre-activations 140 -> 121 us over three
+  // sets of buffers in turn, bf16 output without them 107 -> 100.  Narrower
+  // stores fill a line in several steps and lose by it (98 -> 105).
+  constexpr bool STREAM = TI * TJ >= 24;
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
   const auto clip = [](int v, int most) { return v < 0 ? 0 : (v < most ? v : most); };
   const float sa = p.a_scale_inv && !p.a_rows ? *p.a_scale_inv : 1.0f;
@@ -218,15 +227,11 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
 #pragma unroll
     for (int c = 0; c < NP; ++c) {
       const int at = lane_column<TJ>(g, c);
-      const bool idle = at >= 16 * TJ;  // three tiles: the absent fourth's lanes
 #pragma unroll
       for (int e = 0; e < C; e += 4) {
-        const float4 b4 = *reinterpret_cast<const float4*>(bias_s + (idle ? 0 : at) + e);
-        const float4 c4 = *reinterpret_cast<const float4*>(col_s + (idle ? 0 : at) + e);
-        bias[c][e] = idle ? 0.0f : b4.x;
-        bias[c][e + 1] = idle ? 0.0f : b4.y;
-        bias[c][e + 2] = idle ? 0.0f : b4.z;
-        bias[c][e + 3] = idle ? 0.0f : b4.w;
+        const float4 b4 = *reinterpret_cast<const float4*>(bias_s + at + e);
+        const float4 c4 = *reinterpret_cast<const float4*>(col_s + at + e);
+        bias[c][e] = b4.x; bias[c][e + 1] = b4.y; bias[c][e + 2] = b4.z; bias[c][e + 3] = b4.w;
         // fl32(sa sb); row scales of A are multiplied in strip by strip
         cs[c][e] = sa * c4.x; cs[c][e + 1] = sa * c4.y; cs[c][e + 2] = sa * c4.z; cs[c][e + 3] = sa * c4.w;
       }
@@ -235,7 +240,7 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
 #pragma unroll
   for (int c = 0; c < NP; ++c) {
     const int at = lane_column<TJ>(g, c);
-    n[c] = at >= 16 * TJ ? 0 : clip(cols_in - at, C);
+    n[c] = clip(cols_in - at, C);
     col[c] = col0 + at;
   }
   if constexpr (!LEAN) load_cols();
@@ -281,7 +286,7 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
       for (int c = 0; c < NP; ++c) {
         uint32_t w[C / 2];
         pack_bf16<C>(w, t[c]);
-        store_words<C / 2, 2>(reinterpret_cast<uint8_t*>(p.z + row * p.ld_z + col[c]), w, n[c]);
+        store_words<C / 2, 2, STREAM>(reinterpret_cast<uint8_t*>(p.z + row * p.ld_z + col[c]), w, n[c]);
       }
     }
 #pragma unroll
@@ -353,11 +358,11 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
       }
       if (in)
         store_words<2 * WO, EB>(static_cast<uint8_t*>(p.c) + (at + (col0 + 16 * g) / G) * EB, o,
-                                16 * g >= 16 * TJ ? 0 : clip(cols_in - 16 * g, 16) / G);
+                                clip(cols_in - 16 * g, 16) / G);
     } else if (in) {
 #pragma unroll
       for (int c = 0; c < NP; ++c)  // two codes alone (gated, one tile a wave) fill half their word
-        store_words<WO, EB>(static_cast<uint8_t*>(p.c) + (at + col[c] / G) * EB, w[c], n[c] / G);
+        store_words<WO, EB, STREAM && OUT < 0 && WO == 4>(static_cast<uint8_t*>(p.c) + (at + col[c] / G) * EB, w[c], n[c] / G);
     }
     __builtin_amdgcn_sched_barrier(0);  // one strip's registers at a time
   }
@@ -559,30 +564,32 @@ static inline bool act_few_rows(const MmActArgs& p) {
   return p.M <= 32 && p.N <= 16 * (int64_t)device_cu_count();
 }
 
-// The plain GEMM's tile (pick_tile), or 4: 128 x 192 tiles of four waves, two
+// The plain GEMM's tile (pick_tile) for small problems; for large ones 256 x
+// 256 (0), its mixed grid (7), or 128 x 192 tiles of four waves (4), two
 // workgroups per CU, so that one's epilogue passes under the other's K loop.
-// Costs are in 1/256 of a round of 256 x 256 tiles: a round of 256 x 192 takes
-// 230, one of two 128 x 192 tiles per CU 202 (a last round at most half full
-// 0.6 of it, its workgroups having a CU each), 15% more where K is long and
-// the smaller tile's L2 traffic counts.  The mixed grid's band costs 150 in
-// place of a last round, but not with plain fp8 outputs, where it measured
-// slower than its count.  Both sides measured (us, others -> this tile):
-// 8192 x 6912 x 1536 gelu to fp8 117 -> 100, with pre-activations 122 -> 108;
-// 6144 x 6144 x 1536 gelu 75 -> 70, to fp8 88 -> 68; 2048 x 10240 x 1024 gated
-// to fp8 35 -> 33; and where the rule keeps the others: 8192 x 6912 x 1536
-// without activation 94 against 97, 4096^3 52 against 69, 8192 x 1536 x 6912
-// 72 against 74, 8192^3 392 against 473.
+// Costs are in 1/256 of a round of 256 x 256 tiles: a round of two 128 x 192
+// tiles per CU takes 202 (a last round at most half full 0.6 of it, its
+// workgroups having a CU each), 27% more where K is long and the smaller
+// tile's L2 traffic counts.  The mixed grid's band costs 150 in place of a
+// last round, but not with plain fp8 outputs, where it measured slower than
+// its count.  Both sides measured, over three sets of buffers in turn (us,
+// others -> 128 x 192): 8192 x 6912 x 1536 gelu to fp8 115 -> 102, with
+// pre-activations 120 -> 111; 6144 x 6144 x 1536 gelu 72 -> 68, to fp8 83 -> 67;
+// 4096 x 2560 x 2048 gelu to fp8 34 -> 29; 8192 x 1536 x 1536 residual 31 -> 28;
+// and where the rule keeps the others: 8192 x 6912 x 1536 with residual 137
+// against 157, 4096 x 3584 x 4096 gelu 52 against 70, 8192 x 13824 x 1536 with
+// pre-activations 237 against 268, 8192^3 400 against 494.
 static inline int pick_act_tile(const MmActArgs& p, bool plain_q8, int ncu) {
   static const int forced = env_int_in("FP8MI_MM_TILE", 0, 8, -1);
   if (forced >= 0) return forced;
-  const int base = pick_tile(p, ncu);
+  int base = pick_tile(p, ncu);
   if (base != 0 && base != 3 && base != 7) return base;
-  const int64_t tm = (p.M + 255) / 256;
-  const int64_t r256 = (tm * ((p.N + 255) / 256) + ncu - 1) / ncu, r192 = (tm * ((p.N + 191) / 192) + ncu - 1) / ncu;
-  const int64_t cost = base == 3 ? r192 * 230 : (base == 7 && !plain_q8 ? (r256 - 1) * 256 + 150 : r256 * 256);
+  base = mixed_band_cols(p, ncu) > 0 ? 7 : 0;
+  const int64_t r256 = (((p.M + 255) / 256) * ((p.N + 255) / 256) + ncu - 1) / ncu;
+  const int64_t cost = base == 7 && !plain_q8 ? (r256 - 1) * 256 + 150 : r256 * 256;
   const int64_t t = ((p.M + 127) / 128) * ((p.N + 191) / 192), full = t / (2 * ncu), rest = t % (2 * ncu);
   int64_t own = full * 202 + (rest == 0 ? 0 : (rest <= ncu ? 121 : 202));
-  if (p.K > 2048) own += own * 15 / 100;
+  if (p.K > 2048) own += own * 27 / 100;
   return own < cost ? 4 : base;
 }
 
@@ -601,8 +608,8 @@ template <int OUT, bool GATED> static hipError_t launch_act_family(const MmActAr
     }
   }
   switch (tile) {
-    case 0: return launch_act_tile<256, 256, 2, 4, 1, OUT, P>(p, st);
-    case 3: return launch_act_tile<256, 192, 2, 4, 1, OUT, P>(p, st);
+    case 0:
+    case 3: return launch_act_tile<256, 256, 2, 4, 1, OUT, P>(p, st);
     case 1: return launch_act_tile<128, 128, 2, 2, 2, OUT, P>(p, st);
     case 4: return launch_act_tile<128, 192, 2, 2, 2, OUT, P>(p, st);
     case 5: return launch_act_tile<64, 64, 1, 4, 2, OUT, P>(p, st);
