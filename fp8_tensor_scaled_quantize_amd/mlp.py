@@ -1,0 +1,158 @@
+"""A pre-norm feed-forward block in fp8, driven through the C ABI: the norm
+with the residual's addition, the up-projection with its activation and the
+down-projection with the residual stream, each one call.
+
+    h = x + residual                       (residual optional)
+    n = rmsnorm(h) * norm_weight           fp8_rmsnorm     -> E4M3 codes, h, 1 / rms
+    u = act(n W_up^T + b_up)               fp8_mm_act      -> E4M3 codes, pre-activations
+        (gated: act(gate) * value, W_up's rows alternating gate and value)
+    y = u W_down^T + b_down + h            fp8_mm_act      -> bf16
+
+forward / backward (training, delayed scaling): every quantized tensor has its
+amax-history ring, as Fp8Linear's have; a step has no host synchronisation.
+
+    dY  -> E5M2 codes in both layouts, db_down       fp8_quantize_dual_bias_grad
+    dU  = dY W_down                                  fp8_mm
+    dZ  -> E5M2 codes in both layouts, db_up         fp8_act_grad (from dU, pre-activations)
+    dN  = dZ W_up                                    fp8_mm
+    dW_down = dY^T U, dW_up = dZ^T N                 fp8_mm (U, N read K-major)
+    dX  = gradient of the norm + dY, dnorm_weight    fp8_rmsnorm_grad
+
+decode (serving): weights quantized once by freeze(), the norm's codes with one
+scale per row, the activation's with the trained (or calibrated) scale; the
+residual stream is updated in place.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_quantize_dual,
+               fp8_quantize_dual_bias_grad, fp8_quantize_dynamic, fp8_rmsnorm, fp8_rmsnorm_grad, new_ring)
+
+
+class Fp8Mlp:
+    """norm_weight [d]; w_up [F, d], or [2F, d] with interleaved rows when
+    gated (interleave_gated); w_down [d, F]; biases optional."""
+
+    def __init__(self, norm_weight: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                 b_up: torch.Tensor | None = None, b_down: torch.Tensor | None = None, act="silu",
+                 gated: bool = False, eps: float = 1e-6, hist_len: int = 16):
+        d, n_up = norm_weight.shape[0], w_up.shape[0]
+        f = n_up // 2 if gated else n_up
+        if tuple(w_up.shape) != (n_up, d) or tuple(w_down.shape) != (d, f) or (gated and n_up % 2):
+            raise ValueError(f"weights {tuple(w_up.shape)} and {tuple(w_down.shape)} do not fit a width of {d}"
+                             + (" (gated)" if gated else ""))
+        self.norm_weight, self.w_up, self.w_down = norm_weight, w_up, w_down
+        self.b_up, self.b_down = b_up, b_down
+        self.act, self.gated, self.eps, self.hist_len = act, gated, eps, hist_len
+        dev = norm_weight.device
+        # n, W_up, u, W_down, dY, dZ
+        self.rings = {k: new_ring(hist_len, 1.0, dev) for k in ("n", "w_up", "u", "w_down", "g", "z")}
+        self.scale_inv = {k: torch.empty(1, dtype=torch.float32, device=dev) for k in self.rings}
+        self._frozen = None
+        self._saved = None
+        self._forwards = 0
+
+    def _weight(self, name: str, w: torch.Tensor):
+        return fp8_quantize_dual(w, E4M3, ring=self.rings[name], scale_inv_out=self.scale_inv[name])
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, save_for_backward: bool = True):
+        """x (and residual) bf16 [..., d] -> the residual stream after the
+        block, bf16 [..., d]."""
+        d = self.norm_weight.shape[0]
+        x2 = x.reshape(-1, d)
+        r2 = None if residual is None else residual.reshape(-1, d)
+        rows, dev, s = x2.shape[0], x.device, self.scale_inv
+        h = x2 if r2 is None else torch.empty_like(x2)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2, ring=self.rings["n"],
+                         scale_inv_out=s["n"], sum_out=None if r2 is None else h, rstd_out=rstd)
+        wu, wu_t = self._weight("w_up", self.w_up)
+        wd, wd_t = self._weight("w_down", self.w_down)
+        z = torch.empty(rows, self.w_up.shape[0], dtype=torch.bfloat16, device=dev) if save_for_backward else None
+        uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z, out_fmt=E4M3,
+                        out_ring=self.rings["u"], out_scale_inv=s["u"])
+        y = fp8_mm_act(uq, wd, s["u"], s["w_down"], self.b_down, residual=h)
+        self._saved = (nq, h, rstd, z, uq, wu_t, wd_t, x.shape) if save_for_backward else None
+        self._forwards += 1 if save_for_backward else 0
+        return y.reshape(x.shape)
+
+    def backward(self, dy: torch.Tensor) -> dict:
+        """Gradients of the latest saved forward: dx (x's and the residual's),
+        norm_weight, w_up, w_down, b_up, b_down."""
+        if self._saved is None:
+            raise RuntimeError("backward needs a forward with save_for_backward=True")
+        nq, h, rstd, z, uq, wu_t, wd_t, x_shape = self._saved
+        s, r = self.scale_inv, self.rings
+        dy2 = dy.reshape(h.shape)
+        db_down = None
+        if self.b_down is not None:
+            gq, gq_t, db_down = fp8_quantize_dual_bias_grad(dy2, E5M2, ring=r["g"], scale_inv_out=s["g"])
+        else:
+            gq, gq_t = fp8_quantize_dual(dy2, E5M2, ring=r["g"], scale_inv_out=s["g"])
+        du = fp8_mm(gq, wd_t, E5M2, E4M3, s["g"], s["w_down"])
+        zq, zq_t, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, ring=r["z"], scale_inv_out=s["z"],
+                                       need_bias_grad=self.b_up is not None)
+        dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
+        dw_down = fp8_mm(gq_t, uq.t(), E5M2, E4M3, s["g"], s["u"])
+        dw_up = fp8_mm(zq_t, nq.t(), E5M2, E4M3, s["z"], s["n"])
+        dx, dnw = fp8_rmsnorm_grad(dn, h, self.norm_weight, rstd, dsum=dy2)
+        return {"x": dx.reshape(x_shape), "norm_weight": dnw, "w_up": dw_up, "w_down": dw_down, "b_up": db_up,
+                "b_down": db_down}
+
+    # ------------------------------------------------------------------ serving
+    def freeze(self) -> None:
+        """Quantize the weights once for decode (current scaling)."""
+        out = []
+        for w in (self.w_up, self.w_down):
+            si = torch.empty(1, dtype=torch.float32, device=w.device)
+            out.append((fp8_quantize_dynamic(w, E4M3, LAYOUT_ROW, scale_inv_out=si)[0], si))
+        self._frozen = out
+
+    def calibrate(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
+        """Fold one batch's amax into the activation's ring, for decode of a
+        block that was not trained here."""
+        self.forward(x, residual, save_for_backward=False)
+
+    def decode(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
+        """One serving step on [tokens, d]: adds x to residual and the block's
+        output to that, in place; returns residual."""
+        if self._frozen is None:
+            raise RuntimeError("decode needs freeze()")
+        (wu, s_wu), (wd, s_wd) = self._frozen
+        row_inv = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        nq = fp8_rmsnorm(x, self.norm_weight, E4M3, self.eps, residual=residual, row_scaled=True,
+                         scale_inv_out=row_inv, sum_out=residual)
+        scale = self.rings["u"].view(torch.float32)[self.hist_len:self.hist_len + 1]  # the ring's current scale
+        uq = fp8_mm_act(nq, wu, row_inv, s_wu, self.b_up, self.act, self.gated, out_fmt=E4M3, out_scale=scale,
+                        out_scale_inv=self.scale_inv["u"])
+        return fp8_mm_act(uq, wd, self.scale_inv["u"], s_wd, self.b_down, residual=residual, out=residual)
+
+
+class _Fp8MlpFn(torch.autograd.Function):
+    """One Fp8Mlp step on torch's autograd tape; a backward must belong to the
+    block's latest saved forward."""
+
+    @staticmethod
+    def forward(ctx, x, residual, norm_weight, w_up, w_down, b_up, b_down, block):
+        y = block.forward(x, residual)
+        ctx.block, ctx.step = block, block._forwards
+        ctx.dtypes = [None if t is None else t.dtype for t in (x, residual, norm_weight, w_up, w_down, b_up, b_down)]
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        block = ctx.block
+        if block._forwards != ctx.step:
+            raise RuntimeError("fp8_mlp: the block ran another forward since the one being differentiated")
+        g = block.backward(dy.contiguous())
+        grads = [g["x"], g["x"], g["norm_weight"], g["w_up"], g["w_down"], g["b_up"], g["b_down"]]
+        out = [None if t is None or dt is None or not need else t.to(dt)
+               for t, dt, need in zip(grads, ctx.dtypes, ctx.needs_input_grad)]
+        return (*out, None)
+
+
+def fp8_mlp(x: torch.Tensor, block: Fp8Mlp, residual: torch.Tensor | None = None) -> torch.Tensor:
+    """y = block.forward(x, residual) recorded for autograd: the backward pass
+    fills the gradients of x, residual and the block's weights and biases."""
+    return _Fp8MlpFn.apply(x, residual, block.norm_weight, block.w_up, block.w_down, block.b_up, block.b_down, block)
