@@ -53,33 +53,6 @@ template <int TJ> __device__ __forceinline__ int lane_column(int g, int c) {
   return TJ == 1 ? 4 * g : 32 * c + 16 * (g & 1) + 8 * (g >> 1);
 }
 
-// Brings the residual of a BM-row tile into the L2 while the last K steps run:
-// one dword per 128-byte line, straight to a spare KiB of LDS (no register
-// waits for it).  Called by `waves` waves (w-th of them here) that load nothing
-// else; the resource's base is 4-byte aligned, rows and bytes past `extent` are
-// not fetched.
-template <int BM> __device__ __forceinline__ void warm_res(v4i rsrc, int64_t ld_bytes, int row_bytes, int extent, uint32_t lds,
-                                                           int w, int waves) {
-  const int lane = threadIdx.x & 63;
-  const int lines = (row_bytes + 127) / 128;  // per row, a power of two or less
-  const int lpr = lines <= 1 ? 1 : (lines <= 2 ? 2 : (lines <= 4 ? 4 : 8));
-  const int rpi = 64 / lpr;                   // rows per instruction
-  const int line = lane % lpr;
-  for (int r = w * rpi + lane / lpr; r - lane / lpr < BM; r += waves * rpi) {
-    const int64_t off = (r * ld_bytes + 128 * line) & ~int64_t{3};  // whole dwords
-    const int voff = (line < lines && off < extent) ? (int)off : extent;
-    int saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "buffer_load_dword %2, %3, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc)
-        : "memory");
-  }
-}
-
 // W words to element-aligned memory (EB bytes per element), n of the W * 4 / EB
 // elements; W = 1, 2, 4 or 8.  STREAM: non-temporal.
 template <int W, int EB, bool STREAM = false> __device__ __forceinline__ void store_words(uint8_t* g, const uint32_t (&w)[W], int n) {
@@ -109,41 +82,12 @@ template <int W, int EB, bool STREAM = false> __device__ __forceinline__ void st
   }
 }
 
-// C consecutive residual values as stored: words 0 .. C - 1 (fp32), or packed
-// in words 0 .. C / 2 - 1; n of them lie inside the matrix.  (A vector, not an
-// array: the two types' stores into one array would be merged through a
-// pointer, which puts it into memory.)
-template <int C> struct ResWords {
-  typedef uint32_t V __attribute__((ext_vector_type(C)));
-  V w;
+// C consecutive 16-bit residual values as stored, n of them inside the matrix.
+template <int C> struct Res16 {
+  uint32_t w[C / 2];
 };
-template <int C> __device__ __forceinline__ ResWords<C> load_res(const MmActArgs& p, int64_t row, int64_t col, int n) {
-  ResWords<C> o;
-  o.w = 0u;
-  const int64_t at = row * p.ld_res + col;
-  if (p.res_dt == kF32) {
-    const uint32_t* q = static_cast<const uint32_t*>(p.res) + at;
-    if (n >= C) {
-      if constexpr (C >= 4) {
-#pragma unroll
-        for (int c = 0; c < C / 4; ++c) {
-          const u32x4_any v = reinterpret_cast<const u32x4_any*>(q)[c];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o.w[4 * c + e] = v[e];
-        }
-      } else {
-        const u32x2_any v = *reinterpret_cast<const u32x2_any*>(q);
-        o.w[0] = v[0];
-        o.w[1] = v[1];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < C - 1; ++e)
-        if (e < n) o.w[e] = q[e];
-    }
-    return o;
-  }
-  const uint16_t* q = static_cast<const uint16_t*>(p.res) + at;
+template <int C> __device__ __forceinline__ void load_res16(Res16<C>& o, const MmActArgs& p, int64_t row, int64_t col, int n) {
+  const uint16_t* q = static_cast<const uint16_t*>(p.res) + row * p.ld_res + col;
   if (n >= C) {
     if constexpr (C == 8) {
       const u32x4_any v = *reinterpret_cast<const u32x4_any*>(q);
@@ -157,33 +101,38 @@ template <int C> __device__ __forceinline__ ResWords<C> load_res(const MmActArgs
       typedef uint32_t u32_any __attribute__((aligned(2)));
       o.w[0] = *reinterpret_cast<const u32_any*>(q);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < C - 1; ++e)
-      if (e < n) o.w[e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
+    return;
   }
-  return o;
+#pragma unroll
+  for (int e = 0; e < C / 2; ++e) o.w[e] = 0u;
+#pragma unroll
+  for (int e = 0; e < C - 1; ++e)
+    if (e < n) o.w[e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
 }
-template <int C> __device__ __forceinline__ void add_res(float (&y)[C], const ResWords<C>& r, int dt) {
-  if (dt == kF32) {
+template <int C> __device__ __forceinline__ void add_res16(float (&y)[C], const Res16<C>& r, bool bf16) {
 #pragma unroll
-    for (int e = 0; e < C; ++e) y[e] += __uint_as_float(r.w[e]);
-  } else if (dt == kBF16) {
+  for (int e = 0; e < C; e += 2) {
+    float a, b;
+    if (bf16) widen2<kBF16>(r.w[e / 2], a, b);
+    else widen2<kF16>(r.w[e / 2], a, b);
+    y[e] += a;
+    y[e + 1] += b;
+  }
+}
+template <int C> __device__ __forceinline__ void add_res32(float (&y)[C], const MmActArgs& p, int64_t row, int64_t col, int n) {
+  const float* q = static_cast<const float*>(p.res) + row * p.ld_res + col;
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  if (C % 4 == 0 && n >= C) {
 #pragma unroll
-    for (int e = 0; e < C; e += 2) {
-      float a, b;
-      widen2<kBF16>(r.w[e / 2], a, b);
-      y[e] += a;
-      y[e + 1] += b;
+    for (int c = 0; c < C / 4; ++c) {
+      const f32x4_any v = reinterpret_cast<const f32x4_any*>(q)[c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[4 * c + e] += v[e];
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < C; e += 2) {
-      float a, b;
-      widen2<kF16>(r.w[e / 2], a, b);
-      y[e] += a;
-      y[e + 1] += b;
-    }
+    for (int e = 0; e < C; ++e)
+      if (e < n) y[e] += q[e];
   }
 }
 
@@ -217,8 +166,7 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
   const auto clip = [](int v, int most) { return v < 0 ? 0 : (v < most ? v : most); };
   const float sa = p.a_scale_inv && !p.a_rows ? *p.a_scale_inv : 1.0f;
   // Three pairs (the 128 x 192 tile): bias and scales are read from LDS strip
-  // by strip and the residual where it is added -- the registers would not
-  // suffice, and there the CU's other workgroup covers the latency.
+  // by strip, the registers would not suffice.
   constexpr bool LEAN = NP > 2;
   int n[NP];  // the lane's columns inside the matrix
   int64_t col[NP];
@@ -246,23 +194,29 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
   if constexpr (!LEAN) load_cols();
   const bool sreg = OUT >= 0 && scale_regular(s_c);
   float amax = 0.0f;
-  // residual of strip i + 1 in flight while strip i is finished
-  ResWords<CO> raw[LEAN ? 1 : NP], next[LEAN ? 1 : NP];
-  if (!LEAN && p.res) {
+  // A 16-bit residual's next strips are in flight while one is finished: as many
+  // as the registers that the epilogue leaves free hold.  Over three sets of
+  // buffers in turn, without a residual -> with it (us): 8192 x 6912 x 1536
+  // 91 -> 130, 4096 x 3584 x 4096 48 -> 52, 8192 x 1536 x 6912 78 -> 92 (one
+  // strip ahead 97), 8192^3 383 -> 421; brought into the L2 during the last K
+  // steps by waves that load nothing else 136, 55, 91 and 432.
+  constexpr int AHEAD = (LEAN ? 2 : 4) - (OUT < 0 ? 0 : 1);
+  const bool res16 = p.res && p.res_dt != kF32;
+  Res16<CO> raw[AHEAD][NP];
+  auto fetch = [&](Res16<CO> (&to)[NP], int i) {
 #pragma unroll
-    for (int c = 0; c < (LEAN ? 0 : NP); ++c)
-      raw[c] = load_res<CO>(p, row0 + r16, col[c] / G, r16 < rows_in ? n[c] / G : 0);
+    for (int c = 0; c < NP; ++c)
+      load_res16<CO>(to[c], p, row0 + 16 * i + r16, col[c] / G, 16 * i + r16 < rows_in ? n[c] / G : 0);
+  };
+  if (res16) {
+#pragma unroll
+    for (int i = 0; i < (AHEAD < TI ? AHEAD : TI); ++i) fetch(raw[i], i);
   }
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int lr = 16 * i + r16;
     const bool in = lr < rows_in;
     const int64_t row = row0 + lr;
-    if (!LEAN && p.res && i + 1 < TI) {
-#pragma unroll
-      for (int c = 0; c < (LEAN ? 0 : NP); ++c)
-        next[c] = load_res<CO>(p, row + 16, col[c] / G, lr + 16 < rows_in ? n[c] / G : 0);
-    }
     const float ra = p.a_rows ? p.a_scale_inv[in ? row : row0] : 1.0f;
     // step by step over the whole strip: few, long basic blocks, so that the
     // chains of exp2 and reciprocal of different values overlap
@@ -294,16 +248,13 @@ __device__ __forceinline__ float act_strips(const MmActArgs& p, const v4f (&acc)
 #pragma unroll
       for (int e = 0; e < CO; ++e)
         y[c][e] = GATED ? act_value<ACT>(t[c][G * e]) * t[c][G * e + G - 1] : act_value<ACT>(t[c][e]);
-    if (p.res) {
+    if (res16) {
 #pragma unroll
-      for (int c = 0; c < NP; ++c) {
-        if constexpr (LEAN) {
-          add_res<CO>(y[c], load_res<CO>(p, row, col[c] / G, in ? n[c] / G : 0), p.res_dt);
-        } else {
-          add_res<CO>(y[c], raw[c], p.res_dt);
-          raw[c] = next[c];
-        }
-      }
+      for (int c = 0; c < NP; ++c) add_res16<CO>(y[c], raw[i % AHEAD][c], p.res_dt == kBF16);
+      if (i + AHEAD < TI) fetch(raw[i % AHEAD], i + AHEAD);
+    } else if (p.res) {
+#pragma unroll
+      for (int c = 0; c < NP; ++c) add_res32<CO>(y[c], p, row, col[c] / G, in ? n[c] / G : 0);
     }
     uint32_t w[NP][WO];
     if constexpr (OUT < 0) {

@@ -11,7 +11,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kBK = 128;
-constexpr int kWarmSteps = 4;  // K steps before the end at which a tile's residual is read ahead
 constexpr int kMmThreads = 256;
 
 // LDS tiles: rows of kBK = 128 bytes; the 16-byte chunk c of row r sits at
@@ -280,24 +279,20 @@ template <int BM, int BN, int NWAVES, int DEEP> struct TileLds {
   static constexpr int kBias = kSmem;           // BN floats
   static constexpr int kRed = kBias + 4 * BN;   // NWAVES + 1 words
   static constexpr int kBytes = kRed + 4 * (NWAVES + 1);
-  // The fused epilogue (mm_act_kernel.h) also keeps the tile's column scales,
-  // and a KiB that takes what is read ahead only to be in the L2.  The 128 x
-  // 192 tile, whose stages are half a CU's LDS, keeps all this in a stage that
-  // the K loop has left.
+  // The fused epilogue (mm_act_kernel.h) also keeps the tile's column scales.
+  // The 128 x 192 tile, whose stages are half a CU's LDS, keeps all this in a
+  // stage that the K loop has left.
   static constexpr bool kActInStage = BM * BN == 128 * 192;
   static constexpr int kActBias = kActInStage ? 0 : kBias;
   static constexpr int kActRed = kActInStage ? 8 * BN : kRed;
   static constexpr int kActCol = kActInStage ? 4 * BN : (kBytes + 15) / 16 * 16;  // BN floats
-  static constexpr int kSpare = kActCol + 4 * BN;
-  static constexpr int kActBytes = kActInStage ? kStages * kStage : kSpare + 1024;
+  static constexpr int kActBytes = kActInStage ? kStages * kStage : kActCol + 4 * BN;
 };
 
 // The fused epilogue of fp8_mm_act (mm_act_kernel.h).
 template <int BM, int BN, int WAVES_M, int WAVES_N, int DEEP, int OUT, int TI, int TJ, class P>
 __device__ __forceinline__ void act_epilogue(const P& p, v4f (&acc)[TI][TJ], uint8_t* pool, const int64_t m0,
                                              const int64_t n0);
-template <int BM> __device__ __forceinline__ void warm_res(v4i rsrc, int64_t ld_bytes, int row_bytes, int extent,
-                                                           uint32_t lds, int w, int waves);
 
 // One BM x BN output tile at (m0, n0) of batch bz, with `pool` the
 // workgroup's TileLds bytes.
@@ -503,24 +498,9 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
         issue_chunk(1, kBK, 3);
       }
     }
-    // Fused epilogue: the waves that load nothing bring the tile's residual into
-    // the L2 during the last K steps, so the epilogue does not wait for HBM.
-    constexpr bool kWarm = P::kAct && NLW < NWAVES;
     for (int kt = 0; kt < nk; ++kt) {
       const uint8_t* As = smem + (kt & 1) * STAGE;
       const uint8_t* An = smem + ((kt + 1) & 1) * STAGE;
-      if constexpr (kWarm) {
-        if (wid >= NLW && p.res && kt == (nk > kWarmSteps ? nk - kWarmSteps : 0)) {
-          constexpr int G = P::kGated ? 2 : 1;
-          const int eb = p.res_dt == kF32 ? 4 : 2;
-          const int64_t rows = p.M - m0 < BM ? p.M - m0 : BM, outs = (p.N - n0 < BN ? p.N - n0 : BN) / G;
-          const uintptr_t first = reinterpret_cast<uintptr_t>(p.res) + (m0 * p.ld_res + n0 / G) * eb;
-          const int64_t ext = (((rows - 1) * p.ld_res + outs) * eb + (int64_t)(first & 3u)) & ~int64_t{3};
-          if (outs > 0 && ext < (1ll << 31))
-            warm_res<BM>(buffer_rsrc(reinterpret_cast<const void*>(first & ~uintptr_t{3}), (int)ext), p.ld_res * eb,
-                         (int)outs * eb, (int)ext, smem_lds + Lds::kSpare, wid - NLW, NWAVES - NLW);
-        }
-      }
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         if (i + 2 < TI) ar[(i + 2) & 3] = frag_a(As, i + 2);
@@ -542,8 +522,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
         if (early && i >= TI - 2 && kt + 2 < nk) issue_chunk(kt & 1, (kt + 2) * kBK, 2 + i - (TI - 2));
         if (i == TI - 3) {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          // a wave without K-step loads has only read-ahead in flight: no wait
-          if (!kWarm || wid < NLW) wait_vmem();
+          wait_vmem();
           __syncthreads();
           if (kt + 2 < nk) {
             issue_chunk(kt & 1, (kt + 2) * kBK, 0);
@@ -556,7 +535,6 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     // every wave passed the last barrier after its last read of a stage the
     // epilogue overwrites: wait for the idle-stage reads of the last step too
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if constexpr (kWarm) wait_vmem();  // LDS writes of the read-ahead end before the workgroup can
     if constexpr (P::kAct && Lds::kActInStage) __syncthreads();  // every wave's last reads of the stages are over
     park_bias();
     __syncthreads();
