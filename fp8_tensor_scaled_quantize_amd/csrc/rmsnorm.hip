@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradArgs p) {
       }
     }
     dot = row_sum<WPR>(dot, red[parity], wr, lane);
-    const float k = -(rk * rk) * rk * (dot / p.n_cols);
+    // rstd^3 by itself leaves fp32's range where rows are beyond 1e12 or below 1e-12
+    const float k = -rk * (rk * (rk * (dot / p.n_cols)));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll

@@ -230,6 +230,22 @@ def test_grad_types_and_strides(dt, rows, cols, ld, shift):
     check_grad(rows, cols, dt, w, ld % 2 == 1, f"{dt}", ld, shift)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("size", [1e14, 1e-14])
+@pytest.mark.parametrize("cols", [300, 3001, 9000])
+def test_grad_of_extreme_rows(dt, size, cols):
+    """rstd^3 alone is outside fp32's range; the gradient is not."""
+    print(f"rmsnorm grad extreme {dt} {size} {cols}", flush=True)
+    dy, h, w = R.rand((3, cols), 1e-2, dt, 53), R.rand((3, cols), size, dt, 54), R.rand((cols,), 1.0, BF, 55)
+    rstd = (1 / torch.sqrt(h.double().square().mean(1))).float()
+    dx, dw = fp8mi.fp8_rmsnorm_grad(dy.to(DEV), h.to(DEV), w.to(DEV), rstd.to(DEV))
+    torch.cuda.synchronize()
+    dx64, dw64, mag, wmag = R.rmsnorm_grad(dy, h, w, rstd, None)
+    rel = (min(cols, 32) + 30) * R.F32_ULP  # as check_grad
+    R.assert_close(dx.cpu(), dx64, R.half_ulp(dx64, dt) + rel * mag, "dx")
+    R.assert_close(dw.cpu(), dw64, 14 * R.F32_ULP * wmag, "dweight")
+
+
 def test_grad_in_place_and_repeatable():
     rows, cols = 2300, 1535
     dy, h = R.rand((rows, cols), 1.0, BF, 46).to(DEV), R.rand((rows, cols), 1.0, BF, 47).to(DEV)
