@@ -10,6 +10,10 @@
 // element.  The tile (tile.h) is the dual quantize's; each thread computes its
 // 4 x 8 values in registers, publishes the workgroup's amax before it encodes
 // them, stores the row codes directly and the transposed ones through LDS.
+// Stores are non-temporal (8192 x 6912 with the bias gradient 88.0 -> 81.8 us
+// over three sets of buffers in turn), the gated form's row codes excepted: they
+// gain nothing by it (68.9 against 68.7 us) and the products that follow lose (a
+// gated block's step at 8192 x 1536 x 6912 1062 -> 1080 us).
 #include "activation.h"
 #include "fp8mi_internal.h"
 #include "tile.h"
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) act_grad_kernel(ActGradArgs p
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + 4 * rg + i;
-    if (r < p.rows && n > 0) store_codes8(p.out_row + r * p.ld_row + cc, rw[i][0], rw[i][1], n);
+    if (r < p.rows && n > 0) store_codes8<!GATED>(p.out_row + r * p.ld_row + cc, rw[i][0], rw[i][1], n);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) act_grad_kernel(ActGradArgs p
       uint8_t* dst = p.out_t + c * p.ld_t + rr;
       if (rr + 16 <= p.rows) {
         const u32x4_byte w = {v.x, v.y, v.z, v.w};
-        *reinterpret_cast<u32x4_byte*>(dst) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_byte*>(dst));
       } else {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
