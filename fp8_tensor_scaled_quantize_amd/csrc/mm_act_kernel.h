@@ -449,6 +449,12 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
     }
     __builtin_amdgcn_sched_barrier(0);  // all in flight before anything waits
   };
+  // the residual's lines are on their way to the L2 before the weights' loads:
+  // otherwise the epilogue waits for HBM once more
+  uint32_t warm = 0u;
+  if (p.res && wid < TI && g == 0 && 16 * wid + r16 < p.M)
+    warm = static_cast<const uint8_t*>(p.res)[((16 * wid + r16) * p.ld_res + n0 / (GATED ? 2 : 1)) *
+                                              (p.res_dt == kF32 ? 4 : 2)];
   load(wid);
   // bias and column scales: read behind the first steps' loads, parked after the K loop
   const int64_t pc = n0 + (lane & 15);
@@ -471,6 +477,7 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
     col_s[tid] = col_scale;
   }
   const float s_c = act_out_scale<OUT>(p);
+  asm volatile("" ::"v"(warm));
   __syncthreads();
   float amax = 0.0f;
   const int64_t row0 = 16 * wid;
