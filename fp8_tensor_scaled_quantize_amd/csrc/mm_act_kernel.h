@@ -352,7 +352,7 @@ __device__ __forceinline__ void act_finish(const MmActArgs& p, float amax, float
       }
       if (threadIdx.x == 0) publish_max(reinterpret_cast<uint32_t*>(p.c_amax_out), bmax);
     }
-    if (threadIdx.x == 0 && p.c_scale_inv_out && blockIdx.x == 0) *p.c_scale_inv_out = 1.0f / s_c;
+    if (threadIdx.x == 0 && p.c_scale_inv_out && blockIdx.x + blockIdx.y == 0) *p.c_scale_inv_out = 1.0f / s_c;
   }
 }
 
@@ -395,7 +395,7 @@ static hipError_t launch_act_tile(const P& p0, hipStream_t st) {
 
 // ===========================================================================
 // Few rows (serving): bound by reading the weights once.  A workgroup takes 16
-// weight rows and all of A's (at most 16 TI), its NW waves every NW-th K step
+// weight rows and 16 TI rows of A, its NW waves every NW-th K step
 // of 128; fragments come straight from global memory into registers, U steps in
 // flight per wave, no LDS and no barrier before the end.  Lane group g of a
 // fragment takes k = 16 g .. + 15 and 64 + 16 g .. + 15 of the step instead of
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
   __shared__ float red[NW + 1];
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16 * TI;
   // raw buffers: rows past an edge and chunks past K read as zero
   const int ext_a = (int)p.a_extent_from(0), ext_b = (int)p.b_extent_from(n0);
   const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a), 0, ext_a, 0x00020000);
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
   const uint32_t ob = (uint32_t)r16 * (uint32_t)p.ldb + 16 * g;
   uint32_t oa[TI];  // a row past M - 1 starts at or beyond the extent
 #pragma unroll
-  for (int i = 0; i < TI; ++i) oa[i] = 16 * i + r16 < p.M ? (uint32_t)(16 * i + r16) * (uint32_t)p.lda + 16 * g : (uint32_t)ext_a;
+  for (int i = 0; i < TI; ++i) oa[i] = m0 + 16 * i + r16 < p.M ? (uint32_t)(m0 + 16 * i + r16) * (uint32_t)p.lda + 16 * g : (uint32_t)ext_a;
   const bool b_in = n0 + r16 < p.N;
   auto frag = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, int ext, int kt) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
   // the residual's lines are on their way to the L2 before the weights' loads:
   // otherwise the epilogue waits for HBM once more
   uint32_t warm = 0u;
-  if (p.res && wid < TI && g == 0 && 16 * wid + r16 < p.M)
-    warm = static_cast<const uint8_t*>(p.res)[((16 * wid + r16) * p.ld_res + n0 / (GATED ? 2 : 1)) *
+  if (p.res && wid < TI && g == 0 && m0 + 16 * wid + r16 < p.M)
+    warm = static_cast<const uint8_t*>(p.res)[((m0 + 16 * wid + r16) * p.ld_res + n0 / (GATED ? 2 : 1)) *
                                               (p.res_dt == kF32 ? 4 : 2)];
   load(wid);
   // bias and column scales: read behind the first steps' loads, parked after the K loop
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
   asm volatile("" ::"v"(warm));
   __syncthreads();
   float amax = 0.0f;
-  const int64_t row0 = 16 * wid;
+  const int64_t row0 = m0 + 16 * wid;
   if (wid < TI && row0 < p.M) {
     v4f sum[1][1];
     const float4 f = part[0][wid][lane];
@@ -497,21 +497,33 @@ __global__ void __launch_bounds__(64 * NW) mm_act_rows(MmActArgs p) {
   act_finish<OUT, NT>(p, amax, s_c, red);
 }
 
+// Blocks of 16 rows by 16 columns, a workgroup each, while every one has a CU of
+// its own: each then reads 16 rows of either operand.  Graph replay over twelve
+// sets of buffers, 32-row blocks or tiles -> this (us): 24 x 1536 x 6912 11.8 ->
+// 9.8, 32 x 1536 x 6912 12.9 -> 9.8, 48 x 1024 x 6912 16.3 -> 9.8, 64 x 1024 x
+// 4096 11.7 -> 8.0, 64 x 512 x 512 5.6 -> 3.7, 40 x 512 x 8192 18.4 -> 10.4,
+// 256 x 256 x 4096 11.7 -> 7.9, 4096 x 16 x 512 5.4 -> 3.7.
+// With two workgroups per CU the others win: 32 x 3584 x 2048 7.0 against 8.1,
+// 48 x 1536 x 6912 16.4 against 16.7.
+static inline bool act_row_blocks(const MmActArgs& p) {
+  return (p.N + 15) / 16 * ((p.M + 15) / 16) <= device_cu_count();
+}
 template <int OUT, bool GATED, int TI> static hipError_t launch_act_rows_ti(const MmActArgs& p, hipStream_t st) {
-  const unsigned wgs = (unsigned)((p.N + 15) / 16);
+  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)((p.M + 16 * TI - 1) / (16 * TI)));
+  const int64_t wgs = (int64_t)grid.x * grid.y;
   // waves per workgroup: enough of them over the chip, no more than K steps
   const int64_t steps = (p.K + kBK - 1) / kBK;
-  if (wgs >= 768 || steps <= 8) hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 4>), dim3(wgs), dim3(256), 0, st, p);
-  else if (wgs >= 384 || steps <= 16) hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 8>), dim3(wgs), dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 16>), dim3(wgs), dim3(1024), 0, st, p);
+  if (wgs >= 768 || steps <= 8) hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 4>), grid, dim3(256), 0, st, p);
+  else if (wgs >= 384 || steps <= 16) hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 8>), grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((mm_act_rows<OUT, GATED, TI, 16>), grid, dim3(1024), 0, st, p);
   return hipGetLastError();
 }
 template <int OUT, bool GATED> static hipError_t launch_act_rows(const MmActArgs& p, hipStream_t st) {
-  return p.M <= 16 ? launch_act_rows_ti<OUT, GATED, 1>(p, st) : launch_act_rows_ti<OUT, GATED, 2>(p, st);
+  return p.M <= 16 || act_row_blocks(p) ? launch_act_rows_ti<OUT, GATED, 1>(p, st) : launch_act_rows_ti<OUT, GATED, 2>(p, st);
 }
-// Every workgroup reads all of A, which the tiles share through LDS: taken for
+// Every column of workgroups reads all of A, which the tiles share through LDS: taken for
 // at most 8 rows, for 16 while the weights are small, for 32 while there is
-// at most one workgroup per CU.  Graph replay, tiles -> this (us): 1 x 13824 x
+// at most one workgroup per CU, beyond that in blocks (act_row_blocks).  Graph replay, tiles -> this (us): 1 x 13824 x
 // 1536 9.6 -> 7.5, 8 x 4096 x 4096 11.4 -> 7.7, 16 x 1536 x 6912 16.0 -> 9.6,
 // 32 x 1536 x 6912 16.1 -> 12.8, 32 x 4096 x 4096 11.4 -> 10.8; and where the
 // tiles stay: 16 x 28672 x 8192 50 against 59, 32 x 8192 x 2048 8.3 against
@@ -519,7 +531,7 @@ template <int OUT, bool GATED> static hipError_t launch_act_rows(const MmActArgs
 static inline bool act_few_rows(const MmActArgs& p) {
   if (p.M <= 8) return true;
   if (p.M <= 16) return p.N * p.K <= (int64_t)32 << 20;
-  return p.M <= 32 && p.N <= 16 * (int64_t)device_cu_count();
+  return (p.M <= 32 && p.N <= 16 * (int64_t)device_cu_count()) || act_row_blocks(p);
 }
 
 // The plain GEMM's tile (pick_tile) for small problems; for large ones 256 x

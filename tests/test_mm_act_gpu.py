@@ -125,6 +125,14 @@ def test_shapes(M, N, K, gated, out_fmt):
         keep_z=True, row_scales=True, ring=M % 2 == 0, tag="shapes")
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 512, 2048), (40, 516, 1040), (64, 1008, 528), (33, 30, 6912), (130, 250, 528),
+                                   (250, 256, 1024), (4001, 10, 272)])
+@pytest.mark.parametrize("gated,out_fmt", [(False, None), (True, 0), (False, 0)])
+def test_row_blocks(M, N, K, gated, out_fmt):
+    """16 x 16 blocks, a workgroup each: few rows and columns, ragged edges."""
+    run(M, N, K, "silu", gated, out_fmt, res_dt=BF, bias_dt=F32, keep_z=True, row_scales=True, ring=M % 2 == 0, tag="blocks")
+
+
 # the big tiles of the dispatch: 256 x 192, 256 x 256, the mixed grid; ragged edges
 BIG = [(4096, 2560, 272), (4090, 3586, 288), (8190, 6910, 272)]
 
