@@ -525,7 +525,7 @@ template <int OUT, bool GATED> static hipError_t launch_act_rows(const MmActArgs
 // at most 8 rows, for 16 while the weights are small, for 32 while there is
 // at most one workgroup per CU, beyond that in blocks (act_row_blocks).  Graph replay, tiles -> this (us): 1 x 13824 x
 // 1536 9.6 -> 7.5, 8 x 4096 x 4096 11.4 -> 7.7, 16 x 1536 x 6912 16.0 -> 9.6,
-// 32 x 1536 x 6912 16.1 -> 12.8, 32 x 4096 x 4096 11.4 -> 10.8; and where the
+// 32 x 4096 x 4096 11.4 -> 10.8; and where the
 // tiles stay: 16 x 28672 x 8192 50 against 59, 32 x 8192 x 2048 8.3 against
 // 10.6, 64 x 1536 x 6912 16.2 against 19.6.
 static inline bool act_few_rows(const MmActArgs& p) {
