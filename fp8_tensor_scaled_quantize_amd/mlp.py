@@ -50,6 +50,8 @@ class Fp8Mlp:
         self.rings = {k: new_ring(hist_len, 1.0, dev) for k in ("n", "w_up", "u", "w_down", "g", "z")}
         self.scale_inv = {k: torch.empty(1, dtype=torch.float32, device=dev) for k in self.rings}
         self._frozen = None
+        # decode's multiplier of u: scale_inv holds a pending backward's
+        self._u_inv = torch.empty(1, dtype=torch.float32, device=dev)
         self._saved = None
         self._forwards = 0
 
@@ -125,8 +127,8 @@ class Fp8Mlp:
                          scale_inv_out=row_inv, sum_out=residual)
         scale = self.rings["u"].view(torch.float32)[self.hist_len:self.hist_len + 1]  # the ring's current scale
         uq = fp8_mm_act(nq, wu, row_inv, s_wu, self.b_up, self.act, self.gated, out_fmt=E4M3, out_scale=scale,
-                        out_scale_inv=self.scale_inv["u"])
-        return fp8_mm_act(uq, wd, self.scale_inv["u"], s_wd, self.b_down, residual=residual, out=residual)
+                        out_scale_inv=self._u_inv)
+        return fp8_mm_act(uq, wd, self._u_inv, s_wd, self.b_down, residual=residual, out=residual)
 
 
 class _Fp8MlpFn(torch.autograd.Function):
