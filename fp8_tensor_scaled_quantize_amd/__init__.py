@@ -554,6 +554,10 @@ def _typed_vector(t: torch.Tensor, n: int, name: str, dtypes=_DT) -> int:
     return dt
 
 
+# autograd's record that a tensor was changed in place: the operators below bump
+# it where an output is one of their inputs, as torch's in-place operations do
+_changed_in_place = torch.autograd.graph.increment_version
+
 _F32_ONLY, _BF16_ONLY = {torch.float32: F32}, {torch.bfloat16: BF16}
 
 
@@ -595,15 +599,18 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, fmt=E4M3, eps: flo
         _typed_vector(rstd_out, rows, "rstd_out", _F32_ONLY)
     rp, h = (None, 0) if ring is None else _ring_args(ring)
     _on_device(x, weight, residual, out, scale, ring, scale_inv_out, amax_out, sum_out, rstd_out)
+    px, pr = x.data_ptr(), None if residual is None else residual.data_ptr()
+    ps = None if sum_out is None else sum_out.data_ptr()
     status = lib().fp8_rmsnorm(
-        x.data_ptr(), dt, rows, cols, ld_x, None if residual is None else residual.data_ptr(), ld_res,
+        px, dt, rows, cols, ld_x, pr, ld_res,
         None if weight is None else weight.data_ptr(), wdt, ctypes.byref(ctypes.c_float(eps)), _fmt(fmt),
         out.data_ptr(), ld_out, 1 if row_scaled else 0, None if scale is None else scale.data_ptr(), rp, h,
         None if scale_inv_out is None else scale_inv_out.data_ptr(), None if amax_out is None else amax_out.data_ptr(),
-        None if sum_out is None else sum_out.data_ptr(), ld_sum, None if rstd_out is None else rstd_out.data_ptr(),
-        _stream(x))
+        ps, ld_sum, None if rstd_out is None else rstd_out.data_ptr(), _stream(x))
     if status:
         _check(status)
+    if ps and (ps == pr or ps == px):
+        _changed_in_place(sum_out)
     return out
 
 
@@ -640,13 +647,16 @@ def fp8_rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | N
                                     device=dy.device)
         nbytes = workspace.numel() * workspace.element_size()
     _on_device(dy, h, weight, rstd, dsum, dx, dweight, workspace)
+    py, ph, pd, pg = dy.data_ptr(), h.data_ptr(), None if dsum is None else dsum.data_ptr(), dx.data_ptr()
     status = lib().fp8_rmsnorm_grad(
-        dy.data_ptr(), dt, rows, cols, ld_dy, h.data_ptr(), ld_h, None if weight is None else weight.data_ptr(), wdt,
-        rstd.data_ptr(), None if dsum is None else dsum.data_ptr(), ld_ds, dx.data_ptr(), ld_dx,
+        py, dt, rows, cols, ld_dy, ph, ld_h, None if weight is None else weight.data_ptr(), wdt, rstd.data_ptr(), pd,
+        ld_ds, pg, ld_dx,
         None if dweight is None else dweight.data_ptr(), None if workspace is None else workspace.data_ptr(), nbytes,
         _stream(dy))
     if status:
         _check(status)
+    if pg and (pg == pd or pg == py or pg == ph):
+        _changed_in_place(dx)
     return dx, dweight
 
 
@@ -725,16 +735,19 @@ def fp8_mm_act(a: torch.Tensor, b: torch.Tensor, a_scale_inv: torch.Tensor | Non
         ld_z = _ld(z_out, (M, N), torch.bfloat16, "z_out")
     rp, h = (None, 0) if out_ring is None else _ring_args(out_ring)
     _on_device(a, b, a_scale_inv, b_scale_inv, bias, residual, z_out, out, out_scale, out_ring, out_scale_inv, out_amax)
+    pr, pc = None if residual is None else residual.data_ptr(), out.data_ptr()
     status = lib().fp8_mm_act(
         a.data_ptr(), lda, b.data_ptr(), ldb, M, N, K, None if a_scale_inv is None else a_scale_inv.data_ptr(),
         None if b_scale_inv is None else b_scale_inv.data_ptr(), rows, None if bias is None else bias.data_ptr(),
-        bias_dt, code, None if residual is None else residual.data_ptr(), res_dt, ld_res,
-        None if z_out is None else z_out.data_ptr(), ld_z, out.data_ptr(), FP8_E4M3 if fp8_out else BF16, ldc,
+        bias_dt, code, pr, res_dt, ld_res, None if z_out is None else z_out.data_ptr(), ld_z, pc,
+        FP8_E4M3 if fp8_out else BF16, ldc,
         None if out_scale is None else out_scale.data_ptr(), rp, h,
         None if out_scale_inv is None else out_scale_inv.data_ptr(), None if out_amax is None else out_amax.data_ptr(),
         _stream(a))
     if status:
         _check(status)
+    if pc and pc == pr:
+        _changed_in_place(out)
     return out
 
 

@@ -30,6 +30,11 @@ from . import (E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_qua
                fp8_quantize_dual_bias_grad, fp8_quantize_dynamic, fp8_rmsnorm, fp8_rmsnorm_grad, new_ring)
 
 
+def _version(t: torch.Tensor):
+    """t's count of in-place changes (inference tensors keep none)."""
+    return None if t.is_inference() else t._version
+
+
 class Fp8Mlp:
     """norm_weight [d]; w_up [F, d], or [2F, d] with interleaved rows when
     gated (interleave_gated); w_down [d, F]; biases optional."""
@@ -75,16 +80,25 @@ class Fp8Mlp:
         uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z, out_fmt=E4M3,
                         out_ring=self.rings["u"], out_scale_inv=s["u"])
         y = fp8_mm_act(uq, wd, s["u"], s["w_down"], self.b_down, residual=h)
-        self._saved = (nq, h, rstd, z, uq, wu_t, wd_t, x.shape) if save_for_backward else None
+        # the norm's weight is not a copy, and h is x itself without a residual:
+        # backward, which reads both again, checks their versions
+        nw = self.norm_weight
+        self._saved = ((nq, h, rstd, z, uq, wu_t, wd_t, x.shape, nw, _version(h), _version(nw))
+                       if save_for_backward else None)
         self._forwards += 1 if save_for_backward else 0
         return y.reshape(x.shape)
 
     def backward(self, dy: torch.Tensor) -> dict:
         """Gradients of the latest saved forward: dx (x's and the residual's),
-        norm_weight, w_up, w_down, b_up, b_down."""
+        norm_weight, w_up, w_down, b_up, b_down.  The norm's weight, and x of a
+        forward without a residual, must not have been changed in place since."""
         if self._saved is None:
             raise RuntimeError("backward needs a forward with save_for_backward=True")
-        nq, h, rstd, z, uq, wu_t, wd_t, x_shape = self._saved
+        nq, h, rstd, z, uq, wu_t, wd_t, x_shape, nw, h_version, nw_version = self._saved
+        if _version(h) != h_version:
+            raise RuntimeError("backward reads x again, which was changed in place since the forward pass")
+        if _version(nw) != nw_version:
+            raise RuntimeError("backward reads norm_weight again, which was changed in place since the forward pass")
         s, r = self.scale_inv, self.rings
         dy2 = dy.reshape(h.shape)
         db_down = None
@@ -98,7 +112,7 @@ class Fp8Mlp:
         dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
         dw_down = fp8_mm(gq_t, uq.t(), E5M2, E4M3, s["g"], s["u"])
         dw_up = fp8_mm(zq_t, nq.t(), E5M2, E4M3, s["z"], s["n"])
-        dx, dnw = fp8_rmsnorm_grad(dn, h, self.norm_weight, rstd, dsum=dy2)
+        dx, dnw = fp8_rmsnorm_grad(dn, h, nw, rstd, dsum=dy2)
         return {"x": dx.reshape(x_shape), "norm_weight": dnw, "w_up": dw_up, "w_down": dw_down, "b_up": db_up,
                 "b_down": db_down}
 

@@ -14,7 +14,7 @@ from tests.test_mlp_gpu import BF, G_BOUND, Y_BOUND, make, off, reference
 
 pytestmark = pytest.mark.gpu
 fp8mi = pytest.importorskip("fp8_tensor_scaled_quantize_amd")
-from fp8_tensor_scaled_quantize_amd.mlp import Fp8Mlp  # noqa: E402
+from fp8_tensor_scaled_quantize_amd.mlp import Fp8Mlp, fp8_mlp  # noqa: E402
 
 
 def batch(rows, d, seed, sigma=1.0):
@@ -40,3 +40,55 @@ def test_decode_between_forward_and_backward(act, gated):
         a.forward(x), b.forward(x)
         a.decode(tok, tok.clone())
         same(a.backward(dy), b.backward(dy))
+
+
+@pytest.mark.parametrize("what", ["x", "norm_weight"])
+@pytest.mark.parametrize("tape", [False, True])
+def test_in_place_change_before_backward(what, tape):
+    """What backward reads again must be as forward saw it."""
+    _, dev, block = make(128, 256, "gelu", False, False)
+    x, dy = batch(32, 128, 4), batch(32, 128, 5)
+    if tape:
+        leaf = x.clone().requires_grad_()
+        x = leaf * 1  # a stream that its owner may update
+        y = fp8_mlp(x, block)
+    else:
+        y = block.forward(x)
+    with torch.no_grad():
+        (x if what == "x" else dev[0]).add_(0.25)
+    with pytest.raises(RuntimeError, match="changed in place"):
+        y.backward(dy) if tape else block.backward(dy)
+
+
+@pytest.mark.parametrize("how", ["decode", "rmsnorm", "mm_act", "rmsnorm_grad"])
+def test_in_place_change_by_the_library(how):
+    """The library's own in-place forms count as changes too."""
+    d = 128
+    _, dev, block = make(d, 256, "gelu", False, False)
+    x, other, dy = batch(32, d, 6), batch(32, d, 7), batch(32, d, 8)
+    block.freeze()
+    block.forward(x)
+    one = torch.ones(1, device=DEV)
+    if how == "decode":
+        block.decode(other, x)
+    elif how == "rmsnorm":
+        fp8mi.fp8_rmsnorm(other, None, residual=x, scale=one, sum_out=x.view(32, d))
+    elif how == "mm_act":
+        a, b = torch.zeros(32, 64, dtype=torch.uint8, device=DEV), torch.zeros(d, 64, dtype=torch.uint8, device=DEV)
+        fp8mi.fp8_mm_act(a, b, residual=x, out=x)
+    else:
+        fp8mi.fp8_rmsnorm_grad(other, dy, None, torch.ones(32, device=DEV), dsum=x, dx=x, need_dweight=False)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="changed in place"):
+        block.backward(dy)
+
+
+def test_residual_sum_is_the_blocks_own():
+    """With a residual the saved sum is the block's: x and residual may go."""
+    _, _, a = make(128, 256, "gelu", False, False)
+    _, _, b = make(128, 256, "gelu", False, False)
+    x, r, dy = batch(32, 128, 9), batch(32, 128, 10), batch(32, 128, 11, 1e-2)
+    a.forward(x.clone(), r.clone())
+    b.forward(x, r)
+    x.zero_(), r.zero_()
+    same(b.backward(dy), a.backward(dy))
