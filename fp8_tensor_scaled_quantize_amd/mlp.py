@@ -15,7 +15,8 @@ amax-history ring, as Fp8Linear's have; a step has no host synchronisation.
     dU  = dY W_down                                  fp8_mm
     dZ  -> E5M2 codes in both layouts, db_up         fp8_act_grad (from dU, pre-activations)
     dN  = dZ W_up                                    fp8_mm
-    dW_down = dY^T U, dW_up = dZ^T N                 fp8_mm (U, N read K-major)
+    dW_down = dY^T U, dW_up = dZ^T N                 fp8_mm (U, N read K-major; any
+        token count: zero codes up to a multiple of 16)
     dX  = gradient of the norm + dY, dnorm_weight    fp8_rmsnorm_grad
 
 decode (serving): weights quantized once by freeze(), the norm's codes with one
@@ -33,6 +34,24 @@ from . import (E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_qua
 def _version(t: torch.Tensor):
     """t's count of in-place changes (inference tensors keep none)."""
     return None if t.is_inference() else t._version
+
+
+# The weight gradients sum over tokens, and a product's K is a multiple of 16:
+# codes that they read have that many tokens, the last ones zero.
+def _token_rows(rows: int, cols: int, dev) -> torch.Tensor:
+    """Storage of codes [rows, cols], zero rows up to a multiple of 16."""
+    buf = torch.empty(-(-rows // 16) * 16, cols, dtype=torch.uint8, device=dev)
+    if rows % 16:
+        buf[rows:].zero_()
+    return buf
+
+
+def _token_cols(cols: int, rows: int, dev) -> torch.Tensor:
+    """Storage of transposed codes [cols, rows], zero columns up to a multiple of 16."""
+    buf = torch.empty(cols, -(-rows // 16) * 16, dtype=torch.uint8, device=dev)
+    if rows % 16:
+        buf[:, rows:].zero_()
+    return buf
 
 
 class Fp8Mlp:
@@ -72,18 +91,22 @@ class Fp8Mlp:
         rows, dev, s = x2.shape[0], x.device, self.scale_inv
         h = x2 if r2 is None else torch.empty_like(x2)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2, ring=self.rings["n"],
-                         scale_inv_out=s["n"], sum_out=None if r2 is None else h, rstd_out=rstd)
+        n_buf = _token_rows(rows, d, dev) if save_for_backward else None
+        nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2,
+                         out=None if n_buf is None else n_buf[:rows], ring=self.rings["n"], scale_inv_out=s["n"],
+                         sum_out=None if r2 is None else h, rstd_out=rstd)
         wu, wu_t = self._weight("w_up", self.w_up)
         wd, wd_t = self._weight("w_down", self.w_down)
         z = torch.empty(rows, self.w_up.shape[0], dtype=torch.bfloat16, device=dev) if save_for_backward else None
-        uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z, out_fmt=E4M3,
-                        out_ring=self.rings["u"], out_scale_inv=s["u"])
+        u_buf = _token_rows(rows, self.w_down.shape[1], dev) if save_for_backward else None
+        uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z,
+                        out=None if u_buf is None else u_buf[:rows], out_fmt=E4M3, out_ring=self.rings["u"],
+                        out_scale_inv=s["u"])
         y = fp8_mm_act(uq, wd, s["u"], s["w_down"], self.b_down, residual=h)
         # the norm's weight is not a copy, and h is x itself without a residual:
         # backward, which reads both again, checks their versions
         nw = self.norm_weight
-        self._saved = ((nq, h, rstd, z, uq, wu_t, wd_t, x.shape, nw, _version(h), _version(nw))
+        self._saved = ((n_buf, h, rstd, z, u_buf, wu_t, wd_t, x.shape, nw, _version(h), _version(nw))
                        if save_for_backward else None)
         self._forwards += 1 if save_for_backward else 0
         return y.reshape(x.shape)
@@ -94,24 +117,27 @@ class Fp8Mlp:
         forward without a residual, must not have been changed in place since."""
         if self._saved is None:
             raise RuntimeError("backward needs a forward with save_for_backward=True")
-        nq, h, rstd, z, uq, wu_t, wd_t, x_shape, nw, h_version, nw_version = self._saved
+        n_buf, h, rstd, z, u_buf, wu_t, wd_t, x_shape, nw, h_version, nw_version = self._saved
         if _version(h) != h_version:
             raise RuntimeError("backward reads x again, which was changed in place since the forward pass")
         if _version(nw) != nw_version:
             raise RuntimeError("backward reads norm_weight again, which was changed in place since the forward pass")
         s, r = self.scale_inv, self.rings
         dy2 = dy.reshape(h.shape)
+        rows, d = h.shape
+        g_t, z_t = _token_cols(d, rows, h.device), _token_cols(z.shape[1], rows, h.device)
         db_down = None
         if self.b_down is not None:
-            gq, gq_t, db_down = fp8_quantize_dual_bias_grad(dy2, E5M2, ring=r["g"], scale_inv_out=s["g"])
+            gq, _, db_down = fp8_quantize_dual_bias_grad(dy2, E5M2, out_t=g_t[:, :rows], ring=r["g"],
+                                                         scale_inv_out=s["g"])
         else:
-            gq, gq_t = fp8_quantize_dual(dy2, E5M2, ring=r["g"], scale_inv_out=s["g"])
+            gq, _ = fp8_quantize_dual(dy2, E5M2, out_t=g_t[:, :rows], ring=r["g"], scale_inv_out=s["g"])
         du = fp8_mm(gq, wd_t, E5M2, E4M3, s["g"], s["w_down"])
-        zq, zq_t, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, ring=r["z"], scale_inv_out=s["z"],
-                                       need_bias_grad=self.b_up is not None)
+        zq, _, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, out_t=z_t[:, :rows], ring=r["z"],
+                                    scale_inv_out=s["z"], need_bias_grad=self.b_up is not None)
         dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
-        dw_down = fp8_mm(gq_t, uq.t(), E5M2, E4M3, s["g"], s["u"])
-        dw_up = fp8_mm(zq_t, nq.t(), E5M2, E4M3, s["z"], s["n"])
+        dw_down = fp8_mm(g_t, u_buf.t(), E5M2, E4M3, s["g"], s["u"])
+        dw_up = fp8_mm(z_t, n_buf.t(), E5M2, E4M3, s["z"], s["n"])
         dx, dnw = fp8_rmsnorm_grad(dn, h, nw, rstd, dsum=dy2)
         return {"x": dx.reshape(x_shape), "norm_weight": dnw, "w_up": dw_up, "w_down": dw_down, "b_up": db_up,
                 "b_down": db_down}

@@ -92,3 +92,33 @@ def test_residual_sum_is_the_blocks_own():
     b.forward(x, r)
     x.zero_(), r.zero_()
     same(b.backward(dy), a.backward(dy))
+
+
+@pytest.mark.parametrize("tokens", [0, 1, 7, 40, 250])
+@pytest.mark.parametrize("act,gated,bias", [("gelu", False, True), ("silu", True, False)])
+def test_any_token_count(tokens, act, gated, bias):
+    d, f = 256, 512
+    cpu, dev, block = make(d, f, act, gated, bias)
+    x, res, dy = R.rand((tokens, d), 1.0, BF, 12), R.rand((tokens, d), 1.0, BF, 13), R.rand((tokens, d), 1e-2, BF, 14)
+    xd, rd = x.to(DEV).requires_grad_(), res.to(DEV).requires_grad_()
+    for t in dev:
+        if t is not None:
+            t.requires_grad_()
+    print(f"mlp tokens {tokens} {act} gated={gated}", flush=True)
+    for step in range(2):  # the first step fills the rings
+        for t in (xd, rd, *dev):
+            if t is not None:
+                t.grad = None
+        y = fp8_mlp(xd, block, rd)
+        y.backward(dy.to(DEV))
+    torch.cuda.synchronize()
+    want, h, leaves = reference(cpu, x, res, act, gated)
+    want.backward(dy.double())
+    if tokens == 0:
+        assert xd.grad.shape == (0, d) and all(t is None or not t.grad.any() for t in dev)
+        return
+    assert off(y - (xd + rd), want - h) < Y_BOUND
+    assert off(xd.grad, leaves[0].grad) < G_BOUND and torch.equal(xd.grad, rd.grad)
+    for got, ref in zip(dev, leaves[1:]):
+        if got is not None:
+            assert off(got.grad, ref.grad) < G_BOUND, tuple(got.shape)
