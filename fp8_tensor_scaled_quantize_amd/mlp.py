@@ -84,7 +84,9 @@ class Fp8Mlp:
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, save_for_backward: bool = True):
         """x (and residual) bf16 [..., d] -> the residual stream after the
-        block, bf16 [..., d]."""
+        block, bf16 [..., d].  Without save_for_backward also of fp16 or fp32."""
+        if save_for_backward and x.dtype is not torch.bfloat16:
+            raise ValueError(f"a forward that is saved for backward takes bfloat16, got {x.dtype}")
         d = self.norm_weight.shape[0]
         x2 = x.reshape(-1, d)
         r2 = None if residual is None else residual.reshape(-1, d)
@@ -118,6 +120,8 @@ class Fp8Mlp:
         if self._saved is None:
             raise RuntimeError("backward needs a forward with save_for_backward=True")
         n_buf, h, rstd, z, u_buf, wu_t, wd_t, x_shape, nw, h_version, nw_version = self._saved
+        if dy.dtype is not torch.bfloat16 or dy.shape[-1:] != x_shape[-1:] or dy.numel() != h.numel():
+            raise ValueError(f"dy must be bfloat16 {tuple(x_shape)} like the output, got {dy.dtype} {tuple(dy.shape)}")
         if _version(h) != h_version:
             raise RuntimeError("backward reads x again, which was changed in place since the forward pass")
         if _version(nw) != nw_version:

@@ -122,3 +122,26 @@ def test_any_token_count(tokens, act, gated, bias):
     for got, ref in zip(dev, leaves[1:]):
         if got is not None:
             assert off(got.grad, ref.grad) < G_BOUND, tuple(got.shape)
+
+
+def test_training_refusals_come_first():
+    """What a training step cannot take is refused before a ring has moved."""
+    d = 128
+    _, _, block = make(d, 256, "gelu", False, True)
+    x, dy = batch(16, d, 15), batch(16, d, 16)
+    rings = {k: r.clone() for k, r in block.rings.items()}
+    for t in (x.half(), x.float()):
+        with pytest.raises(ValueError, match="bfloat16"):
+            block.forward(t)
+        with pytest.raises(ValueError, match="bfloat16"):
+            fp8_mlp(t, block)
+    for k, r in block.rings.items():
+        assert torch.equal(r, rings[k]), k
+    y32, y = block.forward(x.float(), save_for_backward=False), block.forward(x)  # inference takes them
+    assert y32.dtype == BF and y32.shape == y.shape
+    rings = {k: r.clone() for k, r in block.rings.items()}
+    for t in (dy.float(), dy.half(), dy[:8], dy.reshape(32, 64)):
+        with pytest.raises(ValueError, match="dy"):
+            block.backward(t)
+    for k, r in block.rings.items():
+        assert torch.equal(r, rings[k]), k
