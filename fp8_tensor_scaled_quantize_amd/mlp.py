@@ -13,7 +13,8 @@ amax-history ring, as Fp8Linear's have; a step has no host synchronisation.
 
     dY  -> E5M2 codes in both layouts, db_down       fp8_quantize_dual_bias_grad
     dU  = dY W_down                                  fp8_mm
-    dZ  -> E5M2 codes in both layouts, db_up         fp8_act_grad (from dU, pre-activations)
+    dZ  -> E5M2 codes in both layouts, db_up         fp8_act_grad (from dU, pre-activations;
+        without activation and gating dZ is dU, quantized as dY is)
     dN  = dZ W_up                                    fp8_mm
     dW_down = dY^T U, dW_up = dZ^T N                 fp8_mm (U, N read K-major; any
         token count: zero codes up to a multiple of 16)
@@ -27,7 +28,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_quantize_dual,
+from . import (ACT_NONE, E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_quantize_dual,
                fp8_quantize_dual_bias_grad, fp8_quantize_dynamic, fp8_rmsnorm, fp8_rmsnorm_grad, new_ring)
 
 
@@ -99,7 +100,9 @@ class Fp8Mlp:
                          sum_out=None if r2 is None else h, rstd_out=rstd)
         wu, wu_t = self._weight("w_up", self.w_up)
         wd, wd_t = self._weight("w_down", self.w_down)
-        z = torch.empty(rows, self.w_up.shape[0], dtype=torch.bfloat16, device=dev) if save_for_backward else None
+        z = None
+        if save_for_backward and (self.gated or self.act not in ("none", None, ACT_NONE)):
+            z = torch.empty(rows, self.w_up.shape[0], dtype=torch.bfloat16, device=dev)
         u_buf = _token_rows(rows, self.w_down.shape[1], dev) if save_for_backward else None
         uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z,
                         out=None if u_buf is None else u_buf[:rows], out_fmt=E4M3, out_ring=self.rings["u"],
@@ -112,6 +115,14 @@ class Fp8Mlp:
                        if save_for_backward else None)
         self._forwards += 1 if save_for_backward else 0
         return y.reshape(x.shape)
+
+    def _gradient(self, name: str, dy: torch.Tensor, out_t: torch.Tensor, bias: bool):
+        """dy's codes in both layouts; returns the row codes and the bias gradient."""
+        ring, inv = self.rings[name], self.scale_inv[name]
+        if bias:
+            codes, _, db = fp8_quantize_dual_bias_grad(dy, E5M2, out_t=out_t, ring=ring, scale_inv_out=inv)
+            return codes, db
+        return fp8_quantize_dual(dy, E5M2, out_t=out_t, ring=ring, scale_inv_out=inv)[0], None
 
     def backward(self, dy: torch.Tensor) -> dict:
         """Gradients of the latest saved forward: dx (x's and the residual's),
@@ -129,16 +140,14 @@ class Fp8Mlp:
         s, r = self.scale_inv, self.rings
         dy2 = dy.reshape(h.shape)
         rows, d = h.shape
-        g_t, z_t = _token_cols(d, rows, h.device), _token_cols(z.shape[1], rows, h.device)
-        db_down = None
-        if self.b_down is not None:
-            gq, _, db_down = fp8_quantize_dual_bias_grad(dy2, E5M2, out_t=g_t[:, :rows], ring=r["g"],
-                                                         scale_inv_out=s["g"])
-        else:
-            gq, _ = fp8_quantize_dual(dy2, E5M2, out_t=g_t[:, :rows], ring=r["g"], scale_inv_out=s["g"])
+        g_t, z_t = _token_cols(d, rows, h.device), _token_cols(self.w_up.shape[0], rows, h.device)
+        gq, db_down = self._gradient("g", dy2, g_t[:, :rows], self.b_down is not None)
         du = fp8_mm(gq, wd_t, E5M2, E4M3, s["g"], s["w_down"])
-        zq, _, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, out_t=z_t[:, :rows], ring=r["z"],
-                                    scale_inv_out=s["z"], need_bias_grad=self.b_up is not None)
+        if z is None:  # no activation
+            zq, db_up = self._gradient("z", du, z_t[:, :rows], self.b_up is not None)
+        else:
+            zq, _, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, out_t=z_t[:, :rows], ring=r["z"],
+                                        scale_inv_out=s["z"], need_bias_grad=self.b_up is not None)
         dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
         dw_down = fp8_mm(g_t, u_buf.t(), E5M2, E4M3, s["g"], s["u"])
         dw_up = fp8_mm(z_t, n_buf.t(), E5M2, E4M3, s["z"], s["n"])

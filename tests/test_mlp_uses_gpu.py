@@ -145,3 +145,21 @@ def test_training_refusals_come_first():
             block.backward(t)
     for k, r in block.rings.items():
         assert torch.equal(r, rings[k]), k
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_linear_pair_without_activation(bias):
+    """act="none" without gating trains as well: dz is dy."""
+    d, f = 256, 512
+    cpu, dev, block = make(d, f, "none", False, bias)
+    x, dy = R.rand((48, d), 1.0, BF, 17), R.rand((48, d), 1e-2, BF, 18)
+    for step in range(2):
+        y = block.forward(x.to(DEV))
+        got = block.backward(dy.to(DEV))
+    torch.cuda.synchronize()
+    want, h, leaves = reference(cpu, x, None, "none", False)
+    want.backward(dy.double())
+    assert off(y - x.to(DEV), want - h) < Y_BOUND
+    for name, leaf in zip(("x", "norm_weight", "w_up", "w_down", "b_up", "b_down"), leaves):
+        if leaf is not None:
+            assert off(got[name], leaf.grad) < G_BOUND, name
