@@ -157,12 +157,14 @@ class Fp8Mlp:
 
     # ------------------------------------------------------------------ serving
     def freeze(self) -> None:
-        """Quantize the weights once for decode (current scaling)."""
-        out = []
-        for w in (self.w_up, self.w_down):
-            si = torch.empty(1, dtype=torch.float32, device=w.device)
-            out.append((fp8_quantize_dynamic(w, E4M3, LAYOUT_ROW, scale_inv_out=si)[0], si))
-        self._frozen = out
+        """Quantize the weights for decode (current scaling).  Called again, it
+        fills the same storage, so that a captured decode has the new weights."""
+        weights = (self.w_up, self.w_down)
+        if self._frozen is None:
+            self._frozen = [(torch.empty(w.shape, dtype=torch.uint8, device=w.device),
+                             torch.empty(1, dtype=torch.float32, device=w.device)) for w in weights]
+        for w, (codes, inv) in zip(weights, self._frozen):
+            fp8_quantize_dynamic(w, E4M3, LAYOUT_ROW, out_row=codes, scale_inv_out=inv)
 
     def calibrate(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Fold one batch's amax into the activation's ring, for decode of a

@@ -163,3 +163,31 @@ def test_linear_pair_without_activation(bias):
     for name, leaf in zip(("x", "norm_weight", "w_up", "w_down", "b_up", "b_down"), leaves):
         if leaf is not None:
             assert off(got[name], leaf.grad) < G_BOUND, name
+
+
+def test_freeze_again_under_a_captured_decode():
+    """New weights, frozen again, reach a decode captured before."""
+    d, f, tokens = 256, 704, 5
+    _, dev, block = make(d, f, "silu", True, False)
+    block.freeze()
+    block.calibrate(batch(64, d, 19))
+    at = [t.data_ptr() for pair in block._frozen for t in pair]
+    x, res = batch(tokens, d, 20), batch(tokens, d, 21)
+    block.decode(x, res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block.decode(x, res)
+    for k in range(3):
+        dev[1].copy_(R.rand(dev[1].shape, (1 + k) * d ** -0.5, BF, 22 + k))
+        dev[2].copy_(R.rand(dev[2].shape, f ** -0.5, BF, 25 + k))
+        block.freeze()
+        assert at == [t.data_ptr() for pair in block._frozen for t in pair]
+        a, b = batch(tokens, d, 28 + k), batch(tokens, d, 31 + k)
+        x.copy_(a), res.copy_(b)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        block.decode(a, b)
+        torch.cuda.synchronize()
+        assert torch.equal(res, b), k
