@@ -160,11 +160,13 @@ class Fp8Mlp:
         """Quantize the weights for decode (current scaling).  Called again, it
         fills the same storage, so that a captured decode has the new weights."""
         weights = (self.w_up, self.w_down)
-        if self._frozen is None:
-            self._frozen = [(torch.empty(w.shape, dtype=torch.uint8, device=w.device),
-                             torch.empty(1, dtype=torch.float32, device=w.device)) for w in weights]
-        for w, (codes, inv) in zip(weights, self._frozen):
+        kept = self._frozen
+        if kept is None:
+            kept = [(torch.empty(w.shape, dtype=torch.uint8, device=w.device),
+                     torch.empty(1, dtype=torch.float32, device=w.device)) for w in weights]
+        for w, (codes, inv) in zip(weights, kept):
             fp8_quantize_dynamic(w, E4M3, LAYOUT_ROW, out_row=codes, scale_inv_out=inv)
+        self._frozen = kept
 
     def calibrate(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Fold one batch's amax into the activation's ring, for decode of a

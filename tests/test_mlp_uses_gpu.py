@@ -191,3 +191,13 @@ def test_freeze_again_under_a_captured_decode():
         block.decode(a, b)
         torch.cuda.synchronize()
         assert torch.equal(res, b), k
+
+
+def test_a_freeze_that_fails_leaves_no_weights():
+    d = 128
+    _, dev, block = make(d, 256, "gelu", False, False)
+    block.w_down = dev[2].double()
+    with pytest.raises(ValueError):
+        block.freeze()
+    with pytest.raises(RuntimeError, match="freeze"):
+        block.decode(batch(3, d, 55), batch(3, d, 56))
