@@ -170,8 +170,23 @@ class Fp8Mlp:
 
     def calibrate(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Fold one batch's amax into the activation's ring, for decode of a
-        block that was not trained here."""
-        self.forward(x, residual, save_for_backward=False)
+        block that was not trained here: the up-projection as decode runs it
+        (the frozen weights where there are some), nothing else touched."""
+        d = self.norm_weight.shape[0]
+        x2 = x.reshape(-1, d)
+        nq, row_inv = self._decode_norm(x2, None if residual is None else residual.reshape(-1, d), None)
+        if self._frozen is None:
+            inv = torch.empty(1, dtype=torch.float32, device=x.device)
+            wu = fp8_quantize_dynamic(self.w_up, E4M3, LAYOUT_ROW, scale_inv_out=inv)[0]
+        else:
+            wu, inv = self._frozen[0]
+        fp8_mm_act(nq, wu, row_inv, inv, self.b_up, self.act, self.gated, out_fmt=E4M3, out_ring=self.rings["u"])
+
+    def _decode_norm(self, x, residual, sum_out):
+        """The norm's codes with one scale per row, and the rows' multipliers."""
+        row_inv = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        return fp8_rmsnorm(x, self.norm_weight, E4M3, self.eps, residual=residual, row_scaled=True,
+                           scale_inv_out=row_inv, sum_out=sum_out), row_inv
 
     def decode(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
         """One serving step on [tokens, d]: adds x to residual and the block's
@@ -179,9 +194,7 @@ class Fp8Mlp:
         if self._frozen is None:
             raise RuntimeError("decode needs freeze()")
         (wu, s_wu), (wd, s_wd) = self._frozen
-        row_inv = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-        nq = fp8_rmsnorm(x, self.norm_weight, E4M3, self.eps, residual=residual, row_scaled=True,
-                         scale_inv_out=row_inv, sum_out=residual)
+        nq, row_inv = self._decode_norm(x, residual, residual)
         scale = self.rings["u"].view(torch.float32)[self.hist_len:self.hist_len + 1]  # the ring's current scale
         uq = fp8_mm_act(nq, wu, row_inv, s_wu, self.b_up, self.act, self.gated, out_fmt=E4M3, out_scale=scale,
                         out_scale_inv=self._u_inv)

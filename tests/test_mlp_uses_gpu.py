@@ -193,6 +193,39 @@ def test_freeze_again_under_a_captured_decode():
         assert torch.equal(res, b), k
 
 
+@pytest.mark.parametrize("frozen", [False, True])
+def test_one_calibration_of_small_weights(frozen):
+    """One calibrate call on weights far below E4M3's range at scale 1, taken
+    back by the down-projection's."""
+    d, f = 512, 1376
+    cpu, dev, block = make(d, f, "silu", True, False)
+    cpu[1], cpu[2] = R.rand((2 * f, d), 1e-4, BF, 34), R.rand((d, f), 1e4, BF, 35)
+    block = Fp8Mlp(dev[0], cpu[1].to(DEV), cpu[2].to(DEV), None, None, "silu", True, 1e-6, 4)
+    if frozen:
+        block.freeze()
+    block.calibrate(batch(64, d, 36), batch(64, d, 37))
+    block.freeze()
+    x, res = R.rand((7, d), 1.0, BF, 38), R.rand((7, d), 1.0, BF, 39)
+    got = block.decode(x.to(DEV), res.to(DEV))
+    torch.cuda.synchronize()
+    want, h, _ = reference(cpu, x, res, "silu", True)
+    # the residual stream's one bf16 rounding (2^-9 of |y|) is in the bound too
+    assert off(got - (x.to(DEV) + res.to(DEV)), want - h) < Y_BOUND + 2.0 ** -9 * float(want.norm() / (want - h).norm())
+
+
+def test_calibrate_leaves_training_alone():
+    d = 128
+    _, _, block = make(d, 256, "gelu", False, False)
+    _, _, twin = make(d, 256, "gelu", False, False)
+    x, dy = batch(32, d, 40), batch(32, d, 41, 1e-2)
+    block.forward(x), twin.forward(x)
+    before = {k: r.clone() for k, r in block.rings.items()}
+    block.calibrate(batch(16, d, 42))
+    for k, r in block.rings.items():
+        assert torch.equal(r, before[k]) == (k != "u"), k
+    same(block.backward(dy), twin.backward(dy))
+
+
 def test_a_freeze_that_fails_leaves_no_weights():
     d = 128
     _, dev, block = make(d, 256, "gelu", False, False)
