@@ -10,6 +10,7 @@ down-projection with the residual stream, each one call.
 
 forward / backward (training, delayed scaling): every quantized tensor has its
 amax-history ring, as Fp8Linear's have; a step has no host synchronisation.
+seed() gives a fresh block's rings the scales of a first batch.
 
     dY  -> E5M2 codes in both layouts, db_down       fp8_quantize_dual_bias_grad
     dU  = dY W_down                                  fp8_mm
@@ -28,8 +29,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (ACT_NONE, E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_quantize_dual,
-               fp8_quantize_dual_bias_grad, fp8_quantize_dynamic, fp8_rmsnorm, fp8_rmsnorm_grad, new_ring)
+from . import (ACT_NONE, E4M3, E5M2, LAYOUT_ROW, fp8_act_grad, fp8_mm, fp8_mm_act, fp8_quantize,
+               fp8_quantize_dual, fp8_quantize_dual_bias_grad, fp8_quantize_dynamic, fp8_ring_seed, fp8_rmsnorm,
+               fp8_rmsnorm_grad, new_ring)
 
 
 def _version(t: torch.Tensor):
@@ -74,11 +76,34 @@ class Fp8Mlp:
         # n, W_up, u, W_down, dY, dZ
         self.rings = {k: new_ring(hist_len, 1.0, dev) for k in ("n", "w_up", "u", "w_down", "g", "z")}
         self.scale_inv = {k: torch.empty(1, dtype=torch.float32, device=dev) for k in self.rings}
+        self._one = torch.ones(1, dtype=torch.float32, device=dev)
+        self._amax = torch.empty(1, dtype=torch.float32, device=dev)
+        self._seed_gradients = False  # set by seed() for the next backward
         self._frozen = None
         # decode's multiplier of u: scale_inv holds a pending backward's
         self._u_inv = torch.empty(1, dtype=torch.float32, device=dev)
         self._saved = None
         self._forwards = 0
+
+    def seed(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
+        """Seed the rings from the weights and a first batch, and those of the
+        gradients in the next backward from what it quantizes, so that the
+        first step has the tensors' own scales.  A fresh block's rings hold
+        scale 1: its first steps lose what E5M2 cannot hold there, gradients
+        below 2^-17.  (Call it before a step is captured in a graph.)"""
+        d = self.norm_weight.shape[0]
+        x2, r2 = x.reshape(-1, d), None if residual is None else residual.reshape(-1, d)
+        self._seed("w_up", E4M3, lambda s, amax: fp8_quantize(self.w_up, E4M3, scale=s, amax_out=amax))
+        self._seed("w_down", E4M3, lambda s, amax: fp8_quantize(self.w_down, E4M3, scale=s, amax_out=amax))
+        self._seed("n", E4M3, lambda s, amax: fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2, scale=s,
+                                                          amax_out=amax))
+        self._seed("u", E4M3, lambda s, amax: self._up(x2, r2, None, out_scale=s, out_amax=amax))
+        self._seed_gradients = True
+
+    def _seed(self, name: str, fmt, measure) -> None:
+        """Seed a ring with the amax that `measure` finds at scale 1, its codes unused."""
+        measure(self._one, self._amax)
+        fp8_ring_seed(self.rings[name], self._amax, fmt)
 
     def _weight(self, name: str, w: torch.Tensor):
         return fp8_quantize_dual(w, E4M3, ring=self.rings[name], scale_inv_out=self.scale_inv[name])
@@ -119,6 +144,8 @@ class Fp8Mlp:
     def _gradient(self, name: str, dy: torch.Tensor, out_t: torch.Tensor, bias: bool):
         """dy's codes in both layouts; returns the row codes and the bias gradient."""
         ring, inv = self.rings[name], self.scale_inv[name]
+        if self._seed_gradients:
+            self._seed(name, E5M2, lambda s, amax: fp8_quantize(dy, E5M2, scale=s, amax_out=amax))
         if bias:
             codes, _, db = fp8_quantize_dual_bias_grad(dy, E5M2, out_t=out_t, ring=ring, scale_inv_out=inv)
             return codes, db
@@ -146,8 +173,12 @@ class Fp8Mlp:
         if z is None:  # no activation
             zq, db_up = self._gradient("z", du, z_t[:, :rows], self.b_up is not None)
         else:
+            if self._seed_gradients:
+                self._seed("z", E5M2, lambda q, amax: fp8_act_grad(du, z, self.act, self.gated, E5M2, scale=q,
+                                                                   amax_out=amax))
             zq, _, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, out_t=z_t[:, :rows], ring=r["z"],
                                         scale_inv_out=s["z"], need_bias_grad=self.b_up is not None)
+        self._seed_gradients = False
         dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
         dw_down = fp8_mm(g_t, u_buf.t(), E5M2, E4M3, s["g"], s["u"])
         dw_up = fp8_mm(z_t, n_buf.t(), E5M2, E4M3, s["z"], s["n"])
@@ -172,15 +203,17 @@ class Fp8Mlp:
         """Fold one batch's amax into the activation's ring, for decode of a
         block that was not trained here: the up-projection as decode runs it
         (the frozen weights where there are some), nothing else touched."""
+        self._up(x, residual, None if self._frozen is None else self._frozen[0], out_ring=self.rings["u"])
+
+    def _up(self, x, residual, weight, **out) -> None:
+        """The up-projection under current scaling, for its output's amax;
+        weight: W_up's codes and multiplier, where they are at hand."""
         d = self.norm_weight.shape[0]
-        x2 = x.reshape(-1, d)
-        nq, row_inv = self._decode_norm(x2, None if residual is None else residual.reshape(-1, d), None)
-        if self._frozen is None:
+        nq, row_inv = self._decode_norm(x.reshape(-1, d), None if residual is None else residual.reshape(-1, d), None)
+        if weight is None:
             inv = torch.empty(1, dtype=torch.float32, device=x.device)
-            wu = fp8_quantize_dynamic(self.w_up, E4M3, LAYOUT_ROW, scale_inv_out=inv)[0]
-        else:
-            wu, inv = self._frozen[0]
-        fp8_mm_act(nq, wu, row_inv, inv, self.b_up, self.act, self.gated, out_fmt=E4M3, out_ring=self.rings["u"])
+            weight = fp8_quantize_dynamic(self.w_up, E4M3, LAYOUT_ROW, scale_inv_out=inv)[0], inv
+        fp8_mm_act(nq, weight[0], row_inv, weight[1], self.b_up, self.act, self.gated, out_fmt=E4M3, **out)
 
     def _decode_norm(self, x, residual, sum_out):
         """The norm's codes with one scale per row, and the rows' multipliers."""

@@ -210,7 +210,7 @@ def test_one_calibration_of_small_weights(frozen):
     torch.cuda.synchronize()
     want, h, _ = reference(cpu, x, res, "silu", True)
     # the residual stream's one bf16 rounding (2^-9 of |y|) is in the bound too
-    assert off(got - (x.to(DEV) + res.to(DEV)), want - h) < Y_BOUND + 2.0 ** -9 * float(want.norm() / (want - h).norm())
+    assert off(got - (x.to(DEV) + res.to(DEV)), want - h) < Y_BOUND + 2.0 ** -9 * float((want.norm() / (want - h).norm()).detach())
 
 
 def test_calibrate_leaves_training_alone():
@@ -224,6 +224,29 @@ def test_calibrate_leaves_training_alone():
     for k, r in block.rings.items():
         assert torch.equal(r, before[k]) == (k != "u"), k
     same(block.backward(dy), twin.backward(dy))
+
+
+@pytest.mark.parametrize("act,gated,bias", [("gelu", False, True), ("silu", True, False), ("none", False, False)])
+def test_seeded_first_step(act, gated, bias):
+    """After seed() the first step has its values and its gradients, dy far
+    below what E5M2 holds at scale 1 (2^-17) included, and the next one too."""
+    d, f = 256, 512
+    cpu, dev, block = make(d, f, act, gated, bias)
+    x, res, dy = R.rand((48, d), 1.0, BF, 43), R.rand((48, d), 1.0, BF, 44), R.rand((48, d), 1e-6, BF, 45)
+    want, h, leaves = reference(cpu, x, res, act, gated)
+    want.backward(dy.double())
+    block.seed(x.to(DEV), res.to(DEV))
+    for step in range(2):
+        y = block.forward(x.to(DEV), res.to(DEV))
+        got = block.backward(dy.to(DEV))
+        torch.cuda.synchronize()
+        assert off(y - (x.to(DEV) + res.to(DEV)), want - h) < Y_BOUND
+        # x's gradient holds dy itself: the block's own share of it, and one bf16 rounding
+        share = leaves[0].grad - dy.double()
+        assert off(got["x"] - dy.to(DEV), share) < G_BOUND + 2.0 ** -8 * float(leaves[0].grad.norm() / share.norm())
+        for name, leaf in zip(("norm_weight", "w_up", "w_down", "b_up", "b_down"), leaves[1:]):
+            if leaf is not None:
+                assert off(got[name], leaf.grad) < G_BOUND, (step, name)
 
 
 def test_a_freeze_that_fails_leaves_no_weights():
