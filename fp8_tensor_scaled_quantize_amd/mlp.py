@@ -105,8 +105,11 @@ class Fp8Mlp:
         measure(self._one, self._amax)
         fp8_ring_seed(self.rings[name], self._amax, fmt)
 
-    def _weight(self, name: str, w: torch.Tensor):
-        return fp8_quantize_dual(w, E4M3, ring=self.rings[name], scale_inv_out=self.scale_inv[name])
+    def _weight(self, name: str, w: torch.Tensor, both: bool):
+        """w's codes, and the transposed ones that only a backward reads."""
+        if both:
+            return fp8_quantize_dual(w, E4M3, ring=self.rings[name], scale_inv_out=self.scale_inv[name])
+        return fp8_quantize(w, E4M3, ring=self.rings[name], scale_inv_out=self.scale_inv[name]), None
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, save_for_backward: bool = True):
         """x (and residual) bf16 [..., d] -> the residual stream after the
@@ -123,8 +126,8 @@ class Fp8Mlp:
         nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2,
                          out=None if n_buf is None else n_buf[:rows], ring=self.rings["n"], scale_inv_out=s["n"],
                          sum_out=None if r2 is None else h, rstd_out=rstd)
-        wu, wu_t = self._weight("w_up", self.w_up)
-        wd, wd_t = self._weight("w_down", self.w_down)
+        wu, wu_t = self._weight("w_up", self.w_up, save_for_backward)
+        wd, wd_t = self._weight("w_down", self.w_down, save_for_backward)
         z = None
         if save_for_backward and (self.gated or self.act not in ("none", None, ACT_NONE)):
             z = torch.empty(rows, self.w_up.shape[0], dtype=torch.bfloat16, device=dev)

@@ -249,6 +249,16 @@ def test_seeded_first_step(act, gated, bias):
                 assert off(got[name], leaf.grad) < G_BOUND, (step, name)
 
 
+def test_forward_without_backward_equals_the_saved_one():
+    _, _, a = make(256, 512, "silu", True, True)
+    _, _, b = make(256, 512, "silu", True, True)
+    for k in range(3):
+        x = batch(40, 256, 46 + k)
+        assert torch.equal(a.forward(x, save_for_backward=False), b.forward(x)), k
+        for name in a.rings:
+            assert torch.equal(a.rings[name], b.rings[name]), (k, name)
+
+
 def test_a_freeze_that_fails_leaves_no_weights():
     d = 128
     _, dev, block = make(d, 256, "gelu", False, False)
