@@ -85,14 +85,21 @@ class Fp8Mlp:
         self._saved = None
         self._forwards = 0
 
+    def _rows(self, x: torch.Tensor, residual: torch.Tensor | None):
+        """x and residual [..., d] as rows."""
+        d = self.norm_weight.shape[0]
+        for t, name in ((x, "x"), (residual, "residual")):
+            if t is not None and t.shape[-1:] != (d,):
+                raise ValueError(f"{name} must be [..., {d}], got {tuple(t.shape)}")
+        return x.reshape(-1, d), None if residual is None else residual.reshape(-1, d)
+
     def seed(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Seed the rings from the weights and a first batch, and those of the
         gradients in the next backward from what it quantizes, so that the
         first step has the tensors' own scales.  A fresh block's rings hold
         scale 1: its first steps lose what E5M2 cannot hold there, gradients
         below 2^-17.  (Call it before a step is captured in a graph.)"""
-        d = self.norm_weight.shape[0]
-        x2, r2 = x.reshape(-1, d), None if residual is None else residual.reshape(-1, d)
+        x2, r2 = self._rows(x, residual)
         self._seed("w_up", E4M3, lambda s, amax: fp8_quantize(self.w_up, E4M3, scale=s, amax_out=amax))
         self._seed("w_down", E4M3, lambda s, amax: fp8_quantize(self.w_down, E4M3, scale=s, amax_out=amax))
         self._seed("n", E4M3, lambda s, amax: fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2, scale=s,
@@ -116,9 +123,8 @@ class Fp8Mlp:
         block, bf16 [..., d].  Without save_for_backward also of fp16 or fp32."""
         if save_for_backward and x.dtype is not torch.bfloat16:
             raise ValueError(f"a forward that is saved for backward takes bfloat16, got {x.dtype}")
-        d = self.norm_weight.shape[0]
-        x2 = x.reshape(-1, d)
-        r2 = None if residual is None else residual.reshape(-1, d)
+        x2, r2 = self._rows(x, residual)
+        d = x2.shape[1]
         rows, dev, s = x2.shape[0], x.device, self.scale_inv
         h = x2 if r2 is None else torch.empty_like(x2)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
@@ -206,15 +212,15 @@ class Fp8Mlp:
         """Fold one batch's amax into the activation's ring, for decode of a
         block that was not trained here: the up-projection as decode runs it
         (the frozen weights where there are some), nothing else touched."""
-        self._up(x, residual, None if self._frozen is None else self._frozen[0], out_ring=self.rings["u"])
+        x2, r2 = self._rows(x, residual)
+        self._up(x2, r2, None if self._frozen is None else self._frozen[0], out_ring=self.rings["u"])
 
-    def _up(self, x, residual, weight, **out) -> None:
+    def _up(self, x2, r2, weight, **out) -> None:
         """The up-projection under current scaling, for its output's amax;
         weight: W_up's codes and multiplier, where they are at hand."""
-        d = self.norm_weight.shape[0]
-        nq, row_inv = self._decode_norm(x.reshape(-1, d), None if residual is None else residual.reshape(-1, d), None)
+        nq, row_inv = self._decode_norm(x2, r2, None)
         if weight is None:
-            inv = torch.empty(1, dtype=torch.float32, device=x.device)
+            inv = torch.empty(1, dtype=torch.float32, device=x2.device)
             weight = fp8_quantize_dynamic(self.w_up, E4M3, LAYOUT_ROW, scale_inv_out=inv)[0], inv
         fp8_mm_act(nq, weight[0], row_inv, weight[1], self.b_up, self.act, self.gated, out_fmt=E4M3, **out)
 
@@ -225,10 +231,12 @@ class Fp8Mlp:
                            scale_inv_out=row_inv, sum_out=sum_out), row_inv
 
     def decode(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
-        """One serving step on [tokens, d]: adds x to residual and the block's
+        """One serving step on bf16 [tokens, d]: adds x to residual and the block's
         output to that, in place; returns residual."""
         if self._frozen is None:
             raise RuntimeError("decode needs freeze()")
+        if residual.dtype is not torch.bfloat16:  # before the norm has written to it
+            raise ValueError(f"residual must be bfloat16, got {residual.dtype}")
         (wu, s_wu), (wd, s_wd) = self._frozen
         nq, row_inv = self._decode_norm(x, residual, residual)
         scale = self.rings["u"].view(torch.float32)[self.hist_len:self.hist_len + 1]  # the ring's current scale

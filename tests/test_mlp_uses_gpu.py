@@ -259,6 +259,25 @@ def test_forward_without_backward_equals_the_saved_one():
             assert torch.equal(a.rings[name], b.rings[name]), (k, name)
 
 
+def test_widths_and_types_are_checked_first():
+    d = 128
+    _, _, block = make(d, 256, "gelu", False, False)
+    block.freeze()
+    x = batch(8, 2 * d, 50)
+    for call in (lambda: block.forward(x), lambda: block.calibrate(x), lambda: fp8_mlp(x, block),
+                 lambda: block.forward(batch(8, d, 51), batch(8, 2 * d, 52)), lambda: block.seed(x),
+                 lambda: block.decode(x, x.clone())):
+        with pytest.raises(ValueError):
+            call()
+    for dt in (torch.float16, torch.float32):
+        a, r = batch(3, d, 53).to(dt), batch(3, d, 54).to(dt)
+        keep = r.clone()
+        with pytest.raises(ValueError, match="bfloat16"):
+            block.decode(a, r)
+        torch.cuda.synchronize()
+        assert torch.equal(r, keep)
+
+
 def test_a_freeze_that_fails_leaves_no_weights():
     d = 128
     _, dev, block = make(d, 256, "gelu", False, False)
