@@ -132,6 +132,7 @@ class Fp8Mlp:
         nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2,
                          out=None if n_buf is None else n_buf[:rows], ring=self.rings["n"], scale_inv_out=s["n"],
                          sum_out=None if r2 is None else h, rstd_out=rstd)
+        self._saved = None  # its multipliers are being replaced, whatever comes of this forward
         wu, wu_t = self._weight("w_up", self.w_up, save_for_backward)
         wd, wd_t = self._weight("w_down", self.w_down, save_for_backward)
         z = None

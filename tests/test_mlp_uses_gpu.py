@@ -286,3 +286,16 @@ def test_a_freeze_that_fails_leaves_no_weights():
         block.freeze()
     with pytest.raises(RuntimeError, match="freeze"):
         block.decode(batch(3, d, 55), batch(3, d, 56))
+
+
+def test_a_forward_that_fails_ends_the_pending_backward():
+    """It has replaced some of the multipliers that the backward would read."""
+    d = 128
+    _, dev, block = make(d, 256, "gelu", False, False)
+    x, dy = batch(16, d, 57), batch(16, d, 58)
+    block.forward(x)
+    block.w_down = dev[2].double()
+    with pytest.raises(ValueError):
+        block.forward(4 * x)
+    with pytest.raises(RuntimeError, match="needs a forward"):
+        block.backward(dy)
