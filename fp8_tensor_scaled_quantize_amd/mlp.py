@@ -41,20 +41,25 @@ def _version(t: torch.Tensor):
 
 # The weight gradients sum over tokens, and a product's K is a multiple of 16:
 # codes that they read have that many tokens, the last ones zero.
-def _token_rows(rows: int, cols: int, dev) -> torch.Tensor:
-    """Storage of codes [rows, cols], zero rows up to a multiple of 16."""
-    buf = torch.empty(-(-rows // 16) * 16, cols, dtype=torch.uint8, device=dev)
-    if rows % 16:
-        buf[rows:].zero_()
-    return buf
+def _token_rows(rows: int, cols: int, dev):
+    """Storage for codes [rows, cols] with zero rows up to a multiple of 16, and
+    the codes' part of it."""
+    pad = -rows % 16
+    buf = torch.empty(rows + pad, cols, dtype=torch.uint8, device=dev)
+    if pad == 0:
+        return buf, buf
+    buf[rows:].zero_()
+    return buf, buf[:rows]
 
 
-def _token_cols(cols: int, rows: int, dev) -> torch.Tensor:
-    """Storage of transposed codes [cols, rows], zero columns up to a multiple of 16."""
-    buf = torch.empty(cols, -(-rows // 16) * 16, dtype=torch.uint8, device=dev)
-    if rows % 16:
-        buf[:, rows:].zero_()
-    return buf
+def _token_cols(cols: int, rows: int, dev):
+    """The same for transposed codes [cols, rows]: zero columns."""
+    pad = -rows % 16
+    buf = torch.empty(cols, rows + pad, dtype=torch.uint8, device=dev)
+    if pad == 0:
+        return buf, buf
+    buf[:, rows:].zero_()
+    return buf, buf[:, :rows]
 
 
 class Fp8Mlp:
@@ -128,20 +133,18 @@ class Fp8Mlp:
         rows, dev, s = x2.shape[0], x.device, self.scale_inv
         h = x2 if r2 is None else torch.empty_like(x2)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        n_buf = _token_rows(rows, d, dev) if save_for_backward else None
-        nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2,
-                         out=None if n_buf is None else n_buf[:rows], ring=self.rings["n"], scale_inv_out=s["n"],
-                         sum_out=None if r2 is None else h, rstd_out=rstd)
+        n_buf, n_out = _token_rows(rows, d, dev) if save_for_backward else (None, None)
+        nq = fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2, out=n_out, ring=self.rings["n"],
+                         scale_inv_out=s["n"], sum_out=None if r2 is None else h, rstd_out=rstd)
         self._saved = None  # its multipliers are being replaced, whatever comes of this forward
         wu, wu_t = self._weight("w_up", self.w_up, save_for_backward)
         wd, wd_t = self._weight("w_down", self.w_down, save_for_backward)
         z = None
         if save_for_backward and (self.gated or self.act not in ("none", None, ACT_NONE)):
             z = torch.empty(rows, self.w_up.shape[0], dtype=torch.bfloat16, device=dev)
-        u_buf = _token_rows(rows, self.w_down.shape[1], dev) if save_for_backward else None
-        uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z,
-                        out=None if u_buf is None else u_buf[:rows], out_fmt=E4M3, out_ring=self.rings["u"],
-                        out_scale_inv=s["u"])
+        u_buf, u_out = _token_rows(rows, self.w_down.shape[1], dev) if save_for_backward else (None, None)
+        uq = fp8_mm_act(nq, wu, s["n"], s["w_up"], self.b_up, self.act, self.gated, z_out=z, out=u_out, out_fmt=E4M3,
+                        out_ring=self.rings["u"], out_scale_inv=s["u"])
         y = fp8_mm_act(uq, wd, s["u"], s["w_down"], self.b_down, residual=h)
         # the norm's weight is not a copy, and h is x itself without a residual:
         # backward, which reads both again, checks their versions
@@ -177,16 +180,17 @@ class Fp8Mlp:
         s, r = self.scale_inv, self.rings
         dy2 = dy.reshape(h.shape)
         rows, d = h.shape
-        g_t, z_t = _token_cols(d, rows, h.device), _token_cols(self.w_up.shape[0], rows, h.device)
-        gq, db_down = self._gradient("g", dy2, g_t[:, :rows], self.b_down is not None)
+        g_t, g_out = _token_cols(d, rows, h.device)
+        z_t, z_out = _token_cols(self.w_up.shape[0], rows, h.device)
+        gq, db_down = self._gradient("g", dy2, g_out, self.b_down is not None)
         du = fp8_mm(gq, wd_t, E5M2, E4M3, s["g"], s["w_down"])
         if z is None:  # no activation
-            zq, db_up = self._gradient("z", du, z_t[:, :rows], self.b_up is not None)
+            zq, db_up = self._gradient("z", du, z_out, self.b_up is not None)
         else:
             if self._seed_gradients:
                 self._seed("z", E5M2, lambda q, amax: fp8_act_grad(du, z, self.act, self.gated, E5M2, scale=q,
                                                                    amax_out=amax))
-            zq, _, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, out_t=z_t[:, :rows], ring=r["z"],
+            zq, _, db_up = fp8_act_grad(du, z, self.act, self.gated, E5M2, out_t=z_out, ring=r["z"],
                                         scale_inv_out=s["z"], need_bias_grad=self.b_up is not None)
         self._seed_gradients = False
         dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
