@@ -16,6 +16,12 @@
 // so the sums that need the whole row (and the row's maximum) cost no second
 // read.  With WPR = 1 a row's sums stay inside one wave: no barrier, no LDS.
 // All sums are fp32.
+//
+// Four vectors a lane at sixteen waves a row (above 16384 columns) pass the 128
+// registers a lane has there: fp32 rows spill in the norm (512 x 32768 63 us for
+// 218 MB), every type in the gradient (1024 x 20480 bf16 154 us for 168 MB, where
+// two vectors a lane take 66 us for the 268 MB of 2048 x 16384).  The one-wave
+// fp32 gradient of 1537 to 2048 columns spills too (8192 x 2048 86 us for 268 MB).
 #include "fp8mi_internal.h"
 #include "vec_io.h"
 
@@ -223,10 +229,6 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs p) {
   if (threadIdx.x == 0 && p.scale_inv_out && blockIdx.x == 0) *p.scale_inv_out = 1.0f / s_t;
 }
 
-// Gradient.  A wave (WPR = 1) or the workgroup walks over rows, the next row's
-// loads in flight while one is finished, and keeps the weights and the weight
-// gradient's sums of its columns in registers; each workgroup then writes one
-// fp32 partial row, and rmsnorm_dw adds those in a fixed order.
 // The weight gradient of few rows, straight from dy and h: workgroups past the
 // rows' own take 16 columns each, NT / 16 row lanes per column, so a second
 // launch is saved for a second read (from the L2).
@@ -260,6 +262,10 @@ template <int DT, int NT> __device__ __forceinline__ void dw_direct(const NormGr
   }
 }
 
+// Gradient.  A wave (WPR = 1) or the workgroup walks over rows, the next row's
+// loads in flight while one is finished, and keeps the weights and the weight
+// gradient's sums of its columns in registers; each workgroup then writes one
+// fp32 partial row, and rmsnorm_dw adds those in a fixed order.
 template <int DT, bool W32, int WPR, int NV, int NT>
 __global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradArgs p) {
   constexpr int RPB = NT / 64 / WPR;
