@@ -124,10 +124,8 @@ class Fp8Mlp:
         return fp8_quantize(w, E4M3, ring=self.rings[name], scale_inv_out=self.scale_inv[name]), None
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, save_for_backward: bool = True):
-        """x (and residual) bf16 [..., d] -> the residual stream after the
-        block, bf16 [..., d].  Without save_for_backward also of fp16 or fp32."""
-        if save_for_backward and x.dtype is not torch.bfloat16:
-            raise ValueError(f"a forward that is saved for backward takes bfloat16, got {x.dtype}")
+        """x (and residual) bf16, fp16 or fp32 [..., d] -> the residual stream
+        after the block, bf16 [..., d]."""
         x2, r2 = self._rows(x, residual)
         d = x2.shape[1]
         rows, dev, s = x2.shape[0], x.device, self.scale_inv
@@ -196,7 +194,11 @@ class Fp8Mlp:
         dn = fp8_mm(zq, wu_t, E5M2, E4M3, s["z"], s["w_up"])
         dw_down = fp8_mm(g_t, u_buf.t(), E5M2, E4M3, s["g"], s["u"])
         dw_up = fp8_mm(z_t, n_buf.t(), E5M2, E4M3, s["z"], s["n"])
-        dx, dnw = fp8_rmsnorm_grad(dn, h, nw, rstd, dsum=dy2)
+        if h.dtype is torch.bfloat16:
+            dx, dnw = fp8_rmsnorm_grad(dn, h, nw, rstd, dsum=dy2)
+        else:  # the products' gradients are bf16: fp32 holds both types, fp16 would not
+            dx, dnw = fp8_rmsnorm_grad(dn.float(), h.float(), nw, rstd, dsum=dy2.float())
+            dx = dx.to(h.dtype)
         return {"x": dx.reshape(x_shape), "norm_weight": dnw, "w_up": dw_up, "w_down": dw_down, "b_up": db_up,
                 "b_down": db_down}
 

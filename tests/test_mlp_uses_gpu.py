@@ -125,26 +125,45 @@ def test_any_token_count(tokens, act, gated, bias):
 
 
 def test_training_refusals_come_first():
-    """What a training step cannot take is refused before a ring has moved."""
+    """What a backward cannot take is refused before a ring has moved."""
     d = 128
     _, _, block = make(d, 256, "gelu", False, True)
     x, dy = batch(16, d, 15), batch(16, d, 16)
-    rings = {k: r.clone() for k, r in block.rings.items()}
-    for t in (x.half(), x.float()):
-        with pytest.raises(ValueError, match="bfloat16"):
-            block.forward(t)
-        with pytest.raises(ValueError, match="bfloat16"):
-            fp8_mlp(t, block)
-    for k, r in block.rings.items():
-        assert torch.equal(r, rings[k]), k
-    y32, y = block.forward(x.float(), save_for_backward=False), block.forward(x)  # inference takes them
-    assert y32.dtype == BF and y32.shape == y.shape
+    block.forward(x)
     rings = {k: r.clone() for k, r in block.rings.items()}
     for t in (dy.float(), dy.half(), dy[:8], dy.reshape(32, 64)):
         with pytest.raises(ValueError, match="dy"):
             block.backward(t)
     for k, r in block.rings.items():
         assert torch.equal(r, rings[k]), k
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+@pytest.mark.parametrize("with_res", [False, True])
+@pytest.mark.parametrize("tokens", [40, 48])
+def test_streams_of_other_types(dt, with_res, tokens):
+    """fp16 and fp32 x (and residual): the output is bf16, dx has x's type.
+    Gradients of 1e-6, where fp16 has steps of 2^-24: dx's own rounding, half a
+    step an element, is in its bound."""
+    d, f, sigma = 256, 512, 1e-6
+    cpu, dev, block = make(d, f, "gelu", False, True)
+    x, dy = R.rand((tokens, d), 1.0, dt, 59), R.rand((tokens, d), sigma, BF, 61)
+    res = R.rand((tokens, d), 1.0, dt, 60) if with_res else None
+    xd, rd = x.to(DEV).requires_grad_(), None if res is None else res.to(DEV)
+    for t in dev:
+        t.requires_grad_()
+    block.seed(xd.detach(), rd)
+    y = fp8_mlp(xd, block, rd)
+    y.backward(dy.to(DEV))
+    torch.cuda.synchronize()
+    want, h, leaves = reference(cpu, x, res, "gelu", False)
+    want.backward(dy.double())
+    assert y.dtype == BF and xd.grad.dtype == dt
+    assert off(y.double().cpu() - h, want - h) < Y_BOUND + 2.0 ** -9 * float((want.norm() / (want - h).norm()).detach())
+    half = 2.0 ** -25 if dt is torch.float16 else 0.0
+    assert off(xd.grad, leaves[0].grad) < G_BOUND + half * (tokens * d) ** 0.5 / float(leaves[0].grad.norm())
+    for got, ref in zip(dev, leaves[1:]):
+        assert off(got.grad, ref.grad) < G_BOUND, tuple(got.shape)
 
 
 @pytest.mark.parametrize("bias", [False, True])
