@@ -90,13 +90,17 @@ class Fp8Mlp:
         self._saved = None
         self._forwards = 0
 
-    def _rows(self, x: torch.Tensor, residual: torch.Tensor | None):
-        """x and residual [..., d] as rows."""
-        d = self.norm_weight.shape[0]
-        for t, name in ((x, "x"), (residual, "residual")):
-            if t is not None and t.shape[-1:] != (d,):
-                raise ValueError(f"{name} must be [..., {d}], got {tuple(t.shape)}")
-        return x.reshape(-1, d), None if residual is None else residual.reshape(-1, d)
+    def _rows(self, t: torch.Tensor, name: str) -> torch.Tensor:
+        """t as rows of d: its last dimension, or its last ones together, hold d
+        (another width would be read as other rows)."""
+        d, n = self.norm_weight.shape[0], 1
+        for size in reversed(t.shape):
+            n *= size
+            if n >= d:
+                break
+        if n != d:
+            raise ValueError(f"{name} must be [..., {d}], got {tuple(t.shape)}")
+        return t.reshape(-1, d)
 
     def seed(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Seed the rings from the weights and a first batch, and those of the
@@ -104,7 +108,7 @@ class Fp8Mlp:
         first step has the tensors' own scales.  A fresh block's rings hold
         scale 1: its first steps lose what E5M2 cannot hold there, gradients
         below 2^-17.  (Call it before a step is captured in a graph.)"""
-        x2, r2 = self._rows(x, residual)
+        x2, r2 = self._rows(x, "x"), None if residual is None else self._rows(residual, "residual")
         self._seed("w_up", E4M3, lambda s, amax: fp8_quantize(self.w_up, E4M3, scale=s, amax_out=amax))
         self._seed("w_down", E4M3, lambda s, amax: fp8_quantize(self.w_down, E4M3, scale=s, amax_out=amax))
         self._seed("n", E4M3, lambda s, amax: fp8_rmsnorm(x2, self.norm_weight, E4M3, self.eps, residual=r2, scale=s,
@@ -126,7 +130,7 @@ class Fp8Mlp:
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, save_for_backward: bool = True):
         """x (and residual) bf16, fp16 or fp32 [..., d] -> the residual stream
         after the block, bf16 [..., d]."""
-        x2, r2 = self._rows(x, residual)
+        x2, r2 = self._rows(x, "x"), None if residual is None else self._rows(residual, "residual")
         d = x2.shape[1]
         rows, dev, s = x2.shape[0], x.device, self.scale_inv
         h = x2 if r2 is None else torch.empty_like(x2)
@@ -169,14 +173,14 @@ class Fp8Mlp:
         if self._saved is None:
             raise RuntimeError("backward needs a forward with save_for_backward=True")
         n_buf, h, rstd, z, u_buf, wu_t, wd_t, x_shape, nw, h_version, nw_version = self._saved
-        if dy.dtype is not torch.bfloat16 or dy.shape[-1:] != x_shape[-1:] or dy.numel() != h.numel():
+        dy2 = self._rows(dy, "dy")
+        if dy.dtype is not torch.bfloat16 or dy2.shape != h.shape:
             raise ValueError(f"dy must be bfloat16 {tuple(x_shape)} like the output, got {dy.dtype} {tuple(dy.shape)}")
         if _version(h) != h_version:
             raise RuntimeError("backward reads x again, which was changed in place since the forward pass")
         if _version(nw) != nw_version:
             raise RuntimeError("backward reads norm_weight again, which was changed in place since the forward pass")
         s, r = self.scale_inv, self.rings
-        dy2 = dy.reshape(h.shape)
         rows, d = h.shape
         g_t, g_out = _token_cols(d, rows, h.device)
         z_t, z_out = _token_cols(self.w_up.shape[0], rows, h.device)
@@ -219,7 +223,7 @@ class Fp8Mlp:
         """Fold one batch's amax into the activation's ring, for decode of a
         block that was not trained here: the up-projection as decode runs it
         (the frozen weights where there are some), nothing else touched."""
-        x2, r2 = self._rows(x, residual)
+        x2, r2 = self._rows(x, "x"), None if residual is None else self._rows(residual, "residual")
         self._up(x2, r2, None if self._frozen is None else self._frozen[0], out_ring=self.rings["u"])
 
     def _up(self, x2, r2, weight, **out) -> None:

@@ -288,6 +288,9 @@ def test_widths_and_types_are_checked_first():
                  lambda: block.decode(x, x.clone())):
         with pytest.raises(ValueError):
             call()
+    h = batch(8, d, 62)  # a width given as several dimensions is one
+    assert torch.equal(block.forward(h.view(2, 4, 8, d // 8)).view(8, d), make(d, 256, "gelu", False, False)[2].forward(h))
+    assert block.backward(h)["x"].shape == (2, 4, 8, d // 8)
     for dt in (torch.float16, torch.float32):
         a, r = batch(3, d, 53).to(dt), batch(3, d, 54).to(dt)
         keep = r.clone()
