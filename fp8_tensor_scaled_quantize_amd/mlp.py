@@ -264,6 +264,7 @@ class _Fp8MlpFn(torch.autograd.Function):
     def forward(ctx, x, residual, norm_weight, w_up, w_down, b_up, b_down, block):
         y = block.forward(x, residual)
         ctx.block, ctx.step = block, block._forwards
+        ctx.residual_shape = None if residual is None else residual.shape
         ctx.dtypes = [None if t is None else t.dtype for t in (x, residual, norm_weight, w_up, w_down, b_up, b_down)]
         return y
 
@@ -273,7 +274,8 @@ class _Fp8MlpFn(torch.autograd.Function):
         if block._forwards != ctx.step:
             raise RuntimeError("fp8_mlp: the block ran another forward since the one being differentiated")
         g = block.backward(dy.contiguous())
-        grads = [g["x"], g["x"], g["norm_weight"], g["w_up"], g["w_down"], g["b_up"], g["b_down"]]
+        g_res = None if ctx.residual_shape is None else g["x"].reshape(ctx.residual_shape)
+        grads = [g["x"], g_res, g["norm_weight"], g["w_up"], g["w_down"], g["b_up"], g["b_down"]]
         out = [None if t is None or dt is None or not need else t.to(dt)
                for t, dt, need in zip(grads, ctx.dtypes, ctx.needs_input_grad)]
         return (*out, None)

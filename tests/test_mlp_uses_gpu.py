@@ -321,3 +321,12 @@ def test_a_forward_that_fails_ends_the_pending_backward():
         block.forward(4 * x)
     with pytest.raises(RuntimeError, match="needs a forward"):
         block.backward(dy)
+
+
+def test_residual_of_another_leading_shape():
+    d = 128
+    _, _, block = make(d, 256, "gelu", False, False)
+    x, r = batch(32, d, 63).view(2, 16, d).requires_grad_(), batch(32, d, 64).requires_grad_()
+    fp8_mlp(x, block, r).backward(batch(32, d, 65).view(2, 16, d))
+    torch.cuda.synchronize()
+    assert r.grad.shape == (32, d) and torch.equal(x.grad.view(32, d), r.grad)
