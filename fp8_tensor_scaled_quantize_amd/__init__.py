@@ -10,6 +10,7 @@ is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -19,6 +20,7 @@ __all__ = ["E4M3", "E5M2", "F32", "F16", "BF16", "Fp8Error", "fp8_quantize", "fp
            "fp8_quantize_dual_bias_grad_noalloc", "NOALLOC_SCRATCH_BYTES", "stream_reference",
            "fp8_quantize_dynamic", "DYNAMIC_WORKSPACE_BYTES", "fp8_amax_fold", "fp8_mm", "fp8_mm_ex", "FP8_E4M3", "FP8_E5M2", "fp8_bias_grad", "fp8_bias_grad_workspace_bytes", "fp8_ring_seed", "new_ring", "ring_words", "version",
            "fp8_rmsnorm", "fp8_rmsnorm_grad", "fp8_rmsnorm_grad_workspace_bytes", "fp8_mm_act", "fp8_act_grad",
+           "fp8_adamw_step", "fp8_grad_norm", "ADAMW_BLOCK", "ADAMW_STEP_WORDS",
            "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_SILU", "interleave_gated"]
 
 E4M3, E5M2 = 0, 1
@@ -35,6 +37,8 @@ _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 RING_SCRATCH_WORDS = 1024  # FP8MI_RING_SCRATCH_WORDS
 DYNAMIC_WORKSPACE_BYTES = 4096  # FP8MI_DYNAMIC_WORKSPACE_BYTES
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # FP8MI_NOALLOC_SCRATCH_BYTES
+ADAMW_BLOCK = 256  # elements of an 8-bit state that share a scale
+ADAMW_STEP_WORDS = 4  # FP8MI_ADAMW_STEP_WORDS
 LAYOUT_ROW, LAYOUT_T, LAYOUT_DUAL = 0, 1, 2
 
 
@@ -800,3 +804,137 @@ def fp8_act_grad(dy: torch.Tensor, z: torch.Tensor, act, gated: bool = False, fm
     if status:
         _check(status)
     return out_row, out_t, bias_grad_out
+
+
+# ------------------------------------------------------------------ optimizer
+# fp8mi_adamw_tensor, fp8mi_adamw and fp8mi_norm_tensor
+_ADAMW_TENSOR, _ADAMW_HYPER, _NORM_TENSOR = "7Pq3if", struct.Struct("@4dq3PI4x"), "Pqi4x"
+
+
+def _flat(ts, name: str, sizes=None) -> None:
+    """Contiguous tensors (elementwise operators read them as flat arrays), of
+    the given element counts."""
+    for i, t in enumerate(ts):
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+    if sizes is not None:
+        if len(ts) != len(sizes):
+            raise ValueError(f"{len(ts)} {name} for {len(sizes)} params")
+        for i, t in enumerate(ts):
+            if t.numel() != sizes[i]:
+                raise ValueError(f"{name}[{i}] has {t.numel()} elements, its param {sizes[i]}")
+
+
+def _dtypes(ts, name: str):
+    try:
+        return [_DT[t.dtype] for t in ts]
+    except KeyError:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {[t.dtype for t in ts]}") from None
+
+
+def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch.Tensor = 1e-3, betas=(0.9, 0.999),
+                   eps: float = 1e-8, weight_decay=0.0, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
+                   grad_scale: torch.Tensor | None = None, seed: int = 0) -> None:
+    """One AdamW step over lists of contiguous tensors, in place.  params and
+    grads are fp32, fp16 or bf16 in any mixture; masters holds a param's fp32
+    weights, or None (or is None).  States are fp32 tensors, or, where the lists
+    of scales hold one for it, bytes: E4M3 codes of m and of sqrt(v) and an
+    fp32 scale per 256 elements (all zero to begin with).  step is this step's
+    number from 1 on, or an int32 device tensor of ADAMW_STEP_WORDS words whose
+    first counts the steps done: the call then counts for itself, and lr may be
+    a device scalar.  weight_decay: a number, or one per tensor.  A grad_scale
+    (device scalar) that is not finite skips the step."""
+    n = len(params)
+    sizes = [p.numel() for p in params]
+    _flat(params, "params")
+    _flat(grads, "grads", sizes)
+    _flat(exp_avgs, "exp_avgs", sizes)
+    _flat(exp_avg_sqs, "exp_avg_sqs", sizes)
+    none = [None] * n
+    kept = [m for m in masters if m is not None] if masters is not None else []
+    masters = none if masters is None else masters
+    ms = none if exp_avg_scales is None else exp_avg_scales
+    vs = none if exp_avg_sq_scales is None else exp_avg_sq_scales
+    if len(masters) != n or len(ms) != n or len(vs) != n:
+        raise ValueError("masters and scales: one entry per param (None where there is none)")
+    if kept:
+        _flat(kept, "masters", [k for m, k in zip(masters, sizes) if m is not None])
+    scales = []
+    for i, (m, v, a, b, k) in enumerate(zip(exp_avgs, exp_avg_sqs, ms, vs, sizes)):
+        if a is None and b is None:
+            if m.dtype is not torch.float32 or v.dtype is not torch.float32:
+                raise ValueError(f"states of params[{i}] must be float32, or codes with their scales")
+            continue
+        if a is None or b is None or m.element_size() != 1 or v.element_size() != 1:
+            raise ValueError(f"8-bit states of params[{i}] need 1-byte codes and scales for both")
+        for t in (a, b):
+            _typed_vector(t, -(-k // ADAMW_BLOCK), "scales", _F32_ONLY)
+        scales += (a, b)
+    for m in kept:
+        if m.dtype is not torch.float32:
+            raise ValueError(f"masters must be float32, got {m.dtype}")
+    pdt, gdt = _dtypes(params, "params"), _dtypes(grads, "grads")
+    decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+    if len(decay) != n:
+        raise ValueError(f"{len(decay)} weight decays for {n} params")
+    step_ptr = lr_ptr = None
+    if isinstance(step, torch.Tensor):
+        if step.dtype is not torch.int32 or step.numel() < ADAMW_STEP_WORDS or not step.is_contiguous():
+            raise ValueError(f"a device step is an int32 tensor of {ADAMW_STEP_WORDS} words")
+        step_ptr = step.data_ptr()
+        if isinstance(lr, torch.Tensor):
+            _scalar(lr, "lr")
+            lr_ptr = lr.data_ptr()
+    elif isinstance(lr, torch.Tensor):
+        raise ValueError("lr on the device needs step on the device")
+    _scalar(grad_scale, "grad_scale")
+    _on_device(*params, *grads, *exp_avgs, *exp_avg_sqs, *kept, *scales, grad_scale,
+               step if step_ptr else None, lr if lr_ptr else None)
+    at = [p.data_ptr() for p in params]
+    written = [a for a, k in zip(at, sizes) if k]
+    if len(set(written)) != len(written):
+        raise ValueError("the same param is there twice")
+    flat = []
+    for f in zip(at, grads, masters, exp_avgs, exp_avg_sqs, ms, vs, sizes, pdt, gdt, decay):
+        p, g, w, m, v, a, b, k, pd, gd, wd = f
+        flat += (p, g.data_ptr(), 0 if w is None else w.data_ptr(), m.data_ptr(), v.data_ptr(),
+                 0 if a is None else a.data_ptr(), 0 if b is None else b.data_ptr(), k, pd, gd, 32 if a is None else 8, wd)
+    hyper = _ADAMW_HYPER.pack(0.0 if lr_ptr else float(lr), betas[0], betas[1], eps, 0 if step_ptr else step, step_ptr or 0,
+                              lr_ptr or 0, 0 if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF)
+    if n == 0 and step_ptr is None:
+        return
+    status = lib().fp8_adamw_step(struct.pack("@" + _ADAMW_TENSOR * n, *flat), n, hyper,
+                                  _stream(params[0] if n else step))
+    if status:
+        _check(status)
+    _changed_in_place(params + kept if isinstance(params, list) else [*params, *kept])
+
+
+def fp8_grad_norm(grads, max_norm: float | None = None, out: torch.Tensor | None = None,
+                  clip_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The Euclidean norm of all elements of a list of contiguous gradients
+    (fp32, fp16 or bf16), fp32 [1].  clip_out receives min(1, max_norm / (norm +
+    1e-6)), or NaN where the norm is not finite: fp8_adamw_step's grad_scale."""
+    n = len(grads)
+    _flat(grads, "grads")
+    if n == 0 and out is None:
+        raise ValueError("no gradients: give out, whose device is used")
+    if out is None:
+        out = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+    _scalar(out, "out")
+    _scalar(clip_out, "clip_out")
+    dts = _dtypes(grads, "grads")
+    flat = []
+    for t, dt in zip(grads, dts):
+        flat += (t.data_ptr(), t.numel(), dt)
+    table = struct.pack("@" + _NORM_TENSOR * n, *flat)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(max(L.fp8_grad_norm_workspace_bytes(table, n), 8), dtype=torch.uint8, device=out.device)
+    _on_device(*grads, out, clip_out, workspace)
+    status = L.fp8_grad_norm(table, n, None if max_norm is None else ctypes.byref(ctypes.c_float(max_norm)),
+                             out.data_ptr(), None if clip_out is None else clip_out.data_ptr(), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream(out))
+    if status:
+        _check(status)
+    return out

@@ -34,6 +34,9 @@ SIGNATURES = {
     "fp8_rmsnorm_grad": (C.c_int, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, _P, _P, _I64, _P, _I64, _P, _P,
                                    C.c_size_t, _P]),
     "fp8_rmsnorm_grad_workspace_bytes": (C.c_size_t, [_I64, _I64]),
+    "fp8_adamw_step": (C.c_int, [_P, _I32, _P, _P]),
+    "fp8_grad_norm": (C.c_int, [_P, _I32, _P, _P, _P, _P, C.c_size_t, _P]),
+    "fp8_grad_norm_workspace_bytes": (C.c_size_t, [_P, _I32]),
     "fp8_ring_seed": (C.c_int, [_P, _I32, _P, _I, _P]),
     "fp8mi_stream_reference": (C.c_int, [_P, _I64, _P, _I64, _P]),
     "fp8mi_status_string": (C.c_char_p, [_I]),

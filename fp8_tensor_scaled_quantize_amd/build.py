@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["abi.hip", "quantize.hip", "mm_fp8.hip", "mm_fp8_q8.hip", "mm_fp8_km.hip", "mm_fp8_km_q8_a.hip",
            "mm_fp8_km_q8_b.hip", "mm_fp8_km_q8_ab.hip", "mm_fp8_prec.hip", "mm_fp8_prec_km.hip", "mm_fp8_prec_q8.hip",
            "mm_fp8_prec_km_q8.hip", "mm_act_bf16.hip", "mm_act_bf16_gated.hip",
-           "mm_act_q8.hip", "mm_act_q8_gated.hip", "act_grad.hip", "grad_bias.hip", "rmsnorm.hip", "stream.hip"]
+           "mm_act_q8.hip", "mm_act_q8_gated.hip", "act_grad.hip", "grad_bias.hip", "rmsnorm.hip", "stream.hip",
+           "adamw.hip"]
 LIB = os.path.join(PKG, "libfp8mi.so")
 
 HIPCC_FLAGS = [

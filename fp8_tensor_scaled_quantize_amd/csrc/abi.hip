@@ -1,6 +1,7 @@
 // C ABI of libfp8mi: argument validation, status reporting and dispatch to
 // the kernel launchers.  Every check runs before any HIP call, so a rejected
 // call has no side effects.
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -638,6 +639,91 @@ fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t c
   p.n_cols = cols > 0 ? (float)cols : 1.0f;
   return from_hip(launch_rmsnorm_grad(p, dtype, dweight, workspace, static_cast<hipStream_t>(stream)),
                   "rmsnorm gradient launch");
+}
+
+// One tensor of a list: n elements of dtype at p.
+static fp8mi_status check_elements(const char* name, int i, const void* p, int64_t n, int dt) {
+  if (!valid_dtype(dt)) return fail(FP8MI_ERR_ENUM, "tensor %d: %s dtype %d is not F32/F16/BF16", i, name, dt);
+  if (n < 0 || n > (INT64_C(1) << 42)) return fail(FP8MI_ERR_SHAPE, "tensor %d: %lld elements", i, (long long)n);
+  if (n > 0 && !p) return fail(FP8MI_ERR_NULL, "tensor %d: %s is NULL", i, name);
+  if (reinterpret_cast<uintptr_t>(p) % dtype_bytes(dt))
+    return fail(FP8MI_ERR_ARG, "tensor %d: %s not aligned to its element size", i, name);
+  return FP8MI_OK;
+}
+
+fp8mi_status fp8_adamw_step(const fp8mi_adamw_tensor* tensors, int32_t count, const fp8mi_adamw* hyper, void* stream) {
+  if (!hyper) return fail(FP8MI_ERR_NULL, "hyper is NULL");
+  if (count < 0) return fail(FP8MI_ERR_SHAPE, "count %d", count);
+  if (count > 0 && !tensors) return fail(FP8MI_ERR_NULL, "tensors is NULL");
+  const fp8mi_adamw& h = *hyper;
+  if (!(h.beta1 >= 0.0 && h.beta1 < 1.0 && h.beta2 >= 0.0 && h.beta2 < 1.0))
+    return fail(FP8MI_ERR_ARG, "betas %g, %g outside [0, 1)", h.beta1, h.beta2);
+  if (!(h.eps >= 0.0) || !(h.lr >= 0.0)) return fail(FP8MI_ERR_ARG, "eps %g or lr %g is not a number >= 0", h.eps, h.lr);
+  if (h.step_device ? h.step != 0 : (h.step < 1 || h.step > INT64_C(0x7FFFFFFF)))
+    return fail(FP8MI_ERR_ARG, "step %lld: a number from 1 on, or 0 with step_device", (long long)h.step);
+  if (h.lr_device && !h.step_device) return fail(FP8MI_ERR_ARG, "lr_device needs step_device");
+  if (!aligned4(h.step_device) || !aligned4(h.lr_device) || !aligned4(h.grad_scale))
+    return fail(FP8MI_ERR_ARG, "device words must be 4-byte aligned");
+  for (int i = 0; i < count; ++i) {
+    const fp8mi_adamw_tensor& t = tensors[i];
+    fp8mi_status s = check_elements("param", i, t.param, t.n, t.param_dtype);
+    if (s == FP8MI_OK) s = check_elements("grad", i, t.grad, t.n, t.grad_dtype);
+    if (s != FP8MI_OK) return s;
+    if (t.state_bits != 32 && t.state_bits != 8)
+      return fail(FP8MI_ERR_ENUM, "tensor %d: state_bits %d is not 32/8", i, t.state_bits);
+    const bool bytes = t.state_bits == 8;
+    if (t.n > 0 && (!t.exp_avg || !t.exp_avg_sq || (bytes && (!t.exp_avg_scale || !t.exp_avg_sq_scale))))
+      return fail(FP8MI_ERR_NULL, "tensor %d: a state or its scales are NULL", i);
+    if (!bytes && (t.exp_avg_scale || t.exp_avg_sq_scale))
+      return fail(FP8MI_ERR_ARG, "tensor %d: scales belong to 8-bit states", i);
+    if (t.master && t.param_dtype == FP8MI_F32)
+      return fail(FP8MI_ERR_ARG, "tensor %d: an fp32 param is its own master", i);
+    if (!aligned4(t.master) || !aligned4(t.exp_avg_scale) || !aligned4(t.exp_avg_sq_scale) ||
+        (!bytes && (!aligned4(t.exp_avg) || !aligned4(t.exp_avg_sq))))
+      return fail(FP8MI_ERR_ARG, "tensor %d: masters, fp32 states and scales must be 4-byte aligned", i);
+    if (!(t.weight_decay >= 0.0f)) return fail(FP8MI_ERR_ARG, "tensor %d: weight_decay %g", i, (double)t.weight_decay);
+  }
+  AdamWHyper a;
+  a.lr = (float)h.lr; a.beta1 = (float)h.beta1; a.beta2 = (float)h.beta2;
+  a.one_beta1 = (float)(1.0 - h.beta1); a.one_beta2 = (float)(1.0 - h.beta2); a.eps = (float)h.eps;
+  a.t = (uint32_t)h.step; a.seed = h.seed;
+  a.step_size = a.root_scale = 0.0f;
+  if (!h.step_device) {
+    a.step_size = (float)(h.lr / (1.0 - pow(h.beta1, (double)h.step)));
+    a.root_scale = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
+  }
+  a.grad_scale = h.grad_scale; a.step_words = h.step_device; a.lr_word = h.lr_device;
+  return from_hip(launch_adamw(tensors, count, a, h.beta1, h.beta2, static_cast<hipStream_t>(stream)), "adamw launch");
+}
+
+size_t fp8_grad_norm_workspace_bytes(const fp8mi_norm_tensor* tensors, int32_t count) {
+  if (!tensors || count <= 0) return 0;
+  for (int i = 0; i < count; ++i)
+    if (tensors[i].n < 0 || tensors[i].n > (INT64_C(1) << 42)) return 0;
+  return (size_t)grad_norm_workspace_bytes(tensors, count);
+}
+
+fp8mi_status fp8_grad_norm(const fp8mi_norm_tensor* tensors, int32_t count, const float* max_norm, float* norm_out,
+                           float* clip_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (count < 0) return fail(FP8MI_ERR_SHAPE, "count %d", count);
+  if (count > 0 && !tensors) return fail(FP8MI_ERR_NULL, "tensors is NULL");
+  if (max_norm && !(*max_norm >= 0.0f)) return fail(FP8MI_ERR_ARG, "max_norm %g is not a number >= 0", (double)*max_norm);
+  if (!aligned4(norm_out) || !aligned4(clip_out)) return fail(FP8MI_ERR_ARG, "fp32 outputs must be 4-byte aligned");
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    const fp8mi_status s = check_elements("grad", i, tensors[i].grad, tensors[i].n, tensors[i].dtype);
+    if (s != FP8MI_OK) return s;
+    total += tensors[i].n;
+    if (total > (INT64_C(1) << 42)) return fail(FP8MI_ERR_SHAPE, "more than 2^42 elements");
+  }
+  const size_t need = fp8_grad_norm_workspace_bytes(tensors, count);
+  if (need > 0 && !workspace) return fail(FP8MI_ERR_NULL, "workspace is NULL (%zu bytes needed)", need);
+  if (workspace_bytes < need)
+    return fail(FP8MI_ERR_ARG, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 7u) return fail(FP8MI_ERR_ARG, "workspace must be 8-byte aligned");
+  return from_hip(launch_grad_norm(tensors, count, max_norm ? *max_norm : -1.0f, norm_out, clip_out,
+                                   static_cast<double*>(workspace), static_cast<hipStream_t>(stream)),
+                  "gradient norm launch");
 }
 
 fp8mi_status fp8_ring_seed(uint32_t* ring, int32_t hist_len, const float* amax, int fmt, void* stream) {

@@ -2,6 +2,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include "../../include/fp8mi.h"
 
 namespace fp8mi {
 
@@ -174,20 +175,7 @@ struct NormGradArgs {
 int64_t rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_grad(const NormGradArgs& p, int dt, float* dweight, void* workspace, hipStream_t st);
 
-// AdamW (adamw.hip).  A launch's table of tensors is in its kernel arguments.
-constexpr int kAdamWTensors = 44, kNormTensors = 128;
-struct AdamWTensor {
-  void* param;
-  const void* grad;
-  float* master;                  // fp32 weights that param is rounded from, or null
-  void* m;                        // fp32, or E4M3 codes (bytes)
-  void* v;                        // fp32, or E4M3 codes of sqrt(v)
-  float* m_scale;                 // one per block of 256 elements (bytes)
-  float* v_scale;
-  int64_t n;
-  int32_t param_dt, grad_dt, bytes;
-  float weight_decay;
-};
+// AdamW and the gradient norm (adamw.hip), over the ABI's own tensor lists.
 struct AdamWHyper {
   float lr, beta1, beta2, one_beta1, one_beta2, eps;  // one_beta: 1 - beta
   float step_size, root_scale;    // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
@@ -196,16 +184,11 @@ struct AdamWHyper {
   uint32_t* step_words;           // a step counted on the device, or null
   const float* lr_word;           // lr on the device (with step_words), or null
 };
-hipError_t launch_adamw(const AdamWTensor* tensors, int count, const AdamWHyper& h, double beta1, double beta2,
+hipError_t launch_adamw(const fp8mi_adamw_tensor* tensors, int count, const AdamWHyper& h, double beta1, double beta2,
                         hipStream_t st);
-struct NormTensor {
-  const void* grad;
-  int64_t n;
-  int32_t dt;
-};
-int64_t grad_norm_workspace_bytes(const NormTensor* tensors, int count);
+int64_t grad_norm_workspace_bytes(const fp8mi_norm_tensor* tensors, int count);
 // max_norm < 0: no clipping; out, clip: one word each, or null.
-hipError_t launch_grad_norm(const NormTensor* tensors, int count, float max_norm, float* out, float* clip,
+hipError_t launch_grad_norm(const fp8mi_norm_tensor* tensors, int count, float max_norm, float* out, float* clip,
                             double* parts, hipStream_t st);
 
 hipError_t launch_ring_seed(uint32_t* ring, int H, const float* amax, int fmt, hipStream_t st);

@@ -468,6 +468,87 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * fp8_adamw_step -- one AdamW step over `count` tensors (the weights that the
+ * gradients of fp8 layers arrive at), a launch for each 44 of them:
+ *   g = c grad                     m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32; w is the tensor's master where it has one, and param = w rounded once.
+ *   tensors    HOST array, read before the call returns (so are the hyper
+ *              parameters).  Per tensor, all device pointers:
+ *     param, grad   n elements of FP8MI_F32 / F16 / BF16 each, any element-aligned base.
+ *     master        fp32 [n], or NULL; not with an fp32 param.
+ *     state_bits    32: exp_avg, exp_avg_sq are fp32 [n]; the scales are NULL.
+ *                   8: they are E4M3 codes [n] of m and of sqrt(v); the scales fp32
+ *                   [ceil(n / 256)], one per 256 elements: m = dec(code) scale,
+ *                   v = (dec(code) scale)^2.  Zeros (codes and scales) to begin with.
+ *                   Codes are rounded stochastically, so that m and v are met on
+ *                   average (rounded to nearest, an average would stand still
+ *                   once it changes by less than half a code step); a v above
+ *                   zero never becomes zero.  The random numbers go by seed, step,
+ *                   the tensor's place in the array and the element's in the tensor
+ *                   alone: a step is the same every time.  A block that holds an
+ *                   infinity or a NaN decodes as such.
+ *     weight_decay  of this tensor.
+ *   step       t >= 1, this step's number, or with step_device 0: the device's count.
+ *   step_device  NULL, or device uint32 [FP8MI_ADAMW_STEP_WORDS], word 0 the steps
+ *              done so far (the rest scratch): the call counts the step itself, so a
+ *              captured call advances with every replay (one more launch).
+ *   lr_device  NULL, or (with step_device) device fp32 in lr's place.
+ *   grad_scale NULL, or device fp32 c (fp8_grad_norm's clip).  Not finite: the step
+ *              is skipped -- parameters, masters, states and step_device stay.
+ * Tensors of n == 0 are allowed.  No two tensors may share memory.
+ */
+#define FP8MI_ADAMW_STEP_WORDS 4
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t state_bits;
+  float weight_decay;
+} fp8mi_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint32_t* step_device;
+  const float* lr_device;
+  const float* grad_scale;
+  uint32_t seed;
+} fp8mi_adamw;
+FP8MI_API fp8mi_status fp8_adamw_step(const fp8mi_adamw_tensor* tensors, int32_t count, const fp8mi_adamw* hyper,
+                                      void* stream);
+
+/*
+ * fp8_grad_norm -- the Euclidean norm of all elements of `count` gradients, and
+ * the factor that brings it down to max_norm:
+ *   norm = sqrt(sum g^2)           clip = min(1, max_norm / (norm + 1e-6))
+ * Squares are added in fp64 in an order that the sizes fix: the same every call.
+ *   tensors    HOST array: device pointer, element count, FP8MI_F32 / F16 / BF16.
+ *   max_norm   HOST pointer to one fp32 >= 0, or NULL (clip is then 1).
+ *   norm_out, clip_out  device fp32, either NULL.  clip is NaN where the norm is not
+ *              finite (fp8_adamw_step skips such a step).
+ *   workspace  device scratch of fp8_grad_norm_workspace_bytes bytes, 8-byte aligned,
+ *              no initialisation; calls in flight on one workspace race.
+ * Two launches (one more for each further 128 tensors).  No gradients: norm 0.
+ */
+typedef struct {
+  const void* grad;
+  int64_t n;
+  int32_t dtype;
+} fp8mi_norm_tensor;
+FP8MI_API fp8mi_status fp8_grad_norm(const fp8mi_norm_tensor* tensors, int32_t count, const float* max_norm,
+                                     float* norm_out, float* clip_out, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+FP8MI_API size_t fp8_grad_norm_workspace_bytes(const fp8mi_norm_tensor* tensors, int32_t count);
+
+/*
  * fp8_ring_seed -- (re)initialise a ring on the device: history, ticket and
  * scratch set to 0, slot 0, and current scale = the scale a fold of *amax
  * into an empty window would publish (fmt_max / amax, or 1.0 when amax is 0
