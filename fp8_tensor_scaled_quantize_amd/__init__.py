@@ -20,7 +20,8 @@ __all__ = ["E4M3", "E5M2", "F32", "F16", "BF16", "Fp8Error", "fp8_quantize", "fp
            "fp8_quantize_dual_bias_grad_noalloc", "NOALLOC_SCRATCH_BYTES", "stream_reference",
            "fp8_quantize_dynamic", "DYNAMIC_WORKSPACE_BYTES", "fp8_amax_fold", "fp8_mm", "fp8_mm_ex", "FP8_E4M3", "FP8_E5M2", "fp8_bias_grad", "fp8_bias_grad_workspace_bytes", "fp8_ring_seed", "new_ring", "ring_words", "version",
            "fp8_rmsnorm", "fp8_rmsnorm_grad", "fp8_rmsnorm_grad_workspace_bytes", "fp8_mm_act", "fp8_act_grad",
-           "fp8_adamw_step", "fp8_grad_norm", "ADAMW_BLOCK", "ADAMW_STEP_WORDS",
+           "fp8_cross_entropy", "fp8_cross_entropy_grad", "fp8_cross_entropy_workspace_bytes",
+           "fp8_cross_entropy_grad_workspace_bytes", "fp8_adamw_step", "fp8_grad_norm", "ADAMW_BLOCK", "ADAMW_STEP_WORDS",
            "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_SILU", "interleave_gated"]
 
 E4M3, E5M2 = 0, 1
@@ -804,6 +805,102 @@ def fp8_act_grad(dy: torch.Tensor, z: torch.Tensor, act, gated: bool = False, fm
     if status:
         _check(status)
     return out_row, out_t, bias_grad_out
+
+
+# ------------------------------------------------------------------ loss
+def fp8_cross_entropy_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Device workspace fp8_cross_entropy needs."""
+    return int(lib().fp8_cross_entropy_workspace_bytes(M, N, K))
+
+
+def fp8_cross_entropy_grad_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Device workspace fp8_cross_entropy_grad needs."""
+    return int(lib().fp8_cross_entropy_grad_workspace_bytes(M, N, K))
+
+
+_TARGET_BITS = {torch.int64: 64, torch.int32: 32}
+
+
+def _xent_operands(a, b, targets):
+    if a.dtype is not torch.uint8:
+        a = _as_codes(a, "a")
+    if b.dtype is not torch.uint8:
+        b = _as_codes(b, "b")
+    _, M, K, lda = _rows2d(a, "a")
+    _, N, Kb, ldb = _rows2d(b, "b")
+    if K != Kb:
+        raise ValueError(f"K mismatch: {tuple(a.shape)} vs {tuple(b.shape)}")
+    return a, b, M, N, K, lda, ldb, _typed_vector(targets, M, "targets", _TARGET_BITS)
+
+
+def fp8_cross_entropy(a: torch.Tensor, b: torch.Tensor, targets: torch.Tensor, a_scale_inv: torch.Tensor | None = None,
+                      b_scale_inv: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, mean_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None):
+    """Softmax cross entropy of E4M3 rows A [M, K] against a vocabulary's E4M3
+    weights B [N, K], without writing the logits A B^T sa sb: returns (loss [M],
+    lse [M]), fp32.  The scale multipliers hold one word, or one per row of their
+    operand.  targets [M], int64 or int32: a negative one ignores its row (loss
+    0).  mean_out (fp32 [2]) receives the mean over the other rows and 1 / their
+    number."""
+    a, b, M, N, K, lda, ldb, bits = _xent_operands(a, b, targets)
+    rows = _row_scales(a_scale_inv, M, "a_scale_inv") | (_row_scales(b_scale_inv, N, "b_scale_inv") << 1)
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=a.device)
+    if lse is None:
+        lse = torch.empty(M, dtype=torch.float32, device=a.device)
+    _typed_vector(loss, M, "loss", _F32_ONLY)
+    _typed_vector(lse, M, "lse", _F32_ONLY)
+    if mean_out is not None:
+        _typed_vector(mean_out, 2, "mean_out", _F32_ONLY)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(max(L.fp8_cross_entropy_workspace_bytes(M, N, K), 16), dtype=torch.uint8, device=a.device)
+    _on_device(a, b, targets, a_scale_inv, b_scale_inv, loss, lse, mean_out, workspace)
+    status = L.fp8_cross_entropy(
+        a.data_ptr(), lda, b.data_ptr(), ldb, M, N, K, None if a_scale_inv is None else a_scale_inv.data_ptr(),
+        None if b_scale_inv is None else b_scale_inv.data_ptr(), rows, targets.data_ptr(), bits, loss.data_ptr(),
+        lse.data_ptr(), None if mean_out is None else mean_out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(a))
+    if status:
+        _check(status)
+    return loss, lse
+
+
+def fp8_cross_entropy_grad(a: torch.Tensor, b: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                           dloss: torch.Tensor, a_scale_inv: torch.Tensor | None = None,
+                           b_scale_inv: torch.Tensor | None = None, da: torch.Tensor | None = None,
+                           db: torch.Tensor | None = None, need_da: bool = True, need_db: bool = True,
+                           workspace: torch.Tensor | None = None):
+    """Gradient of sum dloss * loss of fp8_cross_entropy (one scale per operand)
+    with respect to A sa and B sb: returns (da bf16 [M, K], db bf16 [N, K]; None
+    where not needed).  lse is the forward call's, dloss fp32 [M] or one word for
+    all rows."""
+    a, b, M, N, K, lda, ldb, bits = _xent_operands(a, b, targets)
+    for t, name in ((a_scale_inv, "a_scale_inv"), (b_scale_inv, "b_scale_inv")):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() != 1):
+            raise ValueError(f"{name} must be a float32 tensor of 1 element (the gradient takes no row scales)")
+    _typed_vector(lse, M, "lse", _F32_ONLY)
+    per_row = _row_scales(dloss, M, "dloss")
+    if da is None and need_da:
+        da = torch.empty((M, K), dtype=torch.bfloat16, device=a.device)
+    if db is None and need_db:
+        db = torch.empty((N, K), dtype=torch.bfloat16, device=a.device)
+    ld_da = 0 if da is None else _ld(da, (M, K), torch.bfloat16, "da")
+    ld_db = 0 if db is None else _ld(db, (N, K), torch.bfloat16, "db")
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(max(L.fp8_cross_entropy_grad_workspace_bytes(M, N, K), 16), dtype=torch.uint8,
+                                device=a.device)
+    _on_device(a, b, targets, lse, dloss, a_scale_inv, b_scale_inv, da, db, workspace)
+    status = L.fp8_cross_entropy_grad(
+        a.data_ptr(), lda, b.data_ptr(), ldb, M, N, K, None if a_scale_inv is None else a_scale_inv.data_ptr(),
+        None if b_scale_inv is None else b_scale_inv.data_ptr(), targets.data_ptr(), bits, lse.data_ptr(),
+        dloss.data_ptr(), per_row, None if da is None else da.data_ptr(), ld_da, None if db is None else db.data_ptr(),
+        ld_db, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(a))
+    if status:
+        _check(status)
+    return da, db
 
 
 # ------------------------------------------------------------------ optimizer

@@ -34,6 +34,12 @@ SIGNATURES = {
     "fp8_rmsnorm_grad": (C.c_int, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, _P, _P, _I64, _P, _I64, _P, _P,
                                    C.c_size_t, _P]),
     "fp8_rmsnorm_grad_workspace_bytes": (C.c_size_t, [_I64, _I64]),
+    "fp8_cross_entropy": (C.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _I, _P, _P, _P, _P, C.c_size_t,
+                                    _P]),
+    "fp8_cross_entropy_workspace_bytes": (C.c_size_t, [_I64, _I64, _I64]),
+    "fp8_cross_entropy_grad": (C.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I, _P, _P, _I, _P, _I64, _P,
+                                         _I64, _P, C.c_size_t, _P]),
+    "fp8_cross_entropy_grad_workspace_bytes": (C.c_size_t, [_I64, _I64, _I64]),
     "fp8_adamw_step": (C.c_int, [_P, _I32, _P, _P]),
     "fp8_grad_norm": (C.c_int, [_P, _I32, _P, _P, _P, _P, C.c_size_t, _P]),
     "fp8_grad_norm_workspace_bytes": (C.c_size_t, [_P, _I32]),

@@ -18,7 +18,7 @@ SOURCES = ["abi.hip", "quantize.hip", "mm_fp8.hip", "mm_fp8_q8.hip", "mm_fp8_km.
            "mm_fp8_km_q8_b.hip", "mm_fp8_km_q8_ab.hip", "mm_fp8_prec.hip", "mm_fp8_prec_km.hip", "mm_fp8_prec_q8.hip",
            "mm_fp8_prec_km_q8.hip", "mm_act_bf16.hip", "mm_act_bf16_gated.hip",
            "mm_act_q8.hip", "mm_act_q8_gated.hip", "act_grad.hip", "grad_bias.hip", "rmsnorm.hip", "stream.hip",
-           "adamw.hip"]
+           "adamw.hip", "cross_entropy.hip", "xent_mm_logits.hip", "xent_mm_grads.hip"]
 LIB = os.path.join(PKG, "libfp8mi.so")
 
 HIPCC_FLAGS = [

@@ -641,6 +641,91 @@ fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t c
                   "rmsnorm gradient launch");
 }
 
+// Sizes that the cross entropy's kernels and 32-bit offsets cover.
+static fp8mi_status check_xent_size(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 1 || K < 1)
+    return fail(FP8MI_ERR_SHAPE, "M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+  if (K % 16 || K > 65536 || M > (1 << 20) || M > (INT64_C(1) << 30) / K - 1 || N > INT64_C(0x7FFFFFFF))
+    return fail(FP8MI_ERR_UNSUPPORTED, "M=%lld N=%lld K=%lld: K is a multiple of 16 up to 65536, M at most 2^20, M K below "
+                "2^30, N below 2^31", (long long)M, (long long)N, (long long)K);
+  return FP8MI_OK;
+}
+
+static fp8mi_status check_xent(const XentCall& c, int target_bits, const void* workspace, size_t workspace_bytes,
+                               size_t need) {
+  const fp8mi_status s = check_xent_size(c.M, c.N, c.K);
+  if (s != FP8MI_OK) return s;
+  if (target_bits != 32 && target_bits != 64) return fail(FP8MI_ERR_ENUM, "target_bits %d is not 32/64", target_bits);
+  if (!aligned4(c.a_scale_inv) || !aligned4(c.b_scale_inv)) return fail(FP8MI_ERR_ARG, "fp32 scales must be 4-byte aligned");
+  if (c.M == 0) return FP8MI_OK;
+  if (!c.a || !c.b || !c.targets) return fail(FP8MI_ERR_NULL, "a, b or targets is NULL");
+  if (c.lda < c.K || c.ldb < c.K)
+    return fail(FP8MI_ERR_SHAPE, "lda %lld / ldb %lld < K %lld", (long long)c.lda, (long long)c.ldb, (long long)c.K);
+  if (!span_ok(c.M, c.lda, 1) || !span_ok(c.N, c.ldb, 1))
+    return fail(FP8MI_ERR_SHAPE, "an operand's extent is beyond 2^62 bytes");
+  if ((c.lda % 16) || (c.ldb % 16) || (reinterpret_cast<uintptr_t>(c.a) & 15u) || (reinterpret_cast<uintptr_t>(c.b) & 15u))
+    return fail(FP8MI_ERR_UNSUPPORTED, "a and b must be 16-byte aligned, lda and ldb multiples of 16");
+  if (reinterpret_cast<uintptr_t>(c.targets) % (target_bits / 8)) return fail(FP8MI_ERR_ARG, "targets not aligned to their size");
+  if (!workspace) return fail(FP8MI_ERR_NULL, "workspace is NULL (%zu bytes needed)", need);
+  if (workspace_bytes < need) return fail(FP8MI_ERR_ARG, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 15u) return fail(FP8MI_ERR_ARG, "workspace must be 16-byte aligned");
+  return FP8MI_OK;
+}
+
+size_t fp8_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && check_xent_size(M, N, K) == FP8MI_OK ? (size_t)xent_workspace_bytes(M, N, K) : 0;
+}
+
+size_t fp8_cross_entropy_grad_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && check_xent_size(M, N, K) == FP8MI_OK ? (size_t)xent_grad_workspace_bytes(M, N, K) : 0;
+}
+
+fp8mi_status fp8_cross_entropy(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M, int64_t N,
+                               int64_t K, const float* a_scale_inv, const float* b_scale_inv, int scale_rows,
+                               const void* targets, int target_bits, float* loss, float* lse, float* mean_out,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (scale_rows < 0 || scale_rows > 3)
+    return fail(FP8MI_ERR_ENUM, "scale_rows %d is not a combination of FP8MI_A_ROW_SCALES / FP8MI_B_ROW_SCALES", scale_rows);
+  XentCall c;
+  c.a = a; c.b = b; c.lda = lda; c.ldb = ldb; c.M = M; c.N = N; c.K = K;
+  c.a_scale_inv = a_scale_inv; c.b_scale_inv = b_scale_inv;
+  c.a_rows = (scale_rows & FP8MI_A_ROW_SCALES) != 0; c.b_rows = (scale_rows & FP8MI_B_ROW_SCALES) != 0;
+  c.targets = targets; c.target_bits = target_bits; c.ws = static_cast<uint8_t*>(workspace);
+  c.loss = loss; c.lse = lse; c.mean = mean_out;
+  if ((c.a_rows && !a_scale_inv) || (c.b_rows && !b_scale_inv))
+    return fail(FP8MI_ERR_NULL, "row scales are announced but their array is NULL");
+  const fp8mi_status s = check_xent(c, target_bits, workspace, workspace_bytes, fp8_cross_entropy_workspace_bytes(M, N, K));
+  if (s != FP8MI_OK) return s;
+  if (M > 0 && (!loss || !lse)) return fail(FP8MI_ERR_NULL, "loss or lse is NULL");
+  if (!aligned4(loss) || !aligned4(lse) || !aligned4(mean_out))
+    return fail(FP8MI_ERR_ARG, "loss, lse and mean_out must be 4-byte aligned");
+  return from_hip(launch_xent_forward(c, static_cast<hipStream_t>(stream)), "cross entropy launch");
+}
+
+fp8mi_status fp8_cross_entropy_grad(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M, int64_t N,
+                                    int64_t K, const float* a_scale_inv, const float* b_scale_inv, const void* targets,
+                                    int target_bits, const float* lse, const float* dloss, int dloss_rows, void* da,
+                                    int64_t ld_da, void* db, int64_t ld_db, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (dloss_rows != 0 && dloss_rows != 1) return fail(FP8MI_ERR_ENUM, "dloss_rows %d is not 0/1", dloss_rows);
+  XentCall c;
+  c.a = a; c.b = b; c.lda = lda; c.ldb = ldb; c.M = M; c.N = N; c.K = K;
+  c.a_scale_inv = a_scale_inv; c.b_scale_inv = b_scale_inv;
+  c.targets = targets; c.target_bits = target_bits; c.ws = static_cast<uint8_t*>(workspace);
+  c.lse = const_cast<float*>(lse); c.dloss = dloss; c.dloss_rows = dloss_rows;
+  c.da = static_cast<uint16_t*>(da); c.db = static_cast<uint16_t*>(db); c.ld_da = ld_da; c.ld_db = ld_db;
+  fp8mi_status s = check_xent(c, target_bits, workspace, workspace_bytes, fp8_cross_entropy_grad_workspace_bytes(M, N, K));
+  if (s != FP8MI_OK) return s;
+  if (M > 0 && (!lse || !dloss)) return fail(FP8MI_ERR_NULL, "lse or dloss is NULL");
+  if (!aligned4(lse) || !aligned4(dloss)) return fail(FP8MI_ERR_ARG, "lse and dloss must be 4-byte aligned");
+  s = check_matrix("da", da, false, FP8MI_BF16, M, K, ld_da);
+  if (s != FP8MI_OK) return s;
+  s = check_matrix("db", db, false, FP8MI_BF16, N, K, ld_db);
+  if (s != FP8MI_OK) return s;
+  if (!da && !db) return FP8MI_OK;
+  return from_hip(launch_xent_backward(c, static_cast<hipStream_t>(stream)), "cross entropy gradient launch");
+}
+
 // One tensor of a list: n elements of dtype at p.
 static fp8mi_status check_elements(const char* name, int i, const void* p, int64_t n, int dt) {
   if (!valid_dtype(dt)) return fail(FP8MI_ERR_ENUM, "tensor %d: %s dtype %d is not F32/F16/BF16", i, name, dt);

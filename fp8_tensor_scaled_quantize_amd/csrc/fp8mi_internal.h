@@ -33,7 +33,12 @@ hipError_t launch_quantize_dynamic(const void* x, int dt, int64_t rows, int64_t 
 hipError_t launch_amax_fold(uint32_t* ring, int H, const float* amax, int fmt, hipStream_t st);
 
 struct MmArgs {
-  static constexpr bool kAct = false;  // the plain epilogue
+  static constexpr bool kAct = false;   // the plain epilogue
+  static constexpr bool kTail = false;  // no epilogue of its own (mm_fp8_kernel.h)
+  struct Rows {};
+  template <int BM, int BN> static constexpr int extra_bytes() { return 0; }
+  __host__ __device__ static int64_t k_rows(const MmArgs& p) { return p.K; }
+  __host__ __device__ static int64_t k_bytes(const MmArgs& p, int64_t) { return p.K; }  // of one batch's sums
   const uint8_t* a = nullptr;
   const uint8_t* b = nullptr;
   int64_t lda = 0, ldb = 0, stride_a = 0, stride_b = 0;
@@ -174,6 +179,33 @@ struct NormGradArgs {
 };
 int64_t rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_grad(const NormGradArgs& p, int dt, float* dweight, void* workspace, hipStream_t st);
+
+// Softmax cross entropy over a vocabulary (cross_entropy.hip).
+struct XentCall {
+  const uint8_t* a = nullptr;     // E4M3 codes [M, K]
+  const uint8_t* b = nullptr;     // E4M3 codes [N, K]
+  int64_t lda = 0, ldb = 0, M = 0, N = 0, K = 0;
+  const float* a_scale_inv = nullptr;
+  const float* b_scale_inv = nullptr;
+  int a_rows = 0, b_rows = 0;
+  const void* targets = nullptr;
+  int target_bits = 64;
+  uint8_t* ws = nullptr;
+  // forward
+  float* loss = nullptr;
+  float* lse = nullptr;           // [M]; the gradient's input
+  float* mean = nullptr;          // [2], or null
+  // gradient
+  const float* dloss = nullptr;
+  int dloss_rows = 0;
+  uint16_t* da = nullptr;
+  uint16_t* db = nullptr;
+  int64_t ld_da = 0, ld_db = 0;
+};
+int64_t xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int64_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_xent_forward(const XentCall& c, hipStream_t st);
+hipError_t launch_xent_backward(const XentCall& c, hipStream_t st);
 
 // AdamW and the gradient norm (adamw.hip), over the ABI's own tensor lists.
 struct AdamWHyper {

@@ -8,6 +8,7 @@
 namespace fp8mi {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kBK = 128;
@@ -113,6 +114,52 @@ __device__ __forceinline__ float load_bias(const MmArgs& p, int64_t j, float bsc
   return decode_bias(p, load_bias_bits(p, j), bscale);
 }
 
+// Operands of 16 bits (bf16), for products whose sums fp8's in-group truncation
+// (below) would spoil: the same tile in bytes, a step of 128 bytes being 64 k,
+// with leading dimensions, K and strides in bytes too.
+constexpr int kOpBF16 = 8;
+template <int F> constexpr int kOpBytes = F == kOpBF16 ? 2 : 1;
+
+// K-major tiles of 16-bit operands: 64 k-rows of 2 W bytes.  A fragment's 16
+// columns are 32 contiguous bytes, so 32-byte granules are rotated: a half-wave of
+// a fragment read touches k-rows 16 g + 4 q + j, g of two, j < 4, and
+// rot = j + 4 (g & 1) puts them on the eight granules of the 64 banks.
+template <int W> __device__ __forceinline__ int km16_granule(int c32, int kr) {
+  return (c32 + (kr & 3) + (((kr >> 4) & 1) << 2)) % (W / 16);
+}
+
+// Fragment (lane l: tile column rb + l%16, k = 16(l/16) .. +15, as a row-major
+// fragment's 32 bytes) with ds_read_b64_tr_b16.  Measured lane layout: within
+// each group of 16 lanes, output lane i receives in element j element i % 4 of
+// the 8 bytes addressed by lane 4j + i / 4.
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s_ptr;
+template <int W> __device__ __forceinline__ v8i lds_frag_km16(const uint8_t* S, int rb, int lane) {
+  const int g = lane >> 4, a = lane & 15, j = a >> 2, h = a & 3;
+  v8i r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int kr = 16 * g + 4 * q + j;
+    const v4s d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_v4s_ptr)(S + kr * (2 * W) + km16_granule<W>(rb >> 4, kr) * 32 + 8 * h));
+    const v2i w = __builtin_bit_cast(v2i, d);
+    r[2 * q] = w[0];
+    r[2 * q + 1] = w[1];
+  }
+  return r;
+}
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ v4f mfma_bf16(const v8i& bfrag, const v8i& afrag, v4f c) {
+#pragma unroll
+  for (int h = 0; h < 8; h += 4) {
+    const v4i b = {bfrag[h], bfrag[h + 1], bfrag[h + 2], bfrag[h + 3]};
+    const v4i a = {afrag[h], afrag[h + 1], afrag[h + 2], afrag[h + 3]};
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b), __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
+  }
+  return c;
+}
+
 template <int FA, int FB>
 __device__ __forceinline__ v4f mfma_nt(const v8i& bfrag, const v8i& afrag, const v4f& c) {
   // first operand: B rows (format FB -> cbsz), second: A rows (format FA -> blgp).
@@ -149,7 +196,9 @@ __device__ __forceinline__ v8i spread_dword(const v8i& f, int s) {
 
 template <int FA, int FB, bool PREC>
 __device__ __forceinline__ v4f mma(const v8i& bfrag, const v8i& afrag, v4f c) {
-  if constexpr (!PREC) {
+  if constexpr (FA == kOpBF16) {
+    return mfma_bf16(bfrag, afrag, c);
+  } else if constexpr (!PREC) {
     return mfma_nt<FA, FB>(bfrag, afrag, c);
   } else {
 #pragma unroll
@@ -177,7 +226,6 @@ __device__ __forceinline__ v4f mma(const v8i& bfrag, const v8i& afrag, v4f c) {
 // A and B panels in that XCD's L2.
 // ===========================================================================
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef int v4i __attribute__((ext_vector_type(4)));
 
 // Raw buffer resource over `bytes` bytes from `base` (stride 0, dword3 as for
 // all gfx9 raw buffers); reads at offsets >= bytes return zero.
@@ -300,6 +348,9 @@ template <int FA, int FB, int BM, int BN, int WAVES_M, int WAVES_N, int OUT, int
 __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int64_t n0, const int64_t bz,
                                         uint8_t* pool) {
   constexpr bool KMA = (LAY & 1) != 0, KMB = (LAY & 2) != 0;
+  constexpr int EB = kOpBytes<FA>;  // bytes per operand element
+  static_assert(FA == FB || EB == kOpBytes<FB>, "operands of one width");
+  static_assert(EB == 1 || !KMB, "a 16-bit B is given by rows");
   constexpr int NWAVES = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   constexpr int TI = WM / 16, TJ = WN / 16;
@@ -331,7 +382,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   const int wm = wid / WAVES_N, wn = wid % WAVES_N;
   const int ext_a = (int)(KMA ? p.a_extent_km(m0) : p.a_extent_from(m0));
   const int ext_b = (int)(KMB ? p.b_extent_km(n0) : p.b_extent_from(n0));
-  const v4i rsa = buffer_rsrc(p.a + bz * p.stride_a + (KMA ? m0 : m0 * p.lda), ext_a);
+  const v4i rsa = buffer_rsrc(p.a + bz * p.stride_a + (KMA ? EB * m0 : m0 * p.lda), ext_a);
   const v4i rsb = buffer_rsrc(p.b + bz * p.stride_b + (KMB ? n0 : n0 * p.ldb), ext_b);
   // Lane l of a 1 KiB load fills LDS row r0 + l/8 (r0 a multiple of 8) at
   // chunk position l%8, so it fetches logical chunk (l%8) ^ swz(l/8).
@@ -339,12 +390,22 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   // unsigned: offsets of rows past the edge may wrap; those rows' outputs are never stored
   const uint32_t lda = (uint32_t)p.lda, ldb = (uint32_t)p.ldb;
   const uint32_t va = lr * lda + 16 * lc, vb = lr * ldb + 16 * lc;
-  const int K = (int)p.K;
+  const int K = (int)P::k_bytes(p, bz);
   // K-major operands: load instruction ii fills LDS chunks 64 ii .. 64 ii + 63
   // of the stage; lane l's chunk q = 64 ii + l is position q % CPR of k-row
   // q / CPR, so it fetches the chunk c whose km_pos is that position.  The
   // step's k0 enters as the scalar offset k0 * ld.
   constexpr int CPR_A = BM / 16, CPR_B = BN / 16;
+
+  // 16-bit operands: lane l's chunk is half (q % 2) of the granule that
+  // km16_granule places there.
+  auto km16_offset = [&](int qq, int k0) -> uint32_t {  // past k_rows: beyond the extent
+    constexpr int CPR = BM / 8, G = BM / 16;
+    const int kr = qq / CPR, pos = (qq % CPR) >> 1;
+    const int rot = ((kr & 3) + (((kr >> 4) & 1) << 2)) % G;
+    const uint32_t c = (uint32_t)((pos + G - rot) % G);
+    return k0 / 2 + kr >= P::k_rows(p) ? (uint32_t)ext_a : (uint32_t)kr * lda + 32 * c + 16 * (qq & 1);
+  };
 
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
 
@@ -361,7 +422,13 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   if constexpr (P::kAct) {
     if (p.b_scale_inv && tid < BN) col_scale = p.b_scale_inv[p.b_rows ? (n0 + tid < p.N ? n0 + tid : n0) : 0];
   }
+  typename P::Rows rows_pre;  // an epilogue of its own: what it needs of the tile's rows and columns
+  if constexpr (P::kTail) P::template fetch<BM, BN>(p, rows_pre, tid, m0, n0);
   auto park_bias = [&]() {
+    if constexpr (P::kTail) {
+      P::template park<BM, BN>(p, rows_pre, tid, pool + Lds::kSmem);
+      return;
+    }
     if constexpr (P::kAct) {
       if (tid < BN) reinterpret_cast<float*>(pool + Lds::kActCol)[tid] = col_scale;
     }
@@ -380,7 +447,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
 #pragma unroll
     for (int q = 0; q < (LA > LB ? LA : LB); ++q) {
       if (q < LA) {
-        if constexpr (KMA) {
+        if constexpr (KMA && EB == 2) {
+          dma16(rsa, as + (wid * LA + q) * 1024, (int)km16_offset((wid * LA + q) * 64 + lane, k0),
+                (int)((uint32_t)(k0 / 2) * lda));
+        } else if constexpr (KMA) {
           const int qq = (wid * LA + q) * 64 + lane;
           const int kr = qq / CPR_A, pos = qq % CPR_A;  // k-row within the step; rows past K read zero
           const int rot = ((kr & 7) + (((kr >> 5) & 1) << 3)) % CPR_A;
@@ -419,7 +489,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
 #pragma unroll
     for (int q = c * LPW / NCH; q < (c + 1) * LPW / NCH; ++q) {
       if (q < LA) {
-        if constexpr (KMA) {
+        if constexpr (KMA && EB == 2) {
+          dma16(rsa, as + (wid * LA + q) * 1024, (int)km16_offset((wid * LA + q) * 64 + lane, k0),
+                (int)((uint32_t)(k0 / 2) * lda));
+        } else if constexpr (KMA) {
           const int qq = (wid * LA + q) * 64 + lane;
           const int kr = qq / CPR_A, pos = qq % CPR_A;
           const int rot = ((kr & 7) + (((kr >> 5) & 1) << 3)) % CPR_A;
@@ -456,7 +529,8 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   const int nk = (K + kBK - 1) / kBK;
   const int r16 = lane & 15, g = lane >> 4;
   auto frag_a = [&](const uint8_t* As, int i) -> v8i {
-    return KMA ? lds_frag_km<BM>(As, wm * WM + 16 * i, lane) : lds_frag(As, wm * WM + 16 * i + r16, g);
+    if constexpr (KMA && EB == 2) return lds_frag_km16<BM>(As, wm * WM + 16 * i, lane);
+    else return KMA ? lds_frag_km<BM>(As, wm * WM + 16 * i, lane) : lds_frag(As, wm * WM + 16 * i + r16, g);
   };
   auto frag_b = [&](const uint8_t* Bs, int j) -> v8i {
     return KMB ? lds_frag_km<BN>(Bs, wn * WN + 16 * j, lane) : lds_frag(Bs, wn * WN + 16 * j + r16, g);
@@ -558,7 +632,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
       bfr[j] = KMB ? lds_frag_km<BN>(Bs, wn * WN + 16 * j, lane) : lds_frag(Bs, wn * WN + 16 * j + r16, g);
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      const v8i af = KMA ? lds_frag_km<BM>(As, wm * WM + 16 * i, lane) : lds_frag(As, wm * WM + 16 * i + r16, g);
+      const v8i af = frag_a(As, i);
 #pragma unroll
       for (int j = 0; j < TJ; ++j) acc[i][j] = mma<FA, FB, PREC>(bfr[j], af, acc[i][j]);
     }
@@ -574,7 +648,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   __syncthreads();
   }
 
-  if constexpr (P::kAct) {
+  if constexpr (P::kTail) {
+    P::template tail<BM, BN, WAVES_M, WAVES_N>(p, acc, pool, pool + Lds::kSmem, m0, n0, bz);
+    return;
+  } else if constexpr (P::kAct) {
     act_epilogue<BM, BN, WAVES_M, WAVES_N, DEEP, OUT>(p, acc, pool, m0, n0);
     return;
   } else {
@@ -780,7 +857,8 @@ template <int FA, int FB, int BM, int BN, int WAVES_M, int WAVES_N, int MIN_BLOC
 __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, MIN_BLOCKS) mm_fp8_dma(P p, int64_t tiles_m,
                                                                                  int64_t tiles_n, int group_m) {
   using Lds = TileLds<BM, BN, WAVES_M * WAVES_N, DEEP>;
-  __shared__ __align__(16) uint8_t pool[P::kAct ? Lds::kActBytes : Lds::kBytes];
+  __shared__ __align__(16) uint8_t pool[P::kTail ? Lds::kSmem + P::template extra_bytes<BM, BN>()
+                                                 : P::kAct ? Lds::kActBytes : Lds::kBytes];
   int64_t tm, tn, bz = 0, wg = blockIdx.x;
   if (gridDim.z > 1) batch_tile(wg, bz);
   tile_coords(wg, tiles_m, tiles_n, group_m, tm, tn);

@@ -468,6 +468,55 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * fp8_cross_entropy -- softmax cross entropy over a vocabulary, straight from the
+ * head's fp8 operands: the logits are never written.
+ *   l(i,j) = sa_i sb_j sum_k dec(A(i,k)) dec(B(j,k))      (bf16 MFMA on the codes' values,
+ *            which bf16 holds exactly, with fp32 sums)
+ *   lse_i  = log sum_j exp l(i,j)         loss_i = lse_i - l(i, t_i)
+ *   a, b       device E4M3 codes of the rows [M, K] and of the vocabulary's weights
+ *              [N, K]; K (a multiple of 16, at most 65536), lda, ldb multiples of 16,
+ *              16-byte aligned.
+ *   a_scale_inv, b_scale_inv, scale_rows   as fp8_mm_act.
+ *   targets    device int32 or int64 [M] (target_bits).  Negative: the row is ignored,
+ *              its loss is 0.  N or more: its loss is NaN.
+ *   loss, lse  device fp32 [M]; lse is the gradient's input.
+ *   mean_out   device fp32 [2] or NULL: the mean loss over the rows that are not
+ *              ignored, and 1 / their number (both 0 without any), summed in fp64 in a
+ *              fixed order.
+ *   workspace  device scratch of fp8_cross_entropy_workspace_bytes bytes, 16-byte
+ *              aligned, no initialisation; calls in flight on one workspace race.
+ * M is at most 2^20, M K below 2^30, N below 2^31.  M == 0 writes the mean alone.
+ * A logit that is infinite or NaN makes the row's loss NaN.
+ */
+FP8MI_API fp8mi_status fp8_cross_entropy(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M,
+                                         int64_t N, int64_t K, const float* a_scale_inv, const float* b_scale_inv,
+                                         int scale_rows, const void* targets, int target_bits, float* loss, float* lse,
+                                         float* mean_out, void* workspace, size_t workspace_bytes, void* stream);
+FP8MI_API size_t fp8_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * fp8_cross_entropy_grad -- gradient of sum_i dloss_i loss_i with respect to the
+ * head's operands, the logits computed once more:
+ *   G(i,j) = dloss_i (exp(l(i,j) - lse_i) - [j = t_i])    rounded to bf16; 0 for an
+ *            ignored row, NaN for one whose target is N or more
+ *   da = sb G dec(B)        db = sa G^T dec(A)            fp32 sums, one bf16 rounding
+ * Arguments as fp8_cross_entropy, with one scale per operand (the two factors leave the
+ * sums), and
+ *   lse        device fp32 [M]: the forward call's.
+ *   dloss      device fp32 [M] (dloss_rows 1), or one word for all rows (0).
+ *   da, db     device bf16 [M, K] (ld_da >= K) and [N, K] (ld_db >= K), either NULL when
+ *              it is not wanted.
+ *   workspace  fp8_cross_entropy_grad_workspace_bytes bytes.
+ * M == 0 writes zeros to db.
+ */
+FP8MI_API fp8mi_status fp8_cross_entropy_grad(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M,
+                                              int64_t N, int64_t K, const float* a_scale_inv, const float* b_scale_inv,
+                                              const void* targets, int target_bits, const float* lse,
+                                              const float* dloss, int dloss_rows, void* da, int64_t ld_da, void* db,
+                                              int64_t ld_db, void* workspace, size_t workspace_bytes, void* stream);
+FP8MI_API size_t fp8_cross_entropy_grad_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
  * fp8_adamw_step -- one AdamW step over `count` tensors (the weights that the
  * gradients of fp8 layers arrive at), a launch for each 44 of them:
  *   g = c grad                     m = beta1 m + (1 - beta1) g
