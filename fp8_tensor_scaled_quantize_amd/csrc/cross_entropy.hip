@@ -18,17 +18,21 @@ namespace fp8mi {
 
 namespace {
 
-constexpr int64_t kPieceElements = (int64_t)64 << 20;  // of a piece's weights or of G: 128 MiB in bf16, half the last-level cache
+constexpr int64_t kPieceElements = (int64_t)128 << 20;  // of a piece's weights or of G: 256 MiB in bf16
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// Leading dimension of n bf16 values: rows whose distance is a multiple of 1 KiB
+// fall on few of the memory's channels, so such rows get 128 bytes more
+// (4096 x 1536 x 16384, G B with rows 32 KiB apart: MEASURE).
+int64_t padded(int64_t n) { return n % 512 == 0 ? n + 64 : n; }
+
 // Columns of a piece, a multiple of 256: so many that neither the piece's weights
-// nor (with rows) its G are above kPieceElements.
+// nor (with rows) its G are above kPieceElements, in pieces of about one size.
 int64_t piece_columns(int64_t N, int64_t K, int64_t rows) {
   const int64_t most = kPieceElements / (K > rows ? K : rows);
   const int64_t p = most < 256 ? 256 : (most > (1 << 20) ? 1 << 20 : most / 256 * 256);
-  const int64_t all = up(N, 256);
-  return p < all ? p : all;
+  return up((N + (N + p - 1) / p - 1) / ((N + p - 1) / p), 256);
 }
 
 struct Carve {
@@ -40,22 +44,39 @@ struct Carve {
   }
 };
 
+// Up to 64 rows the logits come from xent_rows, 16 or 32 columns to a workgroup.
+bool few_rows(int64_t M) { return M <= 64; }
+int64_t rows_tile(int64_t N) { return N >= 8192 ? 32 : 16; }
+
+// Rows of a workgroup of the join: 16 fill the lines that it reads, fewer while there
+// are few.
+int join_rows(int64_t M) { return M >= 128 ? 16 : (M >= 16 ? 4 : 1); }
+
 struct ForwardPlan {
-  int64_t cols, tile, parts, logit, a16, b16, bytes;
+  int64_t cols, ld, tile, ticket, slots, parts, logit, a16, b16, bytes;
+  bool rows;
   ForwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
-    cols = piece_columns(N, K, 0);
-    tile = xent_lse_tile(M, N);
-    parts = c.take((N + tile - 1) / tile * M * 8);
+    rows = few_rows(M);
+    cols = rows ? N : piece_columns(N, K, 0);
+    ld = padded(K);
+    tile = rows ? rows_tile(N) : xent_lse_tile(M, N);
+    ticket = c.take(4);
+    slots = c.take((M + join_rows(M) - 1) / join_rows(M) * 16);
+    parts = c.take((N + cols - 1) / cols * ((cols + tile - 1) / tile) * M * 8);
     logit = c.take(M * 4);
-    a16 = c.take(M * K * 2);
-    b16 = c.take(cols * K * 2);
+    if (rows) {
+      bytes = c.at;
+      return;
+    }
+    a16 = c.take(M * ld * 2);
+    b16 = c.take(cols * ld * 2);
     bytes = c.at;
   }
 };
 
 struct BackwardPlan {
-  int64_t cols, splits, ld_t, a16, at16, b16, bt16, g, sums, bytes;
+  int64_t cols, splits, ld, ld_t, ld_g, a16, at16, b16, bt16, g, sums, bytes;
   BackwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
     cols = piece_columns(N, K, M);
@@ -64,24 +85,27 @@ struct BackwardPlan {
     splits = 256 / tiles;
     if (splits > cols / 512) splits = cols / 512;
     if (splits < 1) splits = 1;
-    ld_t = up(M, 8);
-    a16 = c.take(M * K * 2);
+    ld = padded(K);
+    ld_t = padded(up(M, 8));
+    ld_g = padded(cols);
+    a16 = c.take(M * ld * 2);
     at16 = c.take(K * ld_t * 2);
-    b16 = c.take(cols * K * 2);
-    bt16 = c.take(K * cols * 2);
-    g = c.take(M * cols * 2);
+    b16 = c.take(cols * ld * 2);
+    bt16 = c.take(K * ld_g * 2);
+    g = c.take(M * ld_g * 2);
     sums = c.take(splits * M * K * 4);
     bytes = c.at;
   }
 };
 
-// Codes [R, C] as bf16 [R, C] (or null) and transposed, [C, ld_t] (or null) with
+// Codes [R, C] as bf16 [R, ld_out] (or null) and transposed, [C, ld_t] (or null) with
 // zeros up to a multiple of 8 rows.  A workgroup takes 64 x 64.  C % 16 == 0.
 __global__ void __launch_bounds__(256) widen_codes(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out,
-                                                   uint16_t* out_t, int64_t ld_t) {
+                                                   int64_t ld_out, uint16_t* out_t, int64_t ld_t, uint32_t* ticket) {
   __shared__ uint32_t tile[64][33];  // two columns per word
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   const int tid = threadIdx.x, r = tid >> 2, c = 16 * (tid & 3);
+  if (ticket && tid + blockIdx.x + blockIdx.y == 0) *ticket = 0u;  // for the join two launches on
   const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
   u32x4 v = {0u, 0u, 0u, 0u};
   const bool in = r0 + r < R && c0 + c < C;
@@ -93,7 +117,7 @@ __global__ void __launch_bounds__(256) widen_codes(const uint8_t* x, int64_t ld,
     w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[e], 1.0f, true));
   }
   if (out && in) {
-    u32x4* q = reinterpret_cast<u32x4*>(out + (r0 + r) * C + c0 + c);
+    u32x4* q = reinterpret_cast<u32x4*>(out + (r0 + r) * ld_out + c0 + c);
     q[0] = u32x4{w[0], w[1], w[2], w[3]};
     q[1] = u32x4{w[4], w[5], w[6], w[7]};
   }
@@ -119,30 +143,179 @@ __global__ void __launch_bounds__(256) widen_codes(const uint8_t* x, int64_t ld,
   }
 }
 
-hipError_t launch_widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, uint16_t* out_t, int64_t ld_t,
-                        hipStream_t st) {
+hipError_t launch_widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, int64_t ld_out,
+                        uint16_t* out_t, int64_t ld_t, uint32_t* ticket, hipStream_t st) {
   hipLaunchKernelGGL(widen_codes, dim3((unsigned)((C + 63) / 64), (unsigned)((R + 63) / 64)), dim3(256), 0, st, x, ld, R, C,
-                     out, out_t, ld_t);
+                     out, ld_out, out_t, ld_t, ticket);
   return hipGetLastError();
 }
 
+// Few rows (scoring while serving): bound by reading the weights once.  A workgroup
+// takes 16 TJ columns of the vocabulary and all rows (16 TI), its four waves every
+// fourth K step of 128; the codes come straight from global memory into
+// registers, U steps in flight per wave, and become bf16 there (v_cvt_scalef32, 16
+// cycles for two values and a wave, is what a wider workgroup saves on the rows').
+// Lane group g takes k = 16 g .. + 15 and 64 + 16 g .. + 15 of a step, A and B
+// alike, so that a load instruction reads 64 contiguous bytes of a row.  The
+// waves' sums meet in LDS, and wave i finishes strip i.  (1 x 32768 x 1536, widened
+// and in 128 x 128 tiles: 60 us; this: MEASURE.)
+template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentArgs p, uint32_t* ticket) {
+  constexpr int NW = 4, U = TI == 4 ? 2 : 3;
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  __shared__ float4 part[NW][TI][TJ][64];
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid + blockIdx.x == 0) *ticket = 0u;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * TJ);
+  // raw buffers: rows past an edge and chunks past K read as zero
+  const int ext_a = (int)p.a_extent_from(0);
+  const int64_t b_rows = p.N - n0 < 16 * TJ ? p.N - n0 : 16 * TJ;
+  const int ext_b = (int)((b_rows - 1) * p.ldb + p.K);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a), 0, ext_a, 0x00020000);
+  const auto rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.b + n0 * p.ldb), 0, ext_b, 0x00020000);
+  const int K = (int)p.K, steps = (K + kBK - 1) / kBK;
+  uint32_t oa[TI], ob[TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+    oa[i] = 16 * i + r16 < p.M ? (uint32_t)(16 * i + r16) * (uint32_t)p.lda + 16 * g : (uint32_t)ext_a;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+    ob[j] = 16 * j + r16 < b_rows ? (uint32_t)(16 * j + r16) * (uint32_t)p.ldb + 16 * g : (uint32_t)ext_b;
+  struct Codes {
+    u32x4 h[2];
+  };
+  auto fetch = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, int ext, int kt) {
+    const int k = kt * kBK + 16 * g;
+    Codes c;
+    c.h[0] = __builtin_amdgcn_raw_buffer_load_b128(rs, k < K && off < (uint32_t)ext ? off + kt * kBK : ext, 0, 0);
+    c.h[1] = __builtin_amdgcn_raw_buffer_load_b128(rs, k + 64 < K && off < (uint32_t)ext ? off + kt * kBK + 64 : ext, 0, 0);
+    return c;
+  };
+  auto widen = [](const Codes& c, v8bf (&f)[4]) {  // eight k each
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = c.h[q >> 1][2 * (q & 1) + e];
+        w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
+        w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true));
+      }
+      f[q] = __builtin_bit_cast(v8bf, u32x4{w[0], w[1], w[2], w[3]});
+    }
+  };
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  Codes ca[U][TI], cb[U][TJ];
+  auto load = [&](int kt) {  // a step past the end reads nothing (k >= K)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) cb[u][j] = fetch(rsb, ob[j], ext_b, kt + u * NW);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) ca[u][i] = fetch(rsa, oa[i], ext_a, kt + u * NW);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all in flight before anything waits
+  };
+  load(wid);
+  for (int kt = wid; kt < steps;) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v8bf fb[TJ][4];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) widen(cb[u][j], fb[j]);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        v8bf fa[4];
+        widen(ca[u][i], fa);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j][q], fa[q], acc[i][j], 0, 0, 0);
+      }
+    }
+    kt += U * NW;
+    if (kt < steps) load(kt);
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) part[wid][i][j][lane] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+  __syncthreads();
+  const int row = 16 * wid + r16;
+  if (wid >= TI || 16 * wid >= p.M) return;
+  const bool in = row < p.M;
+  const float s = logit_scale(p) * (p.a_rows && in ? p.a_scale_inv[row] : 1.0f);
+  const int64_t t = in ? load_target(p.targets, p.target_bits, row) : -1;
+  float x[TJ][4], m = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    float4 f = part[0][wid][j][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const float4 q = part[w][wid][j][lane];
+      f.x += q.x; f.y += q.y; f.z += q.z; f.w += q.w;
+    }
+    const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t col = n0 + 16 * j + 4 * g + e;
+      const bool has = col < p.N;
+      const float sb = p.b_scale_inv ? p.b_scale_inv[p.b_rows ? (has ? col : 0) : 0] : 1.0f;
+      x[j][e] = has ? v[e] * (s * sb) : -__builtin_inff();
+      if (has && in && col == t) p.target_logit[row] = x[j][e];
+      m = fmaxf(m, x[j][e]);
+    }
+  }
+  m = fmaxf(m, __shfl_xor(m, 16, 64));
+  m = fmaxf(m, __shfl_xor(m, 32, 64));
+  const float ref = m > -3.0e38f ? m : 0.0f;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(x[j][e] - ref);
+  sum += __shfl_xor(sum, 16, 64);
+  sum += __shfl_xor(sum, 32, 64);
+  if (g == 0 && in) p.parts[(int64_t)blockIdx.x * p.M + row] = make_float2(m, sum);
+}
+
 // Joins the statistics of `tiles` column tiles: a workgroup takes RB rows, its
-// threads 256 / RB segments of the tiles.
+// threads 256 / RB segments of the tiles.  The last workgroup to end adds up the
+// mean over the counted rows (and 1 / their number; zeros without any), in fp64 in
+// a fixed order: workgroups leave their sums in `slots` ([2 * workgroups], 64 bits)
+// by returning device-scope atomics and wait for them before they take a ticket
+// (0 before the launch), as the ring's fold does.  (Plain stores behind a
+// device-scope fence, whose L2 write-back every workgroup pays for: 29 us instead
+// of MEASURE at 4096 rows.)
+__device__ __forceinline__ uint64_t swap64(uint64_t* p, uint64_t v) {
+  return __hip_atomic_exchange(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 template <int RB>
 __global__ void __launch_bounds__(256) xent_join(const float2* parts, int64_t tiles, int64_t M, const float* logit,
-                                                 const void* targets, int bits, int64_t vocab, float* loss, float* lse) {
+                                                 const void* targets, int bits, int64_t vocab, float* loss, float* lse,
+                                                 float* mean, uint32_t* ticket, uint64_t* slots) {
   constexpr int SEG = 256 / RB;
   __shared__ float2 red[SEG][RB + 1];
   const int r = threadIdx.x % RB, seg = threadIdx.x / RB;
   const int64_t row = (int64_t)blockIdx.x * RB + r;
   float m = -__builtin_inff(), s = 0.0f;
+  int64_t t = -1;
+  float own = 0.0f;
   if (row < M) {
+    if (seg == 0) {
+      t = load_target(targets, bits, row);
+      if (t >= 0 && t < vocab) own = logit[row];
+    }
     constexpr int U = 8;
-    for (int64_t t = seg; t < tiles; t += U * SEG) {
+    for (int64_t k = seg; k < tiles; k += U * SEG) {
       float2 q[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        q[u] = t + u * SEG < tiles ? parts[(t + u * SEG) * M + row] : make_float2(-__builtin_inff(), 0.0f);
+        q[u] = k + u * SEG < tiles ? parts[(k + u * SEG) * M + row] : make_float2(-__builtin_inff(), 0.0f);
       float top = m;
 #pragma unroll
       for (int u = 0; u < U; ++u) top = fmaxf(top, q[u].x);
@@ -155,46 +328,71 @@ __global__ void __launch_bounds__(256) xent_join(const float2* parts, int64_t ti
   }
   red[seg][r] = make_float2(m, s);
   __syncthreads();
-  if (seg != 0 || row >= M) return;
-  for (int k = 0; k < SEG; ++k) m = fmaxf(m, red[k][r].x);
-  const float ref = m > -3.0e38f ? m : 0.0f;
-  s = 0.0f;
-  for (int k = 0; k < SEG; ++k) s += red[k][r].y * __builtin_amdgcn_exp2f(red[k][r].x - ref);
-  const float l2 = ref + log2f(s);
-  const int64_t t = load_target(targets, bits, row);
-  lse[row] = l2 * kLn2;
-  loss[row] = t < 0 ? 0.0f : (t < vocab ? (l2 - logit[row]) * kLn2 : __builtin_nanf(""));
-}
-
-// The mean over the counted rows and 1 / their number (zeros without any), in fp64
-// in a fixed order.
-__global__ void __launch_bounds__(1024) xent_mean(const float* loss, const void* targets, int bits, int64_t M, float* out) {
-  __shared__ double sums[16];
-  __shared__ int64_t counts[16];
-  double s = 0.0;
-  int64_t n = 0;
-  for (int64_t i = threadIdx.x; i < M; i += 1024) {
-    s += (double)loss[i];  // 0 where the row is ignored
-    n += load_target(targets, bits, i) >= 0;
+  // halves of the segments join the others, in a fixed order
+#pragma unroll
+  for (int half = SEG / 2; half > 0; half >>= 1) {
+    if (seg < half) {
+      const float2 a = red[seg][r], b = red[seg + half][r];
+      const float top = fmaxf(a.x, b.x), ref = top > -3.0e38f ? top : 0.0f;
+      red[seg][r] = make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - ref) + b.y * __builtin_amdgcn_exp2f(b.x - ref));
+    }
+    __syncthreads();
+  }
+  float l = 0.0f;
+  if (seg == 0 && row < M) {
+    const float2 all = red[0][r];
+    const float l2 = (all.x > -3.0e38f ? all.x : 0.0f) + log2f(all.y);
+    l = t < 0 ? 0.0f : (t < vocab ? (l2 - own) * kLn2 : __builtin_nanf(""));
+    lse[row] = l2 * kLn2;
+    loss[row] = l;
+  }
+  if (!mean) return;
+  __shared__ uint32_t last;
+  // rows are in wave 0's first lanes (RB <= 64)
+  double total = (double)l;
+  uint64_t n = row < M && t >= 0 && seg == 0 ? 1u : 0u;
+#pragma unroll
+  for (int off = RB / 2; off > 0; off >>= 1) {
+    total += __shfl_xor(total, off, 64);
+    n += __shfl_xor(n, off, 64);
+  }
+  if (threadIdx.x == 0) {
+    const uint64_t o0 = swap64(slots + 2 * blockIdx.x, __builtin_bit_cast(uint64_t, total));
+    const uint64_t o1 = swap64(slots + 2 * blockIdx.x + 1, n);
+    asm volatile("" ::"v"(o0), "v"(o1) : "memory");
+    wait_vmem();
+    last = dev_add(ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  total = 0.0;
+  n = 0;
+  for (uint32_t i = threadIdx.x; i < gridDim.x; i += 256) {
+    total += __builtin_bit_cast(double, __hip_atomic_load(slots + 2 * i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    n += __hip_atomic_load(slots + 2 * i + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
-    s += __shfl_xor(s, off, 64);
+    total += __shfl_xor(total, off, 64);
     n += __shfl_xor(n, off, 64);
   }
+  __shared__ double sums[4];
+  __shared__ uint64_t counts[4];
   if ((threadIdx.x & 63) == 0) {
-    sums[threadIdx.x >> 6] = s;
+    sums[threadIdx.x >> 6] = total;
     counts[threadIdx.x >> 6] = n;
   }
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int k = 1; k < 16; ++k) {
-    s += sums[k];
+  for (int k = 1; k < 4; ++k) {
+    total += sums[k];
     n += counts[k];
   }
-  out[0] = n > 0 ? (float)(s / (double)n) : 0.0f;
-  out[1] = n > 0 ? (float)(1.0 / (double)n) : 0.0f;
+  mean[0] = n > 0 ? (float)(total / (double)n) : 0.0f;
+  mean[1] = n > 0 ? (float)(1.0 / (double)n) : 0.0f;
 }
+
+__global__ void zero_mean(float* mean) { mean[threadIdx.x] = 0.0f; }
 
 // dA = bf16(sb * the splits' sums), in their order.  K % 16 == 0.
 __global__ void __launch_bounds__(256) xent_finish_da(const float* sums, int64_t splits, int64_t M, int64_t K,
@@ -219,10 +417,12 @@ __global__ void __launch_bounds__(256) zero_rows(uint16_t* p, int64_t rows, int6
     if (e != hipSuccess) return e;       \
   } while (0)
 
-void fill_logits(XentArgs& p, const XentCall& c, const uint16_t* a16, const uint16_t* b16, int64_t v0, int64_t n) {
+void fill_logits(XentArgs& p, const XentCall& c, const uint16_t* a16, const uint16_t* b16, int64_t ld,
+                 int64_t v0, int64_t n) {
   p.a = reinterpret_cast<const uint8_t*>(a16);
   p.b = reinterpret_cast<const uint8_t*>(b16);
-  p.lda = p.ldb = p.K = p.k_total = 2 * c.K;
+  p.lda = p.ldb = 2 * ld;
+  p.K = p.k_total = 2 * c.K;
   p.M = c.M; p.N = n; p.batch = 1;
   p.a_scale_inv = c.a_scale_inv; p.b_scale_inv = c.b_scale_inv && c.b_rows ? c.b_scale_inv + v0 : c.b_scale_inv;
   p.a_rows = c.a_rows; p.b_rows = c.b_rows;
@@ -234,35 +434,57 @@ void fill_logits(XentArgs& p, const XentCall& c, const uint16_t* a16, const uint
 int64_t xent_workspace_bytes(int64_t M, int64_t N, int64_t K) { return ForwardPlan(M, N, K).bytes; }
 int64_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K) { return BackwardPlan(M, N, K).bytes; }
 
+template <int TJ> static hipError_t launch_rows(const XentArgs& p, uint32_t* ticket, hipStream_t st) {
+  const dim3 grid((unsigned)((p.N + 16 * TJ - 1) / (16 * TJ))), block(256);
+  if (p.M <= 16) hipLaunchKernelGGL((xent_rows<1, TJ>), grid, block, 0, st, p, ticket);
+  else if (p.M <= 32) hipLaunchKernelGGL((xent_rows<2, TJ>), grid, block, 0, st, p, ticket);
+  else hipLaunchKernelGGL((xent_rows<4, TJ>), grid, block, 0, st, p, ticket);
+  return hipGetLastError();
+}
+
 hipError_t launch_xent_forward(const XentCall& c, hipStream_t st) {
-  if (c.M > 0) {
-    const ForwardPlan plan(c.M, c.N, c.K);
+  if (c.M == 0) {
+    if (!c.mean) return hipSuccess;
+    hipLaunchKernelGGL(zero_mean, dim3(1), dim3(2), 0, st, c.mean);
+    return hipGetLastError();
+  }
+  const ForwardPlan plan(c.M, c.N, c.K);
+  uint32_t* const ticket = reinterpret_cast<uint32_t*>(c.ws + plan.ticket);
+  float2* const parts = reinterpret_cast<float2*>(c.ws + plan.parts);
+  float* const logit = reinterpret_cast<float*>(c.ws + plan.logit);
+  int64_t tiles = 0;
+  if (plan.rows) {
+    XentArgs p;
+    fill_logits(p, c, nullptr, nullptr, 0, 0, c.N);
+    p.a = c.a; p.b = c.b; p.lda = c.lda; p.ldb = c.ldb; p.K = c.K;
+    p.parts = parts;
+    p.target_logit = logit;
+    tiles = (c.N + plan.tile - 1) / plan.tile;
+    FP8MI_TRY(plan.tile == 32 ? launch_rows<2>(p, ticket, st) : launch_rows<1>(p, ticket, st));
+  } else {
     uint16_t* const a16 = reinterpret_cast<uint16_t*>(c.ws + plan.a16);
     uint16_t* const b16 = reinterpret_cast<uint16_t*>(c.ws + plan.b16);
-    float2* const parts = reinterpret_cast<float2*>(c.ws + plan.parts);
-    float* const logit = reinterpret_cast<float*>(c.ws + plan.logit);
-    FP8MI_TRY(launch_widen(c.a, c.lda, c.M, c.K, a16, nullptr, 0, st));
+    FP8MI_TRY(launch_widen(c.a, c.lda, c.M, c.K, a16, plan.ld, nullptr, 0, ticket, st));
     for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
       const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-      FP8MI_TRY(launch_widen(c.b + v0 * c.ldb, c.ldb, n, c.K, b16, nullptr, 0, st));
+      FP8MI_TRY(launch_widen(c.b + v0 * c.ldb, c.ldb, n, c.K, b16, plan.ld, nullptr, 0, nullptr, st));
       XentLseArgs p;
-      fill_logits(p, c, a16, b16, v0, n);
+      fill_logits(p, c, a16, b16, plan.ld, v0, n);
+      p.tile0 = tiles;
+      tiles += (n + plan.tile - 1) / plan.tile;
       p.parts = parts;
       p.target_logit = logit;
       FP8MI_TRY(launch_xent_lse(p, st));
     }
-    const int64_t tiles = (c.N + plan.tile - 1) / plan.tile;
-    const auto join = [&](auto kernel, int rb) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((c.M + rb - 1) / rb)), dim3(256), 0, st, parts, tiles, c.M, logit,
-                         c.targets, c.target_bits, c.N, c.loss, c.lse);
-      return hipGetLastError();
-    };
-    // rows share a workgroup while that leaves enough workgroups
-    FP8MI_TRY(c.M >= 4096 ? join(xent_join<16>, 16) : c.M >= 512 ? join(xent_join<4>, 4) : join(xent_join<1>, 1));
   }
-  if (!c.mean) return hipSuccess;
-  hipLaunchKernelGGL(xent_mean, dim3(1), dim3(1024), 0, st, c.loss, c.targets, c.target_bits, c.M, c.mean);
-  return hipGetLastError();
+  const int rb = join_rows(c.M);
+  const auto join = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((c.M + rb - 1) / rb)), dim3(256), 0, st, parts, tiles, c.M, logit,
+                       c.targets, c.target_bits, c.N, c.loss, c.lse, c.mean, ticket,
+                       reinterpret_cast<uint64_t*>(c.ws + plan.slots));
+    return hipGetLastError();
+  };
+  return rb == 16 ? join(xent_join<16>) : rb == 4 ? join(xent_join<4>) : join(xent_join<1>);
 }
 
 hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
@@ -274,7 +496,8 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const BackwardPlan plan(c.M, c.N, c.K);
   const auto at = [&](int64_t off) { return reinterpret_cast<uint16_t*>(c.ws + off); };
   float* const sums = reinterpret_cast<float*>(c.ws + plan.sums);
-  FP8MI_TRY(launch_widen(c.a, c.lda, c.M, c.K, at(plan.a16), c.db ? at(plan.at16) : nullptr, plan.ld_t, st));
+  FP8MI_TRY(launch_widen(c.a, c.lda, c.M, c.K, at(plan.a16), plan.ld, c.db ? at(plan.at16) : nullptr, plan.ld_t,
+                         nullptr, st));
   // bytes of G's rows per K split, from the first piece (no later one is wider):
   // whole 128-byte steps, so that every split starts on a chunk
   const int64_t first_cols = up(c.N < plan.cols ? c.N : plan.cols, 8);
@@ -282,18 +505,19 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const int64_t splits = (2 * first_cols + k_split - 1) / k_split;
   for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
     const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-    FP8MI_TRY(launch_widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), c.da ? at(plan.bt16) : nullptr, plan.cols, st));
+    FP8MI_TRY(launch_widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld, c.da ? at(plan.bt16) : nullptr,
+                           plan.ld_g, nullptr, st));
     XentGradArgs g;
-    fill_logits(g, c, at(plan.a16), at(plan.b16), v0, n);
+    fill_logits(g, c, at(plan.a16), at(plan.b16), plan.ld, v0, n);
     g.lse = c.lse;
     g.dloss = c.dloss; g.dloss_rows = c.dloss_rows;
-    g.d = at(plan.g); g.ld_d = plan.cols;
+    g.d = at(plan.g); g.ld_d = plan.ld_g;
     FP8MI_TRY(launch_xent_grad(g, st));
     if (c.da) {
       AddArgs p;
       p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
       p.b = reinterpret_cast<const uint8_t*>(at(plan.bt16));
-      p.lda = p.ldb = 2 * plan.cols;
+      p.lda = p.ldb = 2 * plan.ld_g;
       p.M = c.M; p.N = c.K;
       p.k_total = 2 * up(n, 8);
       p.K = k_split;
@@ -307,9 +531,9 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
       Mm16KmArgs p;
       p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
       p.b = reinterpret_cast<const uint8_t*>(at(plan.at16));
-      p.lda = 2 * plan.cols; p.ldb = 2 * plan.ld_t;
+      p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld_t;
       p.M = n; p.N = c.K; p.batch = 1;
-      p.K = p.k_total = 2 * plan.ld_t;
+      p.K = p.k_total = 2 * up(c.M, 8);
       p.k_major_rows = c.M;
       p.a_scale_inv = c.a_scale_inv;
       p.c = c.db + v0 * c.ld_db; p.ldc = c.ld_db; p.stride_c = 0;

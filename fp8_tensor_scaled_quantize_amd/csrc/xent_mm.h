@@ -45,6 +45,7 @@ struct XentArgs : Mm16Args {
   const void* targets = nullptr;
   int target_bits = 64;
   int64_t v0 = 0, vocab = 0;
+  int64_t tile0 = 0;                // tiles of columns in the pieces before
   // statistics
   float2* parts = nullptr;          // [tiles of columns][M]: (largest, sum of exponentials), in powers of two
   float* target_logit = nullptr;    // [M], in powers of two
@@ -165,7 +166,7 @@ struct XentLseArgs : XentArgs {
       const float ref = m > -3.0e38f ? m : 0.0f;
 #pragma unroll
       for (int k = 0; k < PAIRS; ++k) sum += q[k].y * __builtin_amdgcn_exp2f(q[k].x - ref);
-      p.parts[((p.v0 + n0) / BN) * p.M + m0 + tid] = make_float2(m, sum);
+      p.parts[(p.tile0 + n0 / BN) * p.M + m0 + tid] = make_float2(m, sum);
     }
   }
 };
@@ -262,7 +263,8 @@ template <int BM, int BN, int WM_, int WN_, int MINB, int LAY, int DEEP, class P
 static hipError_t launch_mm16_tile(const P& p0, hipStream_t st) {
   const int64_t tiles_m = (p0.M + BM - 1) / BM, tiles_n = (p0.N + BN - 1) / BN;
   P p = p0;
-  p.early_loads = tiles_m * tiles_n * p0.batch > (int64_t)device_cu_count();
+  // several rounds of tiles, or long sums (a K split of G B is 128 steps and more: 237 -> 214 us)
+  p.early_loads = tiles_m * tiles_n * p0.batch > (int64_t)device_cu_count() || p0.K >= 64 * kBK;
   hipLaunchKernelGGL((mm_fp8_dma<kOpBF16, kOpBF16, BM, BN, WM_, WN_, MINB, -1, LAY, false, DEEP, P>),
                      dim3((unsigned)(tiles_m * tiles_n), 1, (unsigned)p0.batch), dim3(64 * WM_ * WN_), 0, st, p, tiles_m,
                      tiles_n, 4);
