@@ -645,9 +645,9 @@ fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t c
 static fp8mi_status check_xent_size(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 1 || K < 1)
     return fail(FP8MI_ERR_SHAPE, "M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
-  if (K % 16 || K > 65536 || M > (1 << 20) || M > (INT64_C(1) << 30) / K - 1 || N > INT64_C(0x7FFFFFFF))
-    return fail(FP8MI_ERR_UNSUPPORTED, "M=%lld N=%lld K=%lld: K is a multiple of 16 up to 65536, M at most 2^20, M K below "
-                "2^30, N below 2^31", (long long)M, (long long)N, (long long)K);
+  if (K % 16 || K > 65536 || M > (1 << 20) || M >= (INT64_C(1) << 30) / (K + 64) || N > INT64_C(0x7FFFFFFF))
+    return fail(FP8MI_ERR_UNSUPPORTED, "M=%lld N=%lld K=%lld: K is a multiple of 16 up to 65536, M at most 2^20, M (K + 64) "
+                "below 2^30, N below 2^31", (long long)M, (long long)N, (long long)K);
   return FP8MI_OK;
 }
 

@@ -76,7 +76,7 @@ struct ForwardPlan {
 };
 
 struct BackwardPlan {
-  int64_t cols, splits, ld, ld_t, ld_g, a16, at16, b16, bt16, g, sums, bytes;
+  int64_t cols, splits, ld, ld_g, a16, b16, g, sums, bytes;
   BackwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
     cols = piece_columns(N, K, M);
@@ -86,67 +86,61 @@ struct BackwardPlan {
     if (splits > cols / 512) splits = cols / 512;
     if (splits < 1) splits = 1;
     ld = padded(K);
-    ld_t = padded(up(M, 8));
     ld_g = padded(cols);
     a16 = c.take(M * ld * 2);
-    at16 = c.take(K * ld_t * 2);
     b16 = c.take(cols * ld * 2);
-    bt16 = c.take(K * ld_g * 2);
     g = c.take(M * ld_g * 2);
     sums = c.take(splits * M * K * 4);
     bytes = c.at;
   }
 };
 
-// Codes [R, C] as bf16 [R, ld_out] (or null) and transposed, [C, ld_t] (or null) with
-// zeros up to a multiple of 8 rows.  A workgroup takes 64 x 64.  C % 16 == 0.
-__global__ void __launch_bounds__(256) widen_codes(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out,
-                                                   int64_t ld_out, uint16_t* out_t, int64_t ld_t, uint32_t* ticket) {
-  __shared__ uint32_t tile[64][33];  // two columns per word
+// Codes [R, C] of up to two matrices (A, and the first piece of B) as bf16, 32 codes
+// to a thread: C % 16 == 0, whole 16-byte chunks.  Bound by HBM: 3 bytes per code.
+struct Widen {
+  const uint8_t* x;
+  uint16_t* out;
+  int64_t ld, ld_out, chunks;  // chunks of 16 codes, in all
+  int32_t row_chunks;
+};
+__global__ void __launch_bounds__(256) widen_codes(Widen a, Widen b, uint32_t* ticket) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const int tid = threadIdx.x, r = tid >> 2, c = 16 * (tid & 3);
-  if (ticket && tid + blockIdx.x + blockIdx.y == 0) *ticket = 0u;  // for the join two launches on
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  const bool in = r0 + r < R && c0 + c < C;
-  if (in) v = *reinterpret_cast<const u32x4*>(x + (r0 + r) * ld + c0 + c);
-  uint32_t w[8];
+  if (ticket && threadIdx.x + blockIdx.x == 0) *ticket = 0u;  // for the join, launches on
+  const int64_t groups_a = (a.chunks + 511) / 512;
+  const bool first = (int64_t)blockIdx.x < groups_a;
+  const Widen m = first ? a : b;
+  const int64_t at = ((int64_t)blockIdx.x - (first ? 0 : groups_a)) * 512 + threadIdx.x;
+  u32x4 v[2];
+  int64_t out[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[e], 1.0f, false));
-    w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[e], 1.0f, true));
+  for (int u = 0; u < 2; ++u) {
+    const int64_t i = at + 256 * u;
+    const int64_t row = i < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)m.row_chunks) : i / m.row_chunks;
+    const int64_t c = (i - row * m.row_chunks) * 16;
+    out[u] = row * m.ld_out + c;
+    if (i < m.chunks) v[u] = *reinterpret_cast<const u32x4*>(m.x + row * m.ld + c);
   }
-  if (out && in) {
-    u32x4* q = reinterpret_cast<u32x4*>(out + (r0 + r) * ld_out + c0 + c);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (at + 256 * u >= m.chunks) return;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[u][e], 1.0f, false));
+      w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[u][e], 1.0f, true));
+    }
+    u32x4* q = reinterpret_cast<u32x4*>(m.out + out[u]);
     q[0] = u32x4{w[0], w[1], w[2], w[3]};
     q[1] = u32x4{w[4], w[5], w[6], w[7]};
   }
-  if (!out_t) return;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) tile[r][c / 2 + e] = w[e];
-  __syncthreads();
-  // thread: column tid / 4, rows 16 (tid % 4) .. + 15, in two groups of eight
-  const int col = tid >> 2, rr = 16 * (tid & 3);
-  if (c0 + col >= C) return;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t row = r0 + rr + 8 * h;
-    if (row >= R) break;
-    u32x4 o;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = tile[rr + 8 * h + 2 * e][col >> 1] >> (16 * (col & 1)) & 0xFFFFu;
-      const uint32_t hi = tile[rr + 8 * h + 2 * e + 1][col >> 1] >> (16 * (col & 1)) & 0xFFFFu;
-      o[e] = lo | (hi << 16);
-    }
-    *reinterpret_cast<u32x4*>(out_t + (c0 + col) * ld_t + row) = o;
-  }
 }
 
-hipError_t launch_widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, int64_t ld_out,
-                        uint16_t* out_t, int64_t ld_t, uint32_t* ticket, hipStream_t st) {
-  hipLaunchKernelGGL(widen_codes, dim3((unsigned)((C + 63) / 64), (unsigned)((R + 63) / 64)), dim3(256), 0, st, x, ld, R, C,
-                     out, ld_out, out_t, ld_t, ticket);
+Widen widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, int64_t ld_out) {
+  return {x, out, ld, ld_out, R * (C / 16), (int32_t)(C / 16)};
+}
+hipError_t launch_widen(const Widen& a, const Widen& b, uint32_t* ticket, hipStream_t st) {
+  const int64_t groups = (a.chunks + 511) / 512 + (b.chunks + 511) / 512;
+  hipLaunchKernelGGL(widen_codes, dim3((unsigned)groups), dim3(256), 0, st, a, b, ticket);
   return hipGetLastError();
 }
 
@@ -464,10 +458,10 @@ hipError_t launch_xent_forward(const XentCall& c, hipStream_t st) {
   } else {
     uint16_t* const a16 = reinterpret_cast<uint16_t*>(c.ws + plan.a16);
     uint16_t* const b16 = reinterpret_cast<uint16_t*>(c.ws + plan.b16);
-    FP8MI_TRY(launch_widen(c.a, c.lda, c.M, c.K, a16, plan.ld, nullptr, 0, ticket, st));
     for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
       const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-      FP8MI_TRY(launch_widen(c.b + v0 * c.ldb, c.ldb, n, c.K, b16, plan.ld, nullptr, 0, nullptr, st));
+      FP8MI_TRY(launch_widen(widen(c.a, c.lda, v0 == 0 ? c.M : 0, c.K, a16, plan.ld),
+                             widen(c.b + v0 * c.ldb, c.ldb, n, c.K, b16, plan.ld), v0 == 0 ? ticket : nullptr, st));
       XentLseArgs p;
       fill_logits(p, c, a16, b16, plan.ld, v0, n);
       p.tile0 = tiles;
@@ -496,8 +490,6 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const BackwardPlan plan(c.M, c.N, c.K);
   const auto at = [&](int64_t off) { return reinterpret_cast<uint16_t*>(c.ws + off); };
   float* const sums = reinterpret_cast<float*>(c.ws + plan.sums);
-  FP8MI_TRY(launch_widen(c.a, c.lda, c.M, c.K, at(plan.a16), plan.ld, c.db ? at(plan.at16) : nullptr, plan.ld_t,
-                         nullptr, st));
   // bytes of G's rows per K split, from the first piece (no later one is wider):
   // whole 128-byte steps, so that every split starts on a chunk
   const int64_t first_cols = up(c.N < plan.cols ? c.N : plan.cols, 8);
@@ -505,33 +497,35 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const int64_t splits = (2 * first_cols + k_split - 1) / k_split;
   for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
     const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-    FP8MI_TRY(launch_widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld, c.da ? at(plan.bt16) : nullptr,
-                           plan.ld_g, nullptr, st));
+    FP8MI_TRY(launch_widen(widen(c.a, c.lda, v0 == 0 ? c.M : 0, c.K, at(plan.a16), plan.ld),
+                           widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld), nullptr, st));
     XentGradArgs g;
     fill_logits(g, c, at(plan.a16), at(plan.b16), plan.ld, v0, n);
     g.lse = c.lse;
     g.dloss = c.dloss; g.dloss_rows = c.dloss_rows;
     g.d = at(plan.g); g.ld_d = plan.ld_g;
     FP8MI_TRY(launch_xent_grad(g, st));
-    if (c.da) {
+    if (c.da) {  // G by rows, the piece's weights K-major
       AddArgs p;
       p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
-      p.b = reinterpret_cast<const uint8_t*>(at(plan.bt16));
-      p.lda = p.ldb = 2 * plan.ld_g;
+      p.b = reinterpret_cast<const uint8_t*>(at(plan.b16));
+      p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld;
       p.M = c.M; p.N = c.K;
       p.k_total = 2 * up(n, 8);
+      p.k_major_rows = n;
       p.K = k_split;
       p.batch = (p.k_total + k_split - 1) / k_split;
-      p.stride_a = p.stride_b = p.K;
+      p.stride_a = k_split;
+      p.stride_b = k_split / 2 * p.ldb;
       p.sums = sums;
       p.first = v0 == 0;
       FP8MI_TRY(launch_mm16_add(p, st));
     }
-    if (c.db) {
-      Mm16KmArgs p;
+    if (c.db) {  // both K-major
+      Mm16Args p;
       p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
-      p.b = reinterpret_cast<const uint8_t*>(at(plan.at16));
-      p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld_t;
+      p.b = reinterpret_cast<const uint8_t*>(at(plan.a16));
+      p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld;
       p.M = n; p.N = c.K; p.batch = 1;
       p.K = p.k_total = 2 * up(c.M, 8);
       p.k_major_rows = c.M;

@@ -37,7 +37,7 @@ struct MmArgs {
   static constexpr bool kTail = false;  // no epilogue of its own (mm_fp8_kernel.h)
   struct Rows {};
   template <int BM, int BN> static constexpr int extra_bytes() { return 0; }
-  __host__ __device__ static int64_t k_rows(const MmArgs& p) { return p.K; }
+  __host__ __device__ static int64_t k_rows(const MmArgs& p, int64_t) { return p.K; }   // of one batch's K-major operands
   __host__ __device__ static int64_t k_bytes(const MmArgs& p, int64_t) { return p.K; }  // of one batch's sums
   const uint8_t* a = nullptr;
   const uint8_t* b = nullptr;

@@ -118,6 +118,9 @@ __device__ __forceinline__ float load_bias(const MmArgs& p, int64_t j, float bsc
 // (below) would spoil: the same tile in bytes, a step of 128 bytes being 64 k,
 // with leading dimensions, K and strides in bytes too.
 constexpr int kOpBF16 = 8;
+template <int W> struct Width {
+  static constexpr int value = W;
+};
 template <int F> constexpr int kOpBytes = F == kOpBF16 ? 2 : 1;
 
 // K-major tiles of 16-bit operands: 64 k-rows of 2 W bytes.  A fragment's 16
@@ -350,7 +353,6 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   constexpr bool KMA = (LAY & 1) != 0, KMB = (LAY & 2) != 0;
   constexpr int EB = kOpBytes<FA>;  // bytes per operand element
   static_assert(FA == FB || EB == kOpBytes<FB>, "operands of one width");
-  static_assert(EB == 1 || !KMB, "a 16-bit B is given by rows");
   constexpr int NWAVES = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   constexpr int TI = WM / 16, TJ = WN / 16;
@@ -380,10 +382,14 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / WAVES_N, wn = wid % WAVES_N;
-  const int ext_a = (int)(KMA ? p.a_extent_km(m0) : p.a_extent_from(m0));
-  const int ext_b = (int)(KMB ? p.b_extent_km(n0) : p.b_extent_from(n0));
+  int ext_a = (int)(KMA ? p.a_extent_km(m0) : p.a_extent_from(m0));
+  int ext_b = (int)(KMB ? p.b_extent_km(n0) : p.b_extent_from(n0));
+  if constexpr (EB == 2) {  // a K-major operand of 16 bits: whole rows of this batch's k
+    if constexpr (KMA) ext_a = (int)(P::k_rows(p, bz) * p.lda - 2 * m0);
+    if constexpr (KMB) ext_b = (int)(P::k_rows(p, bz) * p.ldb - 2 * n0);
+  }
   const v4i rsa = buffer_rsrc(p.a + bz * p.stride_a + (KMA ? EB * m0 : m0 * p.lda), ext_a);
-  const v4i rsb = buffer_rsrc(p.b + bz * p.stride_b + (KMB ? n0 : n0 * p.ldb), ext_b);
+  const v4i rsb = buffer_rsrc(p.b + bz * p.stride_b + (KMB ? EB * n0 : n0 * p.ldb), ext_b);
   // Lane l of a 1 KiB load fills LDS row r0 + l/8 (r0 a multiple of 8) at
   // chunk position l%8, so it fetches logical chunk (l%8) ^ swz(l/8).
   const int lr = lane >> 3, lc = (lane & 7) ^ swz(lr);
@@ -399,12 +405,13 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
 
   // 16-bit operands: lane l's chunk is half (q % 2) of the granule that
   // km16_granule places there.
-  auto km16_offset = [&](int qq, int k0) -> uint32_t {  // past k_rows: beyond the extent
-    constexpr int CPR = BM / 8, G = BM / 16;
+  const int k_rows = EB == 2 && (KMA || KMB) ? (int)P::k_rows(p, bz) : 0;
+  auto km16_offset = [&](auto w, int qq, int k0, uint32_t ld, int ext) -> uint32_t {  // past k_rows: beyond the extent
+    constexpr int CPR = decltype(w)::value / 8, G = decltype(w)::value / 16;
     const int kr = qq / CPR, pos = (qq % CPR) >> 1;
     const int rot = ((kr & 3) + (((kr >> 4) & 1) << 2)) % G;
     const uint32_t c = (uint32_t)((pos + G - rot) % G);
-    return k0 / 2 + kr >= P::k_rows(p) ? (uint32_t)ext_a : (uint32_t)kr * lda + 32 * c + 16 * (qq & 1);
+    return k0 / 2 + kr >= k_rows ? (uint32_t)ext : (uint32_t)kr * ld + 32 * c + 16 * (qq & 1);
   };
 
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
@@ -448,7 +455,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     for (int q = 0; q < (LA > LB ? LA : LB); ++q) {
       if (q < LA) {
         if constexpr (KMA && EB == 2) {
-          dma16(rsa, as + (wid * LA + q) * 1024, (int)km16_offset((wid * LA + q) * 64 + lane, k0),
+          dma16(rsa, as + (wid * LA + q) * 1024, (int)km16_offset(Width<BM>{}, (wid * LA + q) * 64 + lane, k0, lda, ext_a),
                 (int)((uint32_t)(k0 / 2) * lda));
         } else if constexpr (KMA) {
           const int qq = (wid * LA + q) * 64 + lane;
@@ -463,7 +470,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
         }
       }
       if (q < LB) {
-        if constexpr (KMB) {
+        if constexpr (KMB && EB == 2) {
+          dma16(rsb, bs + (wid * LB + q) * 1024, (int)km16_offset(Width<BN>{}, (wid * LB + q) * 64 + lane, k0, ldb, ext_b),
+                (int)((uint32_t)(k0 / 2) * ldb));
+        } else if constexpr (KMB) {
           const int qq = (wid * LB + q) * 64 + lane;
           const int kr = qq / CPR_B, pos = qq % CPR_B;
           const int rot = ((kr & 7) + (((kr >> 5) & 1) << 3)) % CPR_B;
@@ -490,7 +500,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     for (int q = c * LPW / NCH; q < (c + 1) * LPW / NCH; ++q) {
       if (q < LA) {
         if constexpr (KMA && EB == 2) {
-          dma16(rsa, as + (wid * LA + q) * 1024, (int)km16_offset((wid * LA + q) * 64 + lane, k0),
+          dma16(rsa, as + (wid * LA + q) * 1024, (int)km16_offset(Width<BM>{}, (wid * LA + q) * 64 + lane, k0, lda, ext_a),
                 (int)((uint32_t)(k0 / 2) * lda));
         } else if constexpr (KMA) {
           const int qq = (wid * LA + q) * 64 + lane;
@@ -505,7 +515,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
         }
       } else {
         const int qb = q - LA;
-        if constexpr (KMB) {
+        if constexpr (KMB && EB == 2) {
+          dma16(rsb, bs + (wid * LB + qb) * 1024, (int)km16_offset(Width<BN>{}, (wid * LB + qb) * 64 + lane, k0, ldb, ext_b),
+                (int)((uint32_t)(k0 / 2) * ldb));
+        } else if constexpr (KMB) {
           const int qq = (wid * LB + qb) * 64 + lane;
           const int kr = qq / CPR_B, pos = qq % CPR_B;
           const int rot = ((kr & 7) + (((kr >> 5) & 1) << 3)) % CPR_B;
@@ -533,7 +546,8 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     else return KMA ? lds_frag_km<BM>(As, wm * WM + 16 * i, lane) : lds_frag(As, wm * WM + 16 * i + r16, g);
   };
   auto frag_b = [&](const uint8_t* Bs, int j) -> v8i {
-    return KMB ? lds_frag_km<BN>(Bs, wn * WN + 16 * j, lane) : lds_frag(Bs, wn * WN + 16 * j + r16, g);
+    if constexpr (KMB && EB == 2) return lds_frag_km16<BN>(Bs, wn * WN + 16 * j, lane);
+    else return KMB ? lds_frag_km<BN>(Bs, wn * WN + 16 * j, lane) : lds_frag(Bs, wn * WN + 16 * j + r16, g);
   };
   if constexpr (STAGES == 2) {
     // Two stages, A fragments read two rows ahead.  Iteration kt enters with
@@ -629,7 +643,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     v8i bfr[TJ];
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
-      bfr[j] = KMB ? lds_frag_km<BN>(Bs, wn * WN + 16 * j, lane) : lds_frag(Bs, wn * WN + 16 * j + r16, g);
+      bfr[j] = frag_b(Bs, j);
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const v8i af = frag_a(As, i);

@@ -19,23 +19,19 @@ __device__ __forceinline__ int tile_target(int64_t t, int64_t v0, int64_t n) {
   return t < 0 ? kTargetIgnored : (t >= v0 && t < v0 + n ? (int)(t - v0) : kTargetElsewhere);
 }
 
-// bf16 operands by rows: leading dimensions, K and strides in bytes.  `k_split`:
-// batch z takes bytes z k_split .. of the rows, the last one fewer.
+// bf16 operands: leading dimensions, K and strides in bytes.  Batch z takes bytes
+// z K .. of a row-major operand's rows (the last batch fewer), and the rows z K / 2 ..
+// of a K-major one's k_major_rows.
 struct Mm16Args : MmArgs {
-  int64_t k_total = 0;
+  int64_t k_total = 0, k_major_rows = 0;
   __host__ __device__ static int64_t k_bytes(const Mm16Args& p, int64_t bz) {
     const int64_t left = p.k_total - bz * p.K;
     return left < p.K ? left : p.K;
   }
-};
-
-// A given K-major ([k_major_rows, lda / 2]); plain epilogue.
-struct Mm16KmArgs : Mm16Args {
-  int64_t k_major_rows = 0;
-  __host__ __device__ __forceinline__ int64_t a_extent_km(int64_t r) const {
-    return r < M && k_major_rows > 0 ? k_major_rows * lda - 2 * r : 0;
+  __host__ __device__ static int64_t k_rows(const Mm16Args& p, int64_t bz) {
+    const int64_t left = p.k_major_rows - bz * (p.K / 2);
+    return left < p.K / 2 ? left : p.K / 2;
   }
-  __host__ __device__ static int64_t k_rows(const Mm16KmArgs& p) { return p.k_major_rows; }
 };
 
 // What the logits' epilogues share: scales, targets, the piece's first column.
@@ -288,8 +284,8 @@ static inline int pick16(int64_t M, int64_t N, int64_t batch, bool narrow) {
 // one epilogue each
 hipError_t launch_xent_lse(const XentLseArgs& p, hipStream_t st);
 hipError_t launch_xent_grad(const XentGradArgs& p, hipStream_t st);
-hipError_t launch_mm16_add(const AddArgs& p, hipStream_t st);
-hipError_t launch_mm16_km(const Mm16KmArgs& p, hipStream_t st);
+hipError_t launch_mm16_add(const AddArgs& p, hipStream_t st);    // A by rows, B K-major
+hipError_t launch_mm16_km(const Mm16Args& p, hipStream_t st);    // both K-major, plain epilogue
 int64_t xent_lse_tile(int64_t M, int64_t N);  // columns that share a row's statistics
 
 }  // namespace fp8mi

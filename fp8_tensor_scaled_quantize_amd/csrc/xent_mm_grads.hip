@@ -11,7 +11,7 @@ template <int LAY, class P> static hipError_t launch_grads(const P& p, hipStream
     default: return launch_mm16_tile<64, 64, 1, 4, 2, LAY, 0>(p, st);
   }
 }
-hipError_t launch_mm16_add(const AddArgs& p, hipStream_t st) { return launch_grads<0>(p, st); }
-hipError_t launch_mm16_km(const Mm16KmArgs& p, hipStream_t st) { return launch_grads<1>(p, st); }
+hipError_t launch_mm16_add(const AddArgs& p, hipStream_t st) { return launch_grads<2>(p, st); }
+hipError_t launch_mm16_km(const Mm16Args& p, hipStream_t st) { return launch_grads<3>(p, st); }
 
 }  // namespace fp8mi

@@ -485,7 +485,7 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
  *              fixed order.
  *   workspace  device scratch of fp8_cross_entropy_workspace_bytes bytes, 16-byte
  *              aligned, no initialisation; calls in flight on one workspace race.
- * M is at most 2^20, M K below 2^30, N below 2^31.  M == 0 writes the mean alone.
+ * M is at most 2^20, M (K + 64) below 2^30, N below 2^31.  M == 0 writes the mean alone.
  * A logit that is infinite or NaN makes the row's loss NaN.
  */
 FP8MI_API fp8mi_status fp8_cross_entropy(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M,

@@ -1,0 +1,89 @@
+"""The cross entropy at sizes that reach its larger tiles, K splits, pieces and
+row counts, against a 64-bit computation on the GPU."""
+import pytest
+import torch
+
+import fp8_tensor_scaled_quantize_amd as fp8mi
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E4M3 = torch.float8_e4m3fn
+HALF, U32 = 2.0 ** -8, 2.0 ** -24
+
+
+def operands(M, N, K, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    out = []
+    for rows, sigma in ((M, 1.0), (N, 2.0 / K ** 0.5)):
+        v = torch.randn(rows, K, generator=g, device=DEV) * sigma
+        s = 448 / v.abs().amax()
+        out.append(((v * s).to(E4M3).view(torch.uint8), (1 / s).reshape(1)))
+    t = torch.randint(0, N, (M,), generator=g, device=DEV)
+    t[::5] = -100
+    return out[0][0], out[1][0], t, out[0][1], out[1][1], g
+
+
+def exact(a, b, t, sa, sb, d):
+    a, b = a.view(E4M3).double() * sa.double(), b.view(E4M3).double() * sb.double()
+    bt = b.t().contiguous()
+    lse, loss, da, db = [], [], [], torch.zeros_like(b)
+    for i in range(0, a.shape[0], 2048):
+        l = a[i:i + 2048] @ bt
+        p = torch.softmax(l, 1)
+        lse.append(torch.logsumexp(l, 1))
+        ti = t[i:i + 2048]
+        rows = torch.arange(l.shape[0], device=DEV)
+        loss.append(torch.where(ti >= 0, lse[-1] - l[rows, ti.clamp(min=0)], 0.0))
+        p[rows, ti.clamp(min=0)] -= 1
+        p *= torch.where(ti >= 0, d.double().expand(a.shape[0])[i:i + 2048], 0.0)[:, None]
+        da.append(p @ b)
+        db += p.t().contiguous() @ a[i:i + 2048]
+    return torch.cat(loss), torch.cat(lse), torch.cat(da), db
+
+
+# 64-wide, 128-wide, 256-wide tiles with and without edges, one and more pieces, K from a step to long
+SHAPES = [(2048, 20000, 512), (1111, 33001, 640), (4100, 9000, 1040), (600, 70001, 256), (96, 50001, 512), (64, 40000, 768),
+          (33, 8200, 2048), (17, 8191, 4096), (200, 3000, 4112), (300, 300, 8192), (5000, 700, 96), (129, 131072, 64),
+          (8000, 33000, 32)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_forms(M, N, K):
+    a, b, t, sa, sb, g = operands(M, N, K, seed=M + N)
+    d = torch.rand(M, generator=g, device=DEV) + 0.1
+    mean = torch.empty(2, device=DEV)
+    loss, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb, mean_out=mean)
+    wloss, wlse, wda, wdb = exact(a, b, t, sa, sb, d)
+    # a logit's terms add up to at most |a| |b| (Cauchy-Schwarz), its sums are off by K 2^-23 of that at most and in
+    # truth by the root of it: the bound below is the worst case
+    na = (a.view(E4M3).double() * sa.double()).norm(dim=1)
+    nb = (b.view(E4M3).double() * sb.double()).norm(dim=1).max()
+    el = na * nb * K * 2 * U32
+    assert ((lse - wlse).abs() <= el + 200 * U32 * (1 + wlse.abs())).all()
+    assert ((loss - wloss).abs() <= 2 * el + 200 * U32 * (1 + wlse.abs() + na * nb)).all()
+    # and as a whole: errors of single sums are independent, of the order of 2^-22 of a logit
+    assert (lse - wlse).norm() / wlse.norm() < 1e-6
+    n = int((t >= 0).sum())
+    assert abs(float(mean[0]) - float(wloss.sum()) / n) <= 1e-5 and abs(float(mean[1]) * n - 1) < 1e-6
+    da, db = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
+    # G and the outputs round to bf16 once each, independently
+    for got, want in ((da, wda), (db, wdb)):
+        assert (got - want).norm() / want.norm() <= 2 * HALF
+        big = want.abs().amax(1)
+        # no row is off as a whole
+        assert ((got - want).norm(dim=1) <= 4 * HALF * want.norm(dim=1) + 1e-6 * big.max()).all()
+    assert not da[::5].any()
+
+
+def test_the_same_whatever_the_workspace_holds():
+    a, b, t, sa, sb, g = operands(1500, 20011, 528, 3)
+    d = torch.ones(1, device=DEV)
+    size = fp8mi.fp8_cross_entropy_workspace_bytes(1500, 20011, 528), fp8mi.fp8_cross_entropy_grad_workspace_bytes(1500, 20011, 528)
+    out = []
+    for fill in (0, 0xFF, 0x7F):
+        ws = [torch.full((n + 16,), fill, dtype=torch.uint8, device=DEV)[16:] for n in size]
+        loss, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb, workspace=ws[0])
+        out.append((loss, lse, *fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb, workspace=ws[1])))
+    for o in out[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(o, out[0]))
