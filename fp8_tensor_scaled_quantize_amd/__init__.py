@@ -908,13 +908,14 @@ def fp8_cross_entropy_grad(a: torch.Tensor, b: torch.Tensor, targets: torch.Tens
 _ADAMW_TENSOR, _ADAMW_HYPER, _NORM_TENSOR = "7Pq3if", struct.Struct("@4dq3PI4x"), "Pqi4x"
 
 
+# (A step over small tensors is as long as these checks: they are written as
+# comprehensions, and look for the culprit only once one has failed.)
 def _flat(ts, name: str, sizes=None) -> None:
     """Contiguous tensors (elementwise operators read them as flat arrays), of
     the given element counts."""
-    for i, t in enumerate(ts):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-    if sizes is not None:
+    if False in [t.is_contiguous() for t in ts]:
+        raise ValueError(f"{name}[{[t.is_contiguous() for t in ts].index(False)}] must be contiguous")
+    if sizes is not None and [t.numel() for t in ts] != sizes:
         if len(ts) != len(sizes):
             raise ValueError(f"{len(ts)} {name} for {len(sizes)} params")
         for i, t in enumerate(ts):
@@ -927,6 +928,15 @@ def _dtypes(ts, name: str):
         return [_DT[t.dtype] for t in ts]
     except KeyError:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {[t.dtype for t in ts]}") from None
+
+
+def _all_on_device(*lists) -> None:
+    """_on_device for lists of tensors (no None among them)."""
+    here = {t.get_device() for ts in lists for t in ts}
+    if len(here) != 1 or here.pop() != _current_device():
+        for ts in lists:
+            _on_device(*ts)  # says which
+        _on_device(*[ts[0] for ts in lists if len(ts)])
 
 
 def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch.Tensor = 1e-3, betas=(0.9, 0.999),
@@ -948,28 +958,27 @@ def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch
     _flat(exp_avgs, "exp_avgs", sizes)
     _flat(exp_avg_sqs, "exp_avg_sqs", sizes)
     none = [None] * n
-    kept = [m for m in masters if m is not None] if masters is not None else []
     masters = none if masters is None else masters
     ms = none if exp_avg_scales is None else exp_avg_scales
     vs = none if exp_avg_sq_scales is None else exp_avg_sq_scales
     if len(masters) != n or len(ms) != n or len(vs) != n:
         raise ValueError("masters and scales: one entry per param (None where there is none)")
+    kept = [m for m in masters if m is not None]
     if kept:
         _flat(kept, "masters", [k for m, k in zip(masters, sizes) if m is not None])
-    scales = []
-    for i, (m, v, a, b, k) in enumerate(zip(exp_avgs, exp_avg_sqs, ms, vs, sizes)):
-        if a is None and b is None:
-            if m.dtype is not torch.float32 or v.dtype is not torch.float32:
-                raise ValueError(f"states of params[{i}] must be float32, or codes with their scales")
-            continue
-        if a is None or b is None or m.element_size() != 1 or v.element_size() != 1:
-            raise ValueError(f"8-bit states of params[{i}] need 1-byte codes and scales for both")
-        for t in (a, b):
-            _typed_vector(t, -(-k // ADAMW_BLOCK), "scales", _F32_ONLY)
-        scales += (a, b)
-    for m in kept:
-        if m.dtype is not torch.float32:
-            raise ValueError(f"masters must be float32, got {m.dtype}")
+        if [m for m in kept if m.dtype is not torch.float32]:
+            raise ValueError(f"masters must be float32, got {[m.dtype for m in kept]}")
+    scales = [a for a in (*ms, *vs) if a is not None]
+    if scales:
+        for i, (m, v, a, b, k) in enumerate(zip(exp_avgs, exp_avg_sqs, ms, vs, sizes)):
+            if a is None and b is None:
+                continue
+            if a is None or b is None or m.element_size() != 1 or v.element_size() != 1:
+                raise ValueError(f"8-bit states of params[{i}] need 1-byte codes and scales for both")
+            _typed_vector(a, -(-k // ADAMW_BLOCK), "scales", _F32_ONLY)
+            _typed_vector(b, -(-k // ADAMW_BLOCK), "scales", _F32_ONLY)
+    if [1 for m, a in zip((*exp_avgs, *exp_avg_sqs), (*ms, *vs)) if a is None and m.dtype is not torch.float32]:
+        raise ValueError("states must be float32, or codes with their scales")
     pdt, gdt = _dtypes(params, "params"), _dtypes(grads, "grads")
     decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
     if len(decay) != n:
@@ -985,21 +994,19 @@ def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch
     elif isinstance(lr, torch.Tensor):
         raise ValueError("lr on the device needs step on the device")
     _scalar(grad_scale, "grad_scale")
-    _on_device(*params, *grads, *exp_avgs, *exp_avg_sqs, *kept, *scales, grad_scale,
-               step if step_ptr else None, lr if lr_ptr else None)
-    at = [p.data_ptr() for p in params]
-    written = [a for a, k in zip(at, sizes) if k]
-    if len(set(written)) != len(written):
-        raise ValueError("the same param is there twice")
-    flat = []
-    for f in zip(at, grads, masters, exp_avgs, exp_avg_sqs, ms, vs, sizes, pdt, gdt, decay):
-        p, g, w, m, v, a, b, k, pd, gd, wd = f
-        flat += (p, g.data_ptr(), 0 if w is None else w.data_ptr(), m.data_ptr(), v.data_ptr(),
-                 0 if a is None else a.data_ptr(), 0 if b is None else b.data_ptr(), k, pd, gd, 32 if a is None else 8, wd)
-    hyper = _ADAMW_HYPER.pack(0.0 if lr_ptr else float(lr), betas[0], betas[1], eps, 0 if step_ptr else step, step_ptr or 0,
-                              lr_ptr or 0, 0 if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF)
     if n == 0 and step_ptr is None:
         return
+    words = [t for t in (grad_scale, step if step_ptr else None, lr if lr_ptr else None) if t is not None]
+    _all_on_device(params, grads, exp_avgs, exp_avg_sqs, kept, scales, words)
+    at = [p.data_ptr() for p in params]
+    if len(set(at)) != n and len({p for p, k in zip(at, sizes) if k}) != len([k for k in sizes if k]):
+        raise ValueError("the same param is there twice")
+    wptr, mptr, vptr = ([0 if t is None else t.data_ptr() for t in ts] for ts in (masters, ms, vs))
+    rows = zip(at, [g.data_ptr() for g in grads], wptr, [t.data_ptr() for t in exp_avgs],
+               [t.data_ptr() for t in exp_avg_sqs], mptr, vptr, sizes, pdt, gdt, [32 if a is None else 8 for a in ms], decay)
+    flat = [x for row in rows for x in row]
+    hyper = _ADAMW_HYPER.pack(0.0 if lr_ptr else float(lr), betas[0], betas[1], eps, 0 if step_ptr else step, step_ptr or 0,
+                              lr_ptr or 0, 0 if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF)
     status = lib().fp8_adamw_step(struct.pack("@" + _ADAMW_TENSOR * n, *flat), n, hyper,
                                   _stream(params[0] if n else step))
     if status:
@@ -1020,15 +1027,13 @@ def fp8_grad_norm(grads, max_norm: float | None = None, out: torch.Tensor | None
         out = torch.empty(1, dtype=torch.float32, device=grads[0].device)
     _scalar(out, "out")
     _scalar(clip_out, "clip_out")
-    dts = _dtypes(grads, "grads")
-    flat = []
-    for t, dt in zip(grads, dts):
-        flat += (t.data_ptr(), t.numel(), dt)
+    rows = zip([t.data_ptr() for t in grads], [t.numel() for t in grads], _dtypes(grads, "grads"))
+    flat = [x for row in rows for x in row]
     table = struct.pack("@" + _NORM_TENSOR * n, *flat)
     L = lib()
     if workspace is None:
         workspace = torch.empty(max(L.fp8_grad_norm_workspace_bytes(table, n), 8), dtype=torch.uint8, device=out.device)
-    _on_device(*grads, out, clip_out, workspace)
+    _all_on_device(grads, [t for t in (out, clip_out, workspace) if t is not None])
     status = L.fp8_grad_norm(table, n, None if max_norm is None else ctypes.byref(ctypes.c_float(max_norm)),
                              out.data_ptr(), None if clip_out is None else clip_out.data_ptr(), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _stream(out))

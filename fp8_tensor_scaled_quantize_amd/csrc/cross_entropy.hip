@@ -44,8 +44,12 @@ struct Carve {
   }
 };
 
-// Up to 64 rows the logits come from xent_rows, 16 or 32 columns to a workgroup.
-bool few_rows(int64_t M) { return M <= 64; }
+// Few rows, or few logits: xent_rows, 64 rows by 16 or 32 columns to a workgroup.
+// Graph replay, widened and in tiles -> xent_rows (us), 50001 x 1536: 16 rows 88 -> 37,
+// 64 rows 88 -> 54, 96 rows 88 -> 81, 128 rows 88 -> 91, 192 rows 88 -> 123; 32768 x 4096:
+// 128 rows 158 -> 106, 256 rows 186 -> 195; 8000 x 1024: 192 rows 32 -> 29, 384 rows
+// 40 -> 44; 1000 x 512: 512 rows 21 -> 18.
+bool few_rows(int64_t M, int64_t N) { return M <= 128 || M * N <= (1 << 20); }
 int64_t rows_tile(int64_t N) { return N >= 8192 ? 32 : 16; }
 
 // Rows of a workgroup of the join: 16 fill the lines that it reads, fewer while there
@@ -57,7 +61,7 @@ struct ForwardPlan {
   bool rows;
   ForwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
-    rows = few_rows(M);
+    rows = few_rows(M, N);
     cols = rows ? N : piece_columns(N, K, 0);
     ld = padded(K);
     tile = rows ? rows_tile(N) : xent_lse_tile(M, N);
@@ -154,24 +158,26 @@ hipError_t launch_widen(const Widen& a, const Widen& b, uint32_t* ticket, hipStr
 // waves' sums meet in LDS, and wave i finishes strip i.  (1 x 32768 x 1536, widened
 // and in 128 x 128 tiles: 60 us; this: MEASURE.)
 template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentArgs p, uint32_t* ticket) {
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * TI);
   constexpr int NW = 4, U = TI == 4 ? 2 : 3;
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   __shared__ float4 part[NW][TI][TJ][64];
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (tid + blockIdx.x == 0) *ticket = 0u;
+  if (tid + blockIdx.x + blockIdx.y == 0) *ticket = 0u;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * TJ);
   // raw buffers: rows past an edge and chunks past K read as zero
-  const int ext_a = (int)p.a_extent_from(0);
+  const int64_t a_rows = p.M - m0 < 16 * TI ? p.M - m0 : 16 * TI;
+  const int ext_a = (int)((a_rows - 1) * p.lda + p.K);
   const int64_t b_rows = p.N - n0 < 16 * TJ ? p.N - n0 : 16 * TJ;
   const int ext_b = (int)((b_rows - 1) * p.ldb + p.K);
-  const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a), 0, ext_a, 0x00020000);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a + m0 * p.lda), 0, ext_a, 0x00020000);
   const auto rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.b + n0 * p.ldb), 0, ext_b, 0x00020000);
   const int K = (int)p.K, steps = (K + kBK - 1) / kBK;
   uint32_t oa[TI], ob[TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
-    oa[i] = 16 * i + r16 < p.M ? (uint32_t)(16 * i + r16) * (uint32_t)p.lda + 16 * g : (uint32_t)ext_a;
+    oa[i] = m0 + 16 * i + r16 < p.M ? (uint32_t)(16 * i + r16) * (uint32_t)p.lda + 16 * g : (uint32_t)ext_a;
 #pragma unroll
   for (int j = 0; j < TJ; ++j)
     ob[j] = 16 * j + r16 < b_rows ? (uint32_t)(16 * j + r16) * (uint32_t)p.ldb + 16 * g : (uint32_t)ext_b;
@@ -240,8 +246,8 @@ template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentA
 #pragma unroll
     for (int j = 0; j < TJ; ++j) part[wid][i][j][lane] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
   __syncthreads();
-  const int row = 16 * wid + r16;
-  if (wid >= TI || 16 * wid >= p.M) return;
+  const int64_t row = m0 + 16 * wid + r16;
+  if (wid >= TI || m0 + 16 * wid >= p.M) return;
   const bool in = row < p.M;
   const float s = logit_scale(p) * (p.a_rows && in ? p.a_scale_inv[row] : 1.0f);
   const int64_t t = in ? load_target(p.targets, p.target_bits, row) : -1;
@@ -429,7 +435,7 @@ int64_t xent_workspace_bytes(int64_t M, int64_t N, int64_t K) { return ForwardPl
 int64_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K) { return BackwardPlan(M, N, K).bytes; }
 
 template <int TJ> static hipError_t launch_rows(const XentArgs& p, uint32_t* ticket, hipStream_t st) {
-  const dim3 grid((unsigned)((p.N + 16 * TJ - 1) / (16 * TJ))), block(256);
+  const dim3 grid((unsigned)((p.N + 16 * TJ - 1) / (16 * TJ)), (unsigned)((p.M + 63) / 64)), block(256);
   if (p.M <= 16) hipLaunchKernelGGL((xent_rows<1, TJ>), grid, block, 0, st, p, ticket);
   else if (p.M <= 32) hipLaunchKernelGGL((xent_rows<2, TJ>), grid, block, 0, st, p, ticket);
   else hipLaunchKernelGGL((xent_rows<4, TJ>), grid, block, 0, st, p, ticket);

@@ -177,6 +177,7 @@ struct XentGradArgs : XentArgs {
   __device__ static __forceinline__ void tail(const XentGradArgs& p, const v4f (&acc)[TI][TJ], uint8_t*,
                                               const uint8_t* extra, int64_t m0, int64_t n0, int64_t) {
     constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, C = pair_cols(TJ), NP = strip_pairs(TJ);
+    constexpr bool STREAM = BM * BN == 256 * 256;  // G is larger than the L2 there
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wid / WAVES_N, wn = wid % WAVES_N;
     const float* const rows = reinterpret_cast<const float*>(extra) + BN;
@@ -213,7 +214,7 @@ struct XentGradArgs : XentArgs {
         if (in && (at & ~7) < cols_in) {
           uint32_t w[C / 2];
           pack_bf16<C>(w, t);
-          store_words<C / 2, 2>(reinterpret_cast<uint8_t*>(out + at), w, C);
+          store_words<C / 2, 2, STREAM>(reinterpret_cast<uint8_t*>(out + at), w, C);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -268,7 +269,8 @@ static hipError_t launch_mm16_tile(const P& p0, hipStream_t st) {
 }
 
 // Tiles as pick_tile's: 256 x 256, or 256 x 192 where that needs less time, from
-// 60% of the CUs on, below that 128 x 128, then 64 x 64.
+// 60% of the CUs on, below that 128 x 128, then 64 x 64 (whose eight-stage form is no
+// faster here: 64 x 1000 x 512 logits 7.7 against 8.0 us, G B 6.8 against 6.3).
 static inline int pick16(int64_t M, int64_t N, int64_t batch, bool narrow) {
   // of an MI355X, not of the current device: the workspace's size goes by the tiles
   constexpr int64_t ncu = 256;
