@@ -5,12 +5,12 @@
 //   loss_i = lse_i - l_{i, t_i}
 //   G_ij = d_i (exp(l_ij - lse_i) - [j = t_i])   dA = sb G B   dB = sa G^T A
 //
-// The vocabulary is taken in pieces.  Forward: a piece's codes become bf16 (their
+// The vocabulary is taken in pieces.  Forward: a piece's codes become fp16 (their
 // exact values) in the workspace, and the product's epilogue (xent_mm.h) leaves
 // each row's largest logit and sum of exponentials per tile of columns; one more
-// kernel joins them.  Backward: the piece's logits once more, G in bf16, then
+// kernel joins them.  Backward: the piece's logits once more, G / d in fp16, then
 // G B into fp32 sums and G^T A straight to its rows of dB.  So 2 M N K flop forward
-// and 6 M N K backward, at bf16's rate; what is written besides is M times a
+// and 6 M N K backward, at 16 bits' rate; what is written besides is M times a
 // piece's columns.
 #include "xent_mm.h"
 
@@ -18,11 +18,11 @@ namespace fp8mi {
 
 namespace {
 
-constexpr int64_t kPieceElements = (int64_t)128 << 20;  // of a piece's weights or of G: 256 MiB in bf16
+constexpr int64_t kPieceElements = (int64_t)128 << 20;  // of a piece's weights or of G: 256 MiB in fp16
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Leading dimension of n bf16 values: rows whose distance is a multiple of 1 KiB
+// Leading dimension of n fp16 values: rows whose distance is a multiple of 1 KiB
 // fall on few of the memory's channels, so such rows get 128 bytes more
 // (4096 x 1536 x 16384, G B with rows 32 KiB apart: MEASURE).
 int64_t padded(int64_t n) { return n % 512 == 0 ? n + 64 : n; }
@@ -80,7 +80,7 @@ struct ForwardPlan {
 };
 
 struct BackwardPlan {
-  int64_t cols, splits, ld, ld_g, a16, b16, g, sums, bytes;
+  int64_t cols, splits, ld, ld_g, scale, a16, a16d, b16, g, sums, bytes;
   BackwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
     cols = piece_columns(N, K, M);
@@ -91,7 +91,9 @@ struct BackwardPlan {
     if (splits < 1) splits = 1;
     ld = padded(K);
     ld_g = padded(cols);
+    scale = c.take(4);
     a16 = c.take(M * ld * 2);
+    a16d = c.take(M * ld * 2);
     b16 = c.take(cols * ld * 2);
     g = c.take(M * ld_g * 2);
     sums = c.take(splits * M * K * 4);
@@ -99,48 +101,71 @@ struct BackwardPlan {
   }
 };
 
-// Codes [R, C] of up to two matrices (A, and the first piece of B) as bf16, 32 codes
+// Codes [R, C] of up to two matrices (A, and the first piece of B) as fp16, 32 codes
 // to a thread: C % 16 == 0, whole 16-byte chunks.  Bound by HBM: 3 bytes per code.
+// With targets, the rows of ignored ones are zeros (a NaN among their codes would
+// reach dB as 0 * NaN); with row factors, out_scaled receives each row times its own.
 struct Widen {
   const uint8_t* x;
   uint16_t* out;
   int64_t ld, ld_out, chunks;  // chunks of 16 codes, in all
   int32_t row_chunks;
+  int target_bits;
+  const void* targets;
+  const float* rows;           // [R], times 1 / *rows_by
+  const float* rows_by;
+  uint16_t* out_scaled;
 };
 __global__ void __launch_bounds__(256) widen_codes(Widen a, Widen b, uint32_t* ticket) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   if (ticket && threadIdx.x + blockIdx.x == 0) *ticket = 0u;  // for the join, launches on
   const int64_t groups_a = (a.chunks + 511) / 512;
   const bool first = (int64_t)blockIdx.x < groups_a;
-  const Widen m = first ? a : b;
+  const Widen& m = first ? a : b;
   const int64_t at = ((int64_t)blockIdx.x - (first ? 0 : groups_a)) * 512 + threadIdx.x;
   u32x4 v[2];
-  int64_t out[2];
+  int64_t out[2], row[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int64_t i = at + 256 * u;
-    const int64_t row = i < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)m.row_chunks) : i / m.row_chunks;
-    const int64_t c = (i - row * m.row_chunks) * 16;
-    out[u] = row * m.ld_out + c;
-    if (i < m.chunks) v[u] = *reinterpret_cast<const u32x4*>(m.x + row * m.ld + c);
+    row[u] = i < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)m.row_chunks) : i / m.row_chunks;
+    const int64_t c = (i - row[u] * m.row_chunks) * 16;
+    out[u] = row[u] * m.ld_out + c;
+    if (i < m.chunks) v[u] = *reinterpret_cast<const u32x4*>(m.x + row[u] * m.ld + c);
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     if (at + 256 * u >= m.chunks) return;
+    if (m.targets && load_target(m.targets, m.target_bits, row[u]) < 0) v[u] = u32x4{0u, 0u, 0u, 0u};
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[u][e], 1.0f, false));
-      w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[u][e], 1.0f, true));
+      w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[u][e], 1.0f, false));
+      w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[u][e], 1.0f, true));
     }
     u32x4* q = reinterpret_cast<u32x4*>(m.out + out[u]);
     q[0] = u32x4{w[0], w[1], w[2], w[3]};
     q[1] = u32x4{w[4], w[5], w[6], w[7]};
+    if (m.out_scaled) {
+      const bool counted = load_target(m.targets, m.target_bits, row[u]) >= 0;
+      const float f = counted ? m.rows[row[u]] / *m.rows_by : 0.0f;
+      float t[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        widen2<kF16>(w[e], t[2 * e], t[2 * e + 1]);
+        t[2 * e] *= f;
+        t[2 * e + 1] *= f;
+      }
+      pack_f16<16>(w, t);
+      q = reinterpret_cast<u32x4*>(m.out_scaled + out[u]);
+      q[0] = u32x4{w[0], w[1], w[2], w[3]};
+      q[1] = u32x4{w[4], w[5], w[6], w[7]};
+    }
   }
 }
 
 Widen widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, int64_t ld_out) {
-  return {x, out, ld, ld_out, R * (C / 16), (int32_t)(C / 16)};
+  return {x, out, ld, ld_out, R * (C / 16), (int32_t)(C / 16), 0, nullptr, nullptr, nullptr, nullptr};
 }
 hipError_t launch_widen(const Widen& a, const Widen& b, uint32_t* ticket, hipStream_t st) {
   const int64_t groups = (a.chunks + 511) / 512 + (b.chunks + 511) / 512;
@@ -148,10 +173,26 @@ hipError_t launch_widen(const Widen& a, const Widen& b, uint32_t* ticket, hipStr
   return hipGetLastError();
 }
 
+// The power of two at or above the largest |dloss| of the counted rows: dB's rows of
+// A carry dloss over it, which fp16 holds (1 where that is no normal number).
+__global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const void* targets, int bits, int64_t M, float* out) {
+  __shared__ float red[16];
+  float m = 0.0f;
+  for (int64_t i = threadIdx.x; i < M; i += 1024)
+    if (load_target(targets, bits, i) >= 0) m = __builtin_elementwise_maximum(m, fabsf(dloss[i]));  // a NaN kept
+  for (int off = 32; off > 0; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int k = 1; k < 16; ++k) m = __builtin_elementwise_maximum(m, red[k]);
+  const uint32_t exp = __float_as_uint(m) & 0x7F800000u;
+  *out = exp > 0u && exp < 0x7F000000u ? __uint_as_float(exp + 0x00800000u) : 1.0f;
+}
+
 // Few rows (scoring while serving): bound by reading the weights once.  A workgroup
 // takes 16 TJ columns of the vocabulary and all rows (16 TI), its four waves every
 // fourth K step of 128; the codes come straight from global memory into
-// registers, U steps in flight per wave, and become bf16 there (v_cvt_scalef32, 16
+// registers, U steps in flight per wave, and become fp16 there (v_cvt_scalef32, 16
 // cycles for two values and a wave, is what a wider workgroup saves on the rows').
 // Lane group g takes k = 16 g .. + 15 and 64 + 16 g .. + 15 of a step, A and B
 // alike, so that a load instruction reads 64 contiguous bytes of a row.  The
@@ -191,17 +232,17 @@ template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentA
     c.h[1] = __builtin_amdgcn_raw_buffer_load_b128(rs, k + 64 < K && off < (uint32_t)ext ? off + kt * kBK + 64 : ext, 0, 0);
     return c;
   };
-  auto widen = [](const Codes& c, v8bf (&f)[4]) {  // eight k each
+  auto widen = [](const Codes& c, v8h (&f)[4]) {  // eight k each
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t x = c.h[q >> 1][2 * (q & 1) + e];
-        w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
-        w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true));
+        w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, false));
+        w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, true));
       }
-      f[q] = __builtin_bit_cast(v8bf, u32x4{w[0], w[1], w[2], w[3]});
+      f[q] = __builtin_bit_cast(v8h, u32x4{w[0], w[1], w[2], w[3]});
     }
   };
   v4f acc[TI][TJ];
@@ -224,18 +265,18 @@ template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentA
   for (int kt = wid; kt < steps;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      v8bf fb[TJ][4];
+      v8h fb[TJ][4];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) widen(cb[u][j], fb[j]);
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
-        v8bf fa[4];
+        v8h fa[4];
         widen(ca[u][i], fa);
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j][q], fa[q], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j][q], fa[q], acc[i][j], 0, 0, 0);
       }
     }
     kt += U * NW;
@@ -394,16 +435,19 @@ __global__ void __launch_bounds__(256) xent_join(const float2* parts, int64_t ti
 
 __global__ void zero_mean(float* mean) { mean[threadIdx.x] = 0.0f; }
 
-// dA = bf16(sb * the splits' sums), in their order.  K % 16 == 0.
-__global__ void __launch_bounds__(256) xent_finish_da(const float* sums, int64_t splits, int64_t M, int64_t K,
-                                                      const float* sb, uint16_t* da, int64_t ld) {
+// dA's rows = bf16(sb dloss_i / kGScale * the splits' sums), in their order; zeros
+// where ignored.  K % 16 == 0.
+__global__ void __launch_bounds__(256) xent_finish_da(const float* sums, int64_t splits, XentCall c) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= M * K) return;
+  if (i >= c.M * c.K) return;
+  const int64_t row = i / c.K;
+  const bool counted = load_target(c.targets, c.target_bits, row) >= 0;
+  const float f = (c.b_scale_inv ? *c.b_scale_inv : 1.0f) * c.dloss[c.dloss_rows ? row : 0] * (1.0f / kGScale);
   v4f v = *reinterpret_cast<const v4f*>(sums + i);
-  for (int64_t z = 1; z < splits; ++z) v += *reinterpret_cast<const v4f*>(sums + z * M * K + i);
-  v *= sb ? *sb : 1.0f;
+  for (int64_t z = 1; z < splits; ++z) v += *reinterpret_cast<const v4f*>(sums + z * c.M * c.K + i);
+  v = counted ? v * f : v4f{0.0f, 0.0f, 0.0f, 0.0f};
   const uint2 w = bf16x4_rne(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<u32x2_any*>(da + i / K * ld + i % K) = u32x2_any{w.x, w.y};
+  *reinterpret_cast<u32x2_any*>(c.da + row * c.ld_da + i % c.K) = u32x2_any{w.x, w.y};
 }
 
 __global__ void __launch_bounds__(256) zero_rows(uint16_t* p, int64_t rows, int64_t cols, int64_t ld) {
@@ -496,6 +540,13 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const BackwardPlan plan(c.M, c.N, c.K);
   const auto at = [&](int64_t off) { return reinterpret_cast<uint16_t*>(c.ws + off); };
   float* const sums = reinterpret_cast<float*>(c.ws + plan.sums);
+  // with a loss gradient per row, dB takes A's rows times theirs
+  const bool scaled = c.db && c.dloss_rows;
+  float* const scale = reinterpret_cast<float*>(c.ws + plan.scale);
+  if (scaled) {
+    hipLaunchKernelGGL(dloss_scale, dim3(1), dim3(1024), 0, st, c.dloss, c.targets, c.target_bits, c.M, scale);
+    FP8MI_TRY(hipGetLastError());
+  }
   // bytes of G's rows per K split, from the first piece (no later one is wider):
   // whole 128-byte steps, so that every split starts on a chunk
   const int64_t first_cols = up(c.N < plan.cols ? c.N : plan.cols, 8);
@@ -503,12 +554,18 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const int64_t splits = (2 * first_cols + k_split - 1) / k_split;
   for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
     const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-    FP8MI_TRY(launch_widen(widen(c.a, c.lda, v0 == 0 ? c.M : 0, c.K, at(plan.a16), plan.ld),
-                           widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld), nullptr, st));
+    Widen rows = widen(c.a, c.lda, v0 == 0 ? c.M : 0, c.K, at(plan.a16), plan.ld);
+    rows.targets = c.targets;
+    rows.target_bits = c.target_bits;
+    if (scaled) {
+      rows.rows = c.dloss;
+      rows.rows_by = scale;
+      rows.out_scaled = at(plan.a16d);
+    }
+    FP8MI_TRY(launch_widen(rows, widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld), nullptr, st));
     XentGradArgs g;
     fill_logits(g, c, at(plan.a16), at(plan.b16), plan.ld, v0, n);
     g.lse = c.lse;
-    g.dloss = c.dloss; g.dloss_rows = c.dloss_rows;
     g.d = at(plan.g); g.ld_d = plan.ld_g;
     FP8MI_TRY(launch_xent_grad(g, st));
     if (c.da) {  // G by rows, the piece's weights K-major
@@ -530,19 +587,19 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
     if (c.db) {  // both K-major
       Mm16Args p;
       p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
-      p.b = reinterpret_cast<const uint8_t*>(at(plan.a16));
+      p.b = reinterpret_cast<const uint8_t*>(at(scaled ? plan.a16d : plan.a16));
       p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld;
       p.M = n; p.N = c.K; p.batch = 1;
       p.K = p.k_total = 2 * up(c.M, 8);
       p.k_major_rows = c.M;
       p.a_scale_inv = c.a_scale_inv;
+      p.b_scale_inv = scaled ? scale : c.dloss;
       p.c = c.db + v0 * c.ld_db; p.ldc = c.ld_db; p.stride_c = 0;
       FP8MI_TRY(launch_mm16_km(p, st));
     }
   }
   if (!c.da) return hipSuccess;
-  hipLaunchKernelGGL(xent_finish_da, dim3((unsigned)((c.M * c.K / 4 + 255) / 256)), dim3(256), 0, st, sums, splits, c.M,
-                     c.K, c.b_scale_inv, c.da, c.ld_da);
+  hipLaunchKernelGGL(xent_finish_da, dim3((unsigned)((c.M * c.K / 4 + 255) / 256)), dim3(256), 0, st, sums, splits, c);
   return hipGetLastError();
 }
 

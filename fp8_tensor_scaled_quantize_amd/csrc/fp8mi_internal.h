@@ -36,6 +36,7 @@ struct MmArgs {
   static constexpr bool kAct = false;   // the plain epilogue
   static constexpr bool kTail = false;  // no epilogue of its own (mm_fp8_kernel.h)
   struct Rows {};
+  __host__ __device__ static float out_scale(const MmArgs&, float sab) { return sab; }
   template <int BM, int BN> static constexpr int extra_bytes() { return 0; }
   __host__ __device__ static int64_t k_rows(const MmArgs& p, int64_t) { return p.K; }   // of one batch's K-major operands
   __host__ __device__ static int64_t k_bytes(const MmArgs& p, int64_t) { return p.K; }  // of one batch's sums
@@ -196,7 +197,7 @@ struct XentCall {
   float* lse = nullptr;           // [M]; the gradient's input
   float* mean = nullptr;          // [2], or null
   // gradient
-  const float* dloss = nullptr;
+  const float* dloss = nullptr;   // [M] with dloss_rows, else one word
   int dloss_rows = 0;
   uint16_t* da = nullptr;
   uint16_t* db = nullptr;

@@ -114,14 +114,14 @@ __device__ __forceinline__ float load_bias(const MmArgs& p, int64_t j, float bsc
   return decode_bias(p, load_bias_bits(p, j), bscale);
 }
 
-// Operands of 16 bits (bf16), for products whose sums fp8's in-group truncation
+// Operands of 16 bits (fp16), for products whose sums fp8's in-group truncation
 // (below) would spoil: the same tile in bytes, a step of 128 bytes being 64 k,
 // with leading dimensions, K and strides in bytes too.
-constexpr int kOpBF16 = 8;
+constexpr int kOpF16 = 8;
 template <int W> struct Width {
   static constexpr int value = W;
 };
-template <int F> constexpr int kOpBytes = F == kOpBF16 ? 2 : 1;
+template <int F> constexpr int kOpBytes = F == kOpF16 ? 2 : 1;
 
 // K-major tiles of 16-bit operands: 64 k-rows of 2 W bytes.  A fragment's 16
 // columns are 32 contiguous bytes, so 32-byte granules are rotated: a half-wave of
@@ -152,13 +152,13 @@ template <int W> __device__ __forceinline__ v8i lds_frag_km16(const uint8_t* S, 
   return r;
 }
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ v4f mfma_bf16(const v8i& bfrag, const v8i& afrag, v4f c) {
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ v4f mfma_f16(const v8i& bfrag, const v8i& afrag, v4f c) {
 #pragma unroll
   for (int h = 0; h < 8; h += 4) {
     const v4i b = {bfrag[h], bfrag[h + 1], bfrag[h + 2], bfrag[h + 3]};
     const v4i a = {afrag[h], afrag[h + 1], afrag[h + 2], afrag[h + 3]};
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b), __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, b), __builtin_bit_cast(v8h, a), c, 0, 0, 0);
   }
   return c;
 }
@@ -199,8 +199,8 @@ __device__ __forceinline__ v8i spread_dword(const v8i& f, int s) {
 
 template <int FA, int FB, bool PREC>
 __device__ __forceinline__ v4f mma(const v8i& bfrag, const v8i& afrag, v4f c) {
-  if constexpr (FA == kOpBF16) {
-    return mfma_bf16(bfrag, afrag, c);
+  if constexpr (FA == kOpF16) {
+    return mfma_f16(bfrag, afrag, c);
   } else if constexpr (!PREC) {
     return mfma_nt<FA, FB>(bfrag, afrag, c);
   } else {
@@ -673,7 +673,7 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   // rounding (OUT < 0) or the output quantization (OUT = E4M3 / E5M2).
   const float sa = p.a_scale_inv ? *p.a_scale_inv : 1.0f;
   const float sb = p.b_scale_inv ? *p.b_scale_inv : 1.0f;
-  const float sab = sa * sb;
+  const float sab = P::out_scale(p, sa * sb);
   const int ng = lane >> 4;
   float bias_v[TJ][4];
 #pragma unroll

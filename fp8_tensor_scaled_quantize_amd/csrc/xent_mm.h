@@ -1,8 +1,14 @@
 // The products of the cross entropy over a vocabulary (cross_entropy.hip), on
-// mm_tile (mm_fp8_kernel.h) with bf16 operands -- the E4M3 codes' values, which
-// bf16 holds exactly -- and epilogues of their own.  The fp8 MFMA cuts products to
+// mm_tile (mm_fp8_kernel.h) with fp16 operands -- the E4M3 codes' values, which
+// fp16 holds exactly -- and epilogues of their own.  The fp8 MFMA cuts products to
 // 2^-13 of the largest of eight, always toward zero: 1e-4 of a logit, more than a
-// loss in fp32 may lose.  bf16's products are exact and their sums fp32.
+// loss in fp32 may lose.  fp16's products of codes are exact and their sums fp32.
+//
+// The logits' gradient is kept as exp(l - lse) - [target] times kGScale, without the
+// rows' loss gradients (they are factors of dA's rows, and of A's rows in dB): in
+// [-2^14, 2^14], so that fp16 rounds it by 2^-11 at most and entries below 2^-28 by
+// 2^-39, where bf16 would round by 2^-8: a bf16 gradient is then off by its own
+// rounding alone (64 x 1000 x 512: 0.0017 of its norm, with a bf16 G 0.0025).
 #pragma once
 #include "mm_act_kernel.h"
 
@@ -19,7 +25,9 @@ __device__ __forceinline__ int tile_target(int64_t t, int64_t v0, int64_t n) {
   return t < 0 ? kTargetIgnored : (t >= v0 && t < v0 + n ? (int)(t - v0) : kTargetElsewhere);
 }
 
-// bf16 operands: leading dimensions, K and strides in bytes.  Batch z takes bytes
+constexpr float kGScale = 16384.0f;
+
+// fp16 operands: leading dimensions, K and strides in bytes.  Batch z takes bytes
 // z K .. of a row-major operand's rows (the last batch fewer), and the rows z K / 2 ..
 // of a K-major one's k_major_rows.
 struct Mm16Args : MmArgs {
@@ -32,6 +40,7 @@ struct Mm16Args : MmArgs {
     const int64_t left = p.k_major_rows - bz * (p.K / 2);
     return left < p.K / 2 ? left : p.K / 2;
   }
+  __host__ __device__ static float out_scale(const Mm16Args&, float sab) { return sab * (1.0f / kGScale); }
 };
 
 // What the logits' epilogues share: scales, targets, the piece's first column.
@@ -47,16 +56,14 @@ struct XentArgs : Mm16Args {
   float* target_logit = nullptr;    // [M], in powers of two
   // gradient
   const float* lse = nullptr;       // [M]
-  const float* dloss = nullptr;     // [M], or one word
-  int dloss_rows = 0;
-  uint16_t* d = nullptr;            // bf16 [M, ld_d]
+  uint16_t* d = nullptr;            // fp16 [M, ld_d]
   int64_t ld_d = 0;
 
   struct Rows {
-    float col = 1.0f, row = 1.0f, d = 0.0f;
+    float col = 1.0f, row = 1.0f;
     int target = kTargetElsewhere;
   };
-  template <int BM, int BN> static constexpr int extra_bytes() { return 4 * BN + 12 * BM; }
+  template <int BM, int BN> static constexpr int extra_bytes() { return 4 * BN + 8 * BM; }
   template <int BM, int BN, bool GRAD>
   __device__ static __forceinline__ void fetch_rows(const XentArgs& p, Rows& r, int tid, int64_t m0, int64_t n0) {
     if (p.b_scale_inv && tid < BN) r.col = p.b_scale_inv[p.b_rows ? (n0 + tid < p.N ? n0 + tid : n0) : 0];
@@ -64,23 +71,29 @@ struct XentArgs : Mm16Args {
     const int64_t t = load_target(p.targets, p.target_bits, m0 + tid);
     r.target = tile_target(t, p.v0 + n0, p.N - n0 < BN ? p.N - n0 : BN);
     if constexpr (GRAD) {
-      r.row = p.lse[m0 + tid] * kLog2e;
-      r.d = t < p.vocab ? p.dloss[p.dloss_rows ? m0 + tid : 0] : __builtin_nanf("");
+      r.row = t < p.vocab ? p.lse[m0 + tid] * kLog2e : __builtin_nanf("");
     } else {
       if (p.a_rows) r.row = p.a_scale_inv[m0 + tid];
     }
   }
-  // extra: column scales [BN], row words [BM], targets [BM], loss gradients [BM]
+  // extra: column scales [BN], row words [BM], targets [BM]
   template <int BM, int BN> __device__ static __forceinline__ void park(const XentArgs&, const Rows& r, int tid, uint8_t* extra) {
     float* f = reinterpret_cast<float*>(extra);
     if (tid < BN) f[tid] = r.col;
     if (tid < BM) {
       f[BN + tid] = r.row;
       reinterpret_cast<int*>(f)[BN + BM + tid] = r.target;
-      f[BN + 2 * BM + tid] = r.d;
     }
   }
 };
+
+template <int C> __device__ __forceinline__ void pack_f16(uint32_t (&w)[C / 2], const float (&f)[C]) {
+#pragma unroll
+  for (int e = 0; e < C; e += 2) {
+    const f32x2 v = {f[e], f[e + 1]};
+    w[e / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  }
+}
 
 // A logit in powers of two is acc * (sa_i sb_j log2 e).
 __device__ __forceinline__ float logit_scale(const XentArgs& p) {
@@ -167,7 +180,7 @@ struct XentLseArgs : XentArgs {
   }
 };
 
-// d (exp(l - lse) - [target]) in bf16, rows of the gradient's two products.
+// kGScale (exp(l - lse) - [target]) in fp16, rows of the gradient's two products.
 struct XentGradArgs : XentArgs {
   template <int BM, int BN>
   __device__ static __forceinline__ void fetch(const XentArgs& p, Rows& r, int tid, int64_t m0, int64_t n0) {
@@ -182,7 +195,6 @@ struct XentGradArgs : XentArgs {
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wid / WAVES_N, wn = wid % WAVES_N;
     const float* const rows = reinterpret_cast<const float*>(extra) + BN;
     const int* const tgt = reinterpret_cast<const int*>(extra) + BN + BM;
-    const float* const dl = reinterpret_cast<const float*>(extra) + BN + 2 * BM;
     const float s = logit_scale(p) * (p.b_scale_inv ? *p.b_scale_inv : 1.0f);
     // whole groups of eight columns are written: those past the vocabulary as zeros
     const int64_t cl = p.N - n0 - wn * WN;
@@ -191,7 +203,7 @@ struct XentGradArgs : XentArgs {
     for (int i = 0; i < TI; ++i) {
       const int lr = wm * WM + 16 * i + r16;
       const bool in = m0 + lr < p.M;
-      const float lse = rows[lr], d = dl[lr];
+      const float lse = rows[lr];
       const int own = tgt[lr] - wn * WN;
       const bool ignored = tgt[lr] == kTargetIgnored;
       uint16_t* const out = p.d + (m0 + lr) * p.ld_d + n0 + wn * WN;
@@ -204,7 +216,7 @@ struct XentGradArgs : XentArgs {
         for (int e = 0; e < C; ++e) {
           float q = __builtin_amdgcn_exp2f(fmaf(t[e], s, -lse));
           if (own == at + e) q -= 1.0f;
-          t[e] = ignored ? 0.0f : q * d;
+          t[e] = ignored ? 0.0f : q * kGScale;
         }
         if (cols_in < WN) {
 #pragma unroll
@@ -213,7 +225,7 @@ struct XentGradArgs : XentArgs {
         }
         if (in && (at & ~7) < cols_in) {
           uint32_t w[C / 2];
-          pack_bf16<C>(w, t);
+          pack_f16<C>(w, t);
           store_words<C / 2, 2, STREAM>(reinterpret_cast<uint8_t*>(out + at), w, C);
         }
       }
@@ -262,7 +274,7 @@ static hipError_t launch_mm16_tile(const P& p0, hipStream_t st) {
   P p = p0;
   // several rounds of tiles, or long sums (a K split of G B is 128 steps and more: 237 -> 214 us)
   p.early_loads = tiles_m * tiles_n * p0.batch > (int64_t)device_cu_count() || p0.K >= 64 * kBK;
-  hipLaunchKernelGGL((mm_fp8_dma<kOpBF16, kOpBF16, BM, BN, WM_, WN_, MINB, -1, LAY, false, DEEP, P>),
+  hipLaunchKernelGGL((mm_fp8_dma<kOpF16, kOpF16, BM, BN, WM_, WN_, MINB, -1, LAY, false, DEEP, P>),
                      dim3((unsigned)(tiles_m * tiles_n), 1, (unsigned)p0.batch), dim3(64 * WM_ * WN_), 0, st, p, tiles_m,
                      tiles_n, 4);
   return hipGetLastError();

@@ -470,8 +470,8 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
 /*
  * fp8_cross_entropy -- softmax cross entropy over a vocabulary, straight from the
  * head's fp8 operands: the logits are never written.
- *   l(i,j) = sa_i sb_j sum_k dec(A(i,k)) dec(B(j,k))      (bf16 MFMA on the codes' values,
- *            which bf16 holds exactly, with fp32 sums)
+ *   l(i,j) = sa_i sb_j sum_k dec(A(i,k)) dec(B(j,k))      (fp16 MFMA on the codes' values,
+ *            which fp16 holds exactly, with fp32 sums)
  *   lse_i  = log sum_j exp l(i,j)         loss_i = lse_i - l(i, t_i)
  *   a, b       device E4M3 codes of the rows [M, K] and of the vocabulary's weights
  *              [N, K]; K (a multiple of 16, at most 65536), lda, ldb (at most 2^24) multiples
@@ -497,9 +497,11 @@ FP8MI_API size_t fp8_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t
 /*
  * fp8_cross_entropy_grad -- gradient of sum_i dloss_i loss_i with respect to the
  * head's operands, the logits computed once more:
- *   G(i,j) = dloss_i (exp(l(i,j) - lse_i) - [j = t_i])    rounded to bf16; 0 for an
- *            ignored row, NaN for one whose target is N or more
- *   da = sb G dec(B)        db = sa G^T dec(A)            fp32 sums, one bf16 rounding
+ *   G(i,j) = exp(l(i,j) - lse_i) - [j = t_i]      rounded to fp16 (2^-11, or 2^-39 in all);
+ *            0 for an ignored row, NaN for one whose target is N or more
+ *   da(i,k) = sb dloss_i sum_j G(i,j) dec(B(j,k))         fp32 sums, one bf16 rounding
+ *   db(j,k) = sa sum_i dloss_i G(i,j) dec(A(i,k))         (dloss_i A rounded to fp16 where
+ *            there is one per row); the codes and dloss of ignored rows are not used
  * Arguments as fp8_cross_entropy, with one scale per operand (the two factors leave the
  * sums), and
  *   lse        device fp32 [M]: the forward call's.

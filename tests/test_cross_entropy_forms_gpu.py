@@ -67,9 +67,9 @@ def test_forms(M, N, K):
     n = int((t >= 0).sum())
     assert abs(float(mean[0]) - float(wloss.sum()) / n) <= 1e-5 and abs(float(mean[1]) * n - 1) < 1e-6
     da, db = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
-    # G and the outputs round to bf16 once each, independently
+    # the outputs round to bf16, G and the rows of d A to fp16 (an eighth of it), independently
     for got, want in ((da, wda), (db, wdb)):
-        assert (got - want).norm() / want.norm() <= 2 * HALF
+        assert (got - want).norm() / want.norm() <= 1.25 * HALF
         big = want.abs().amax(1)
         # no row is off as a whole
         assert ((got - want).norm(dim=1) <= 4 * HALF * want.norm(dim=1) + 1e-6 * big.max()).all()

@@ -67,22 +67,26 @@ class Case:
         # G's error before its rounding: the argument's (logit, lse, product with log2 e) and exp2's
         eg = g * (self.el + 4 * R.U32 * (np.abs(l) + np.abs(f64(lse))[:, None]) + 4 * R.U32)
         g[np.arange(M), np.maximum(self.t, 0)] -= 1
-        d = np.where(self.t >= 0, np.broadcast_to(dloss, M), 0.0)[:, None]
-        g, eg = g * d, eg * np.abs(d) + np.abs(g * d) * 2 * R.U32
+        eg = eg + 2 * R.U32 * np.abs(g)
         before = eg
-        eg = eg + (np.abs(g) + eg) * HALF  # rounded to bf16
+        eg = eg + (np.abs(g) + eg) * 2.0 ** -11 + 2.0 ** -39  # rounded to fp16, in units of 2^-14
+        d = np.where(self.t >= 0, np.broadcast_to(dloss, M), 0.0)[:, None]
         a, b = R.decode_e4m3(self.codes[0]) * float(self.sa[0]), R.decode_e4m3(self.codes[1]) * float(self.sb[0])
-        for got, x, y, ex, e0, n in ((da, g, b, eg, before, len(b)), (db, g.T, a, eg.T, before.T, len(a))):
+        # with a dloss per row db takes fp16 rows of d A: a half step (or 2^-25 of the largest d's unit) of each more
+        ea = np.abs(d * a) * 2.0 ** -11 + 2.0 ** -24 * np.abs(d).max() * float(self.sa[0]) if np.size(dloss) > 1 else 0 * a
+        for got, x, y, ex, e0, ey, n in ((da, d * g, b, np.abs(d) * eg, np.abs(d) * before, 0 * b, len(b)),
+                                         (db, g.T, d * a, eg.T, before.T, ea, len(a))):
             if got is None:
                 continue
             want = x @ y
-            # sums of n terms in fp32 and one rounding to bf16
-            err = ex @ np.abs(y) + (n + 8) * 2 * R.U32 * (np.abs(x) @ np.abs(y))
+            # sums of n terms in fp32, their factors' roundings, and one rounding to bf16
+            err = ex @ np.abs(y) + (np.abs(x) + ex) @ ey + (n + 8) * 2 * R.U32 * (np.abs(x) @ np.abs(y))
             assert (np.abs(f64(got) - want) <= err + HALF * (np.abs(want) + err)).all()
-            # and as a whole: G's roundings, at most half a step of each and independent (so no larger in the sums than in
-            # G), and the output's; apart from what G is off by before it is rounded (with one column G is that alone)
+            # and as a whole: the output's half steps, G's and d A's (an eighth of those each; all independent), apart from
+            # what G is off by before it is rounded (with one column G is that alone)
             off = np.linalg.norm(f64(got) - want)
-            assert off <= 2 * HALF * np.linalg.norm(want) + np.linalg.norm(e0 @ np.abs(y)), off
+            tiny = 2.0 ** -39 * np.sqrt(x.size) * np.linalg.norm(y)
+            assert off <= 1.25 * HALF * np.linalg.norm(want) + np.linalg.norm(e0 @ np.abs(y)) + tiny, off
 
 
 SHAPES = [(1, 2, 16), (1, 1, 16), (3, 17, 32), (16, 255, 64), (17, 256, 128), (64, 257, 144), (65, 1000, 512), (127, 513, 48),
@@ -161,18 +165,22 @@ def test_everything_ignored_and_no_rows():
 
 @pytest.mark.parametrize("M", [20, 300])
 def test_nan_rows_and_targets_past_the_vocabulary(M):
-    """A NaN code makes its own row's loss NaN; an ignored row with one stays out of
-    both gradients' other rows; a target past the vocabulary gives NaN."""
+    """A NaN code makes its own row's loss NaN; an ignored row with one, or with a
+    NaN dloss, stays out of both gradients; a target past the vocabulary gives NaN."""
     c = Case(M, 400, 64, seed=8, ignored=0.0)
     c.a[3, 5] = 0x7F
     c.targets[3] = -1
     loss, lse = c.forward()
     assert loss[3] == 0 and torch.isnan(lse[3]) and torch.isfinite(loss).all()
     da, db = fp8mi.fp8_cross_entropy_grad(c.a, c.b, c.targets, lse, torch.ones(1, device=DEV), *c.scales)
-    assert not da[3].any() and torch.isfinite(da).all()
-    # db's column 5 sums 0 * NaN: the ignored row's own code
-    rest = torch.arange(64, device=DEV) != 5
-    assert torch.isfinite(db[:, rest]).all()
+    assert not da[3].any() and torch.isfinite(da).all() and torch.isfinite(db).all()
+    dl = torch.full((M,), 0.25, device=DEV)
+    same = fp8mi.fp8_cross_entropy_grad(c.a, c.b, c.targets, lse, dl, *c.scales)
+    dl[3] = float("nan")
+    odd = fp8mi.fp8_cross_entropy_grad(c.a, c.b, c.targets, lse, dl, *c.scales)
+    assert torch.equal(odd[0], same[0]) and torch.equal(odd[1], same[1])
+    assert torch.equal(same[0], (0.25 * da.float()).to(torch.bfloat16))  # powers of two leave the roundings alone
+    assert torch.equal(same[1], (0.25 * db.float()).to(torch.bfloat16))
     c.targets[3] = 7
     loss, lse = c.forward()
     assert torch.isnan(loss[3]) and int(torch.isnan(loss).sum()) == 1
@@ -224,6 +232,17 @@ def test_captured_on_a_stream_and_the_same_every_time():
         torch.cuda.synchronize()
         for got, w in zip((loss, lse, mean, da, db), want):
             assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e6, 1e30])
+def test_dloss_of_any_size(size):
+    """One dloss, and rows a factor of 10^4 apart: each of da's rows has its own
+    precision, db that of its largest terms."""
+    c = Case(100, 300, 64, seed=14, ignored=0.1)
+    _, lse = c.forward()
+    for d in (torch.full((1,), size, device=DEV), torch.logspace(-4, 0, 100, device=DEV) * size):
+        da, db = fp8mi.fp8_cross_entropy_grad(c.a, c.b, c.targets, lse, d, *c.scales)
+        c.check_grad(da, db, f64(d), lse)
 
 
 def test_gradient_against_differences():
