@@ -116,13 +116,12 @@ struct Widen {
   const float* rows_by;
   uint16_t* out_scaled;
 };
-__global__ void __launch_bounds__(256) widen_codes(Widen a, Widen b, uint32_t* ticket) {
+__device__ __forceinline__ void widen_group(const Widen& a, const Widen& b, int64_t group) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  if (ticket && threadIdx.x + blockIdx.x == 0) *ticket = 0u;  // for the join, launches on
   const int64_t groups_a = (a.chunks + 511) / 512;
-  const bool first = (int64_t)blockIdx.x < groups_a;
+  const bool first = group < groups_a;
   const Widen& m = first ? a : b;
-  const int64_t at = ((int64_t)blockIdx.x - (first ? 0 : groups_a)) * 512 + threadIdx.x;
+  const int64_t at = (group - (first ? 0 : groups_a)) * 512 + threadIdx.x;
   u32x4 v[2];
   int64_t out[2], row[2];
 #pragma unroll
@@ -164,12 +163,17 @@ __global__ void __launch_bounds__(256) widen_codes(Widen a, Widen b, uint32_t* t
   }
 }
 
+__global__ void __launch_bounds__(256) widen_codes(Widen a, Widen b, uint32_t* ticket) {
+  if (ticket && threadIdx.x + blockIdx.x == 0) *ticket = 0u;  // for the join, launches on
+  widen_group(a, b, blockIdx.x);
+}
+int64_t widen_groups(const Widen& a, const Widen& b) { return (a.chunks + 511) / 512 + (b.chunks + 511) / 512; }
+
 Widen widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, int64_t ld_out) {
   return {x, out, ld, ld_out, R * (C / 16), (int32_t)(C / 16), 0, nullptr, nullptr, nullptr, nullptr};
 }
 hipError_t launch_widen(const Widen& a, const Widen& b, uint32_t* ticket, hipStream_t st) {
-  const int64_t groups = (a.chunks + 511) / 512 + (b.chunks + 511) / 512;
-  hipLaunchKernelGGL(widen_codes, dim3((unsigned)groups), dim3(256), 0, st, a, b, ticket);
+  hipLaunchKernelGGL(widen_codes, dim3((unsigned)widen_groups(a, b)), dim3(256), 0, st, a, b, ticket);
   return hipGetLastError();
 }
 
@@ -198,15 +202,33 @@ __global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const vo
 // alike, so that a load instruction reads 64 contiguous bytes of a row.  The
 // waves' sums meet in LDS, and wave i finishes strip i.  (1 x 32768 x 1536, widened
 // and in 128 x 128 tiles: 60 us; this: MEASURE.)
-template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentArgs p, uint32_t* ticket) {
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * TI);
+struct RowsGrad {  // what the gradient's form does besides: the operands' 16-bit forms, for the products after it
+  static constexpr bool kGrad = true;
+  Widen a, b;
+};
+struct RowsStats {
+  static constexpr bool kGrad = false;
+  uint32_t* ticket;
+};
+template <int TI, int TJ, class G>
+__global__ void __launch_bounds__(256) xent_rows(XentArgs p, G extra, uint32_t col_blocks, uint32_t blocks) {
+  if constexpr (G::kGrad) {
+    if (blockIdx.x >= blocks) {
+      widen_group(extra.a, extra.b, blockIdx.x - blocks);
+      return;
+    }
+  }
+  const uint32_t row_block = blockIdx.x / col_blocks, col_block = blockIdx.x % col_blocks;
+  const int64_t m0 = (int64_t)row_block * (16 * TI);
   constexpr int NW = 4, U = TI == 4 ? 2 : 3;
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   __shared__ float4 part[NW][TI][TJ][64];
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (tid + blockIdx.x + blockIdx.y == 0) *ticket = 0u;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * TJ);
+  if constexpr (!G::kGrad) {
+    if (tid + blockIdx.x == 0) *extra.ticket = 0u;
+  }
+  const int64_t n0 = (int64_t)col_block * (16 * TJ);
   // raw buffers: rows past an edge and chunks past K read as zero
   const int64_t a_rows = p.M - m0 < 16 * TI ? p.M - m0 : 16 * TI;
   const int ext_a = (int)((a_rows - 1) * p.lda + p.K);
@@ -308,20 +330,42 @@ template <int TI, int TJ> __global__ void __launch_bounds__(256) xent_rows(XentA
       const bool has = col < p.N;
       const float sb = p.b_scale_inv ? p.b_scale_inv[p.b_rows ? (has ? col : 0) : 0] : 1.0f;
       x[j][e] = has ? v[e] * (s * sb) : -__builtin_inff();
-      if (has && in && col == t) p.target_logit[row] = x[j][e];
-      m = fmaxf(m, x[j][e]);
+      if constexpr (!G::kGrad) {
+        if (has && in && col == t) p.target_logit[row] = x[j][e];
+        m = fmaxf(m, x[j][e]);
+      }
     }
   }
-  m = fmaxf(m, __shfl_xor(m, 16, 64));
-  m = fmaxf(m, __shfl_xor(m, 32, 64));
-  const float ref = m > -3.0e38f ? m : 0.0f;
+  if constexpr (G::kGrad) {  // as XentGradArgs: groups of eight columns, those past the vocabulary as zeros
+    if (!in) return;
+    const float lse = t < p.vocab ? p.lse[row] * kLog2e : __builtin_nanf("");
 #pragma unroll
-  for (int j = 0; j < TJ; ++j)
+    for (int j = 0; j < TJ; ++j) {
+      const int64_t at = n0 + 16 * j + 4 * g;
+      if ((at & ~(int64_t)7) >= p.N) continue;
+      float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(x[j][e] - ref);
-  sum += __shfl_xor(sum, 16, 64);
-  sum += __shfl_xor(sum, 32, 64);
-  if (g == 0 && in) p.parts[(int64_t)blockIdx.x * p.M + row] = make_float2(m, sum);
+      for (int e = 0; e < 4; ++e) {
+        float q = __builtin_amdgcn_exp2f(x[j][e] - lse);
+        if (p.v0 + at + e == t) q -= 1.0f;
+        v[e] = t < 0 || at + e >= p.N ? 0.0f : q * kGScale;
+      }
+      uint32_t w[2];
+      pack_f16<4>(w, v);
+      *reinterpret_cast<uint2*>(p.d + row * p.ld_d + at) = make_uint2(w[0], w[1]);
+    }
+  } else {
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    const float ref = m > -3.0e38f ? m : 0.0f;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(x[j][e] - ref);
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if (g == 0 && in) p.parts[(int64_t)col_block * p.M + row] = make_float2(m, sum);
+  }
 }
 
 // Joins the statistics of `tiles` column tiles: a workgroup takes RB rows, its
@@ -478,12 +522,18 @@ void fill_logits(XentArgs& p, const XentCall& c, const uint16_t* a16, const uint
 int64_t xent_workspace_bytes(int64_t M, int64_t N, int64_t K) { return ForwardPlan(M, N, K).bytes; }
 int64_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K) { return BackwardPlan(M, N, K).bytes; }
 
-template <int TJ> static hipError_t launch_rows(const XentArgs& p, uint32_t* ticket, hipStream_t st) {
-  const dim3 grid((unsigned)((p.N + 16 * TJ - 1) / (16 * TJ)), (unsigned)((p.M + 63) / 64)), block(256);
-  if (p.M <= 16) hipLaunchKernelGGL((xent_rows<1, TJ>), grid, block, 0, st, p, ticket);
-  else if (p.M <= 32) hipLaunchKernelGGL((xent_rows<2, TJ>), grid, block, 0, st, p, ticket);
-  else hipLaunchKernelGGL((xent_rows<4, TJ>), grid, block, 0, st, p, ticket);
-  return hipGetLastError();
+template <int TJ, class G>
+static hipError_t launch_rows(const XentArgs& p, const G& extra, int64_t more, hipStream_t st) {
+  const int64_t rows = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : 64), cols = (p.N + 16 * TJ - 1) / (16 * TJ);
+  const int64_t blocks = cols * ((p.M + rows - 1) / rows);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks + more)), dim3(256), 0, st, p, extra, (uint32_t)cols, (uint32_t)blocks);
+    return hipGetLastError();
+  };
+  return rows == 16 ? go(xent_rows<1, TJ, G>) : rows == 32 ? go(xent_rows<2, TJ, G>) : go(xent_rows<4, TJ, G>);
+}
+template <class G> static hipError_t launch_rows(const XentArgs& p, const G& extra, int64_t more, hipStream_t st) {
+  return rows_tile(p.N) == 32 ? launch_rows<2>(p, extra, more, st) : launch_rows<1>(p, extra, more, st);
 }
 
 hipError_t launch_xent_forward(const XentCall& c, hipStream_t st) {
@@ -504,7 +554,7 @@ hipError_t launch_xent_forward(const XentCall& c, hipStream_t st) {
     p.parts = parts;
     p.target_logit = logit;
     tiles = (c.N + plan.tile - 1) / plan.tile;
-    FP8MI_TRY(plan.tile == 32 ? launch_rows<2>(p, ticket, st) : launch_rows<1>(p, ticket, st));
+    FP8MI_TRY(launch_rows(p, RowsStats{ticket}, 0, st));
   } else {
     uint16_t* const a16 = reinterpret_cast<uint16_t*>(c.ws + plan.a16);
     uint16_t* const b16 = reinterpret_cast<uint16_t*>(c.ws + plan.b16);
@@ -562,41 +612,42 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
       rows.rows_by = scale;
       rows.out_scaled = at(plan.a16d);
     }
-    FP8MI_TRY(launch_widen(rows, widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld), nullptr, st));
+    const Widen weights = widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld);
     XentGradArgs g;
     fill_logits(g, c, at(plan.a16), at(plan.b16), plan.ld, v0, n);
     g.lse = c.lse;
     g.d = at(plan.g); g.ld_d = plan.ld_g;
-    FP8MI_TRY(launch_xent_grad(g, st));
-    if (c.da) {  // G by rows, the piece's weights K-major
-      AddArgs p;
-      p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
-      p.b = reinterpret_cast<const uint8_t*>(at(plan.b16));
-      p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld;
-      p.M = c.M; p.N = c.K;
-      p.k_total = 2 * up(n, 8);
-      p.k_major_rows = n;
-      p.K = k_split;
-      p.batch = (p.k_total + k_split - 1) / k_split;
-      p.stride_a = k_split;
-      p.stride_b = k_split / 2 * p.ldb;
-      p.sums = sums;
-      p.first = v0 == 0;
-      FP8MI_TRY(launch_mm16_add(p, st));
+    if (few_rows(c.M, n)) {  // the logits straight from the codes, beside the widening
+      g.a = c.a; g.b = c.b + v0 * c.ldb; g.lda = c.lda; g.ldb = c.ldb; g.K = c.K;
+      FP8MI_TRY(launch_rows(g, RowsGrad{rows, weights}, widen_groups(rows, weights), st));
+    } else {
+      FP8MI_TRY(launch_widen(rows, weights, nullptr, st));
+      FP8MI_TRY(launch_xent_grad(g, st));
     }
-    if (c.db) {  // both K-major
-      Mm16Args p;
-      p.a = reinterpret_cast<const uint8_t*>(at(plan.g));
-      p.b = reinterpret_cast<const uint8_t*>(at(scaled ? plan.a16d : plan.a16));
-      p.lda = 2 * plan.ld_g; p.ldb = 2 * plan.ld;
-      p.M = n; p.N = c.K; p.batch = 1;
-      p.K = p.k_total = 2 * up(c.M, 8);
-      p.k_major_rows = c.M;
-      p.a_scale_inv = c.a_scale_inv;
-      p.b_scale_inv = scaled ? scale : c.dloss;
-      p.c = c.db + v0 * c.ld_db; p.ldc = c.ld_db; p.stride_c = 0;
-      FP8MI_TRY(launch_mm16_km(p, st));
-    }
+    AddArgs add;  // G by rows, the piece's weights K-major
+    add.a = reinterpret_cast<const uint8_t*>(at(plan.g));
+    add.b = reinterpret_cast<const uint8_t*>(at(plan.b16));
+    add.lda = 2 * plan.ld_g; add.ldb = 2 * plan.ld;
+    add.M = c.M; add.N = c.K;
+    add.k_total = 2 * up(n, 8);
+    add.k_major_rows = n;
+    add.K = k_split;
+    add.batch = (add.k_total + k_split - 1) / k_split;
+    add.stride_a = k_split;
+    add.stride_b = k_split / 2 * add.ldb;
+    add.sums = sums;
+    add.first = v0 == 0;
+    Mm16Args km;  // both K-major
+    km.a = reinterpret_cast<const uint8_t*>(at(plan.g));
+    km.b = reinterpret_cast<const uint8_t*>(at(scaled ? plan.a16d : plan.a16));
+    km.lda = 2 * plan.ld_g; km.ldb = 2 * plan.ld;
+    km.M = n; km.N = c.K; km.batch = 1;
+    km.K = km.k_total = 2 * up(c.M, 8);
+    km.k_major_rows = c.M;
+    km.a_scale_inv = c.a_scale_inv;
+    km.b_scale_inv = scaled ? scale : c.dloss;
+    km.c = c.db + v0 * c.ld_db; km.ldc = c.ld_db; km.stride_c = 0;
+    FP8MI_TRY(launch_mm16_grads(c.da ? &add : nullptr, c.db ? &km : nullptr, st));
   }
   if (!c.da) return hipSuccess;
   hipLaunchKernelGGL(xent_finish_da, dim3((unsigned)((c.M * c.K / 4 + 255) / 256)), dim3(256), 0, st, sums, splits, c);

@@ -298,8 +298,9 @@ static inline int pick16(int64_t M, int64_t N, int64_t batch, bool narrow) {
 // one epilogue each
 hipError_t launch_xent_lse(const XentLseArgs& p, hipStream_t st);
 hipError_t launch_xent_grad(const XentGradArgs& p, hipStream_t st);
-hipError_t launch_mm16_add(const AddArgs& p, hipStream_t st);    // A by rows, B K-major
-hipError_t launch_mm16_km(const Mm16Args& p, hipStream_t st);    // both K-major, plain epilogue
+// G B into fp32 sums (A by rows, B K-major) and G^T A (both K-major, plain epilogue);
+// either may be null.
+hipError_t launch_mm16_grads(const AddArgs* add, const Mm16Args* km, hipStream_t st);
 int64_t xent_lse_tile(int64_t M, int64_t N);  // columns that share a row's statistics
 
 }  // namespace fp8mi
