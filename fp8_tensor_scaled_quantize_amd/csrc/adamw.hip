@@ -140,19 +140,20 @@ __device__ __forceinline__ void store_codes4(uint8_t* p, int64_t i, uint32_t w, 
 // v so that v itself (not its root) is met on average.  v > 0 never becomes 0:
 // a later step without a gradient would divide m by eps alone.
 
-// max over the wave's 64 lanes in every lane, NaN kept
-__device__ __forceinline__ float wave_maximum(float v) {
-  const auto step = [](float x, uint32_t y) { return __builtin_elementwise_maximum(x, __uint_as_float(y)); };
-#define FP8MI_ROR(n) __builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + n, 0xf, 0xf, false)
-  v = step(v, FP8MI_ROR(8));
-  v = step(v, FP8MI_ROR(4));
-  v = step(v, FP8MI_ROR(2));
-  v = step(v, FP8MI_ROR(1));
+// Magnitudes are compared as the bits of non-negative floats, whose order theirs
+// is; a NaN is above all.  Max over the wave's 64 lanes in every lane:
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+#define FP8MI_ROR(n) (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xf, 0xf, true)
+  v = umax(v, FP8MI_ROR(8));
+  v = umax(v, FP8MI_ROR(4));
+  v = umax(v, FP8MI_ROR(2));
+  v = umax(v, FP8MI_ROR(1));
 #undef FP8MI_ROR
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = step(__uint_as_float(a[0]), a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return step(__uint_as_float(b[0]), b[1]);
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = umax(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return umax(b[0], b[1]);
 }
 
 // Scale word of a block whose largest magnitude is `most`.  Below 2^-100 a block
@@ -172,6 +173,17 @@ __device__ __forceinline__ uint32_t grid_steps(float y, float& k, float& f) {
   k = floorf(t);
   f = t - k;
   return (e >> 20) - 968u + (uint32_t)k;
+}
+
+// y >= 0 rounded to the grid point above with the probability of its place between
+// the two: h16 / 2^16 against the 20 bits below a code's mantissa.  Adding to the
+// value's bits carries into the exponent as the codes' order does; subnormals (the
+// grid 2^-9 below 2^-6) go one binade up, where that is the grid.
+__device__ __forceinline__ uint32_t round_code(float y, uint32_t h16) {
+  y = fminf(y, 448.0f);
+  const bool small = y < 0.015625f;
+  const uint32_t bits = __float_as_uint(small ? y + 0.015625f : y);
+  return ((bits + (0xFFFF7u - 16u * h16)) >> 20) - (small ? 968u : 960u);
 }
 
 // A 32-bit integer hash (two multiplications between shifts).
@@ -252,10 +264,8 @@ __device__ __forceinline__ void adamw_chunk(const fp8mi_adamw_tensor& t, const A
       const f32x2 m1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)rm[b].w[0], true);
       const f32x2 r0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)rv[b].w[0], false);
       const f32x2 r1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)rv[b].w[0], true);
-      m[0] = m0[0] * ms[b]; m[1] = m0[1] * ms[b]; m[2] = m1[0] * ms[b]; m[3] = m1[1] * ms[b];
-      r[0] = r0[0] * vs[b]; r[1] = r0[1] * vs[b]; r[2] = r1[0] * vs[b]; r[3] = r1[1] * vs[b];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = r[e] * r[e];
+      m[0] = m0[0]; m[1] = m0[1]; m[2] = m1[0]; m[3] = m1[1];  // in units of the blocks' scales
+      r[0] = r0[0]; r[1] = r0[1]; r[2] = r1[0]; r[3] = r1[1];
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -263,34 +273,28 @@ __device__ __forceinline__ void adamw_chunk(const fp8mi_adamw_tensor& t, const A
         v[e] = __uint_as_float(rv[b].w[e]);
       }
     }
-    float mm = 0.0f, rr = 0.0f;
+    if constexpr (BYTES) {
+      uint32_t mm = 0u, rr = 0u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      g[e] *= c;
-      m[e] = b1 * m[e] + a1 * g[e];
-      v[e] = b2 * v[e] + a2 * g[e] * g[e];
-      if constexpr (BYTES) {
+      for (int e = 0; e < 4; ++e) {
+        m[e] = fmaf(m[e], b1 * ms[b], g[e] * (c * a1));
+        const float q = r[e] * (h.root_beta2 * vs[b]), z = g[e] * (c * h.root_one_beta2);
+        v[e] = fmaf(z, z, q * q);
         // one ulp each is far below the codes' steps
         r[e] = __builtin_amdgcn_sqrtf(v[e]);
-        w[e] = w[e] * decay - s.step_size * m[e] * __builtin_amdgcn_rcpf(r[e] * s.root_scale + h.eps);
-        mm = __builtin_elementwise_maximum(mm, fabsf(m[e]));
-        rr = __builtin_elementwise_maximum(rr, r[e]);
-      } else {
-        w[e] = w[e] * decay - s.step_size * m[e] / (sqrtf(v[e]) * s.root_scale + h.eps);
+        w[e] = fmaf(w[e], decay, -(s.step_size * m[e]) * __builtin_amdgcn_rcpf(fmaf(r[e], s.root_scale, h.eps)));
+        mm = umax(mm, __float_as_uint(fabsf(m[e])));
+        rr = umax(rr, __float_as_uint(r[e]));
       }
-    }
-    if constexpr (BYTES) {
-      const float sm = block_scale(wave_maximum(mm)), sr = block_scale(wave_maximum(rr));
-      const float im = sm != 0.0f ? 1.0f / sm : 0.0f, ir = sr != 0.0f ? 1.0f / sr : 0.0f;
+      const float sm = block_scale(__uint_as_float(wave_umax(mm))), sr = block_scale(__uint_as_float(wave_umax(rr)));
+      const float im = sm != 0.0f ? __builtin_amdgcn_rcpf(sm) : 0.0f, ir = sr != 0.0f ? __builtin_amdgcn_rcpf(sr) : 0.0f;
       const uint64_t group = (uint64_t)i >> 2;
       uint32_t x = mix32((uint32_t)group ^ key ^ mix32((uint32_t)(group >> 32))) | 1u, cm = 0u, cv = 0u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        cm |= (round_code(fabsf(m[e]) * im, x & 0xFFFFu) | ((__float_as_uint(m[e]) >> 24) & 0x80u)) << (8 * e);
         float k, f;
-        uint32_t code = grid_steps(fabsf(m[e]) * im, k, f);
-        code += unit16(x) < f ? 1u : 0u;
-        cm |= (code | ((__float_as_uint(m[e]) >> 24) & 0x80u)) << (8 * e);
-        code = grid_steps(r[e] * ir, k, f);
+        uint32_t code = grid_steps(r[e] * ir, k, f);
         code += unit16(x >> 16) * (2.0f * k + 1.0f) < f * (2.0f * k + f) || (k == 0.0f && f > 0.0f) ? 1u : 0u;
         cv |= code << (8 * e);
         x ^= x << 13;
@@ -304,6 +308,13 @@ __device__ __forceinline__ void adamw_chunk(const fp8mi_adamw_tensor& t, const A
         t.exp_avg_sq_scale[i / kBlock] = sr;
       }
     } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] *= c;
+        m[e] = b1 * m[e] + a1 * g[e];
+        v[e] = b2 * v[e] + a2 * g[e] * g[e];
+        w[e] = w[e] * decay - s.step_size * m[e] / (sqrtf(v[e]) * s.root_scale + h.eps);
+      }
       store4(t.exp_avg, kF32, i, m, n[b]);
       store4(t.exp_avg_sq, kF32, i, v, n[b]);
     }
