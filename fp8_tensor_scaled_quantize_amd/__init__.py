@@ -933,7 +933,7 @@ def _dtypes(ts, name: str):
 def _all_on_device(*lists) -> None:
     """_on_device for lists of tensors (no None among them)."""
     here = {t.get_device() for ts in lists for t in ts}
-    if len(here) != 1 or here.pop() != _current_device():
+    if len(here) != 1 or min(here) < 0 or min(here) != _current_device():
         for ts in lists:
             _on_device(*ts)  # says which
         _on_device(*[ts[0] for ts in lists if len(ts)])

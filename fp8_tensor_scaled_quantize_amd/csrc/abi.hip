@@ -771,7 +771,6 @@ fp8mi_status fp8_adamw_step(const fp8mi_adamw_tensor* tensors, int32_t count, co
   AdamWHyper a;
   a.lr = (float)h.lr; a.beta1 = (float)h.beta1; a.beta2 = (float)h.beta2;
   a.one_beta1 = (float)(1.0 - h.beta1); a.one_beta2 = (float)(1.0 - h.beta2); a.eps = (float)h.eps;
-  a.root_beta2 = (float)sqrt(h.beta2); a.root_one_beta2 = (float)sqrt(1.0 - h.beta2);
   a.t = (uint32_t)h.step; a.seed = h.seed;
   a.step_size = a.root_scale = 0.0f;
   if (!h.step_device) {

@@ -211,7 +211,6 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st);
 // AdamW and the gradient norm (adamw.hip), over the ABI's own tensor lists.
 struct AdamWHyper {
   float lr, beta1, beta2, one_beta1, one_beta2, eps;  // one_beta: 1 - beta
-  float root_beta2, root_one_beta2;                   // roots of beta2 and one_beta2
   float step_size, root_scale;    // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   uint32_t t, seed;
   const float* grad_scale;        // or null; not finite: the step is skipped

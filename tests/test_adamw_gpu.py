@@ -144,6 +144,26 @@ def test_first_steps_and_scale(bits):
         c.check(old, t, 0.01, float(scale))
 
 
+@pytest.mark.parametrize("gdt", ["bf16", "f32"])
+def test_codes_are_those_of_ieee_arithmetic(gdt):
+    """Each code and scale is the formula's in fp32, bit for bit (a code that fell
+    the other way now and then would make runs of other builds drift apart).
+    Values below 2^-6 of a code step's grid (2^-15 of a block's largest) are left
+    out: there the sum of the rounding's number and the value is rounded once more."""
+    c = Case([300000, 777], "bf16", gdt, 8, True, 0, seed=21)
+    before = [[t.cpu().numpy().copy() for t in ts] for ts in (c.m, c.ms, c.v, c.vs, [x.float() for x in c.g])]
+    scale = torch.full((1,), 0.61, device=DEV)
+    c.run(12, 0.1, scale, seed=31)
+    for i in range(2):
+        m, ms, v, vs, g = (b[i] for b in before)
+        wm, wms, wr, wvs = R.adamw8_fp32(m, ms, v, vs, g, 31, 12, i, HP["b1"], HP["b2"], float(scale))
+        assert (c.ms[i].cpu().numpy() == wms).all() and (c.vs[i].cpu().numpy() == wvs).all()
+        assert (R.decode_e4m3(c.v[i].cpu().numpy()) == wr).all()
+        normal = np.abs(wm) > 2.0 ** -6
+        got = R.decode_e4m3(c.m[i].cpu().numpy())
+        assert (got == wm)[normal].all() and (got != wm).sum() <= 1
+
+
 def test_more_tensors_than_a_launch_holds():
     for bits in (32, 8):
         c = Case([100 + i for i in range(130)], "bf16", "f32", bits, True, 0, seed=9)

@@ -89,7 +89,7 @@ def test_binding_refuses_lists():
         (dict(g=[f32(5)]), "elements"), (dict(g=[f32(), f32()]), "grads for"), (dict(m=[f32(3)]), "elements"),
         (dict(p=[torch.zeros(4, 4).t()], g=[f32(16)], m=[f32(16)], v=[f32(16)]), "contiguous"),
         (dict(p=[torch.zeros(4, dtype=torch.int32)]), "params must be"), (dict(g=[torch.zeros(4, dtype=torch.uint8)]), "grads must be"),
-        (dict(m=[torch.zeros(4, dtype=torch.bfloat16)]), "float32, or codes"), (dict(masters=[]), "one entry per"),
+        (dict(m=[torch.zeros(4, dtype=torch.bfloat16)]), "states must be float32"), (dict(masters=[]), "one entry per"),
         (dict(masters=[torch.zeros(4, dtype=torch.float16)]), "masters must be float32"), (dict(masters=[f32(5)]), "elements"),
         (dict(exp_avg_scales=[f32(1)]), "8-bit states"), (dict(exp_avg_scales=[f32(1)], exp_avg_sq_scales=[f32(1)]), "1-byte"),
         (dict(m=[torch.zeros(4, dtype=torch.uint8)], v=[torch.zeros(4, dtype=torch.uint8)], exp_avg_scales=[f32(2)],
@@ -115,3 +115,76 @@ def test_reference_grid_and_numbers():
     assert (f == 0).all() and (k * step == R.decode_e4m3(codes)).all()
     for u in R.uniforms(1 << 16, 3, 4, 5):
         assert abs(u.mean() - 0.5) < 5 * 0.289 / 256 and abs((u < 0.25).mean() - 0.25) < 5 * 0.433 / 256
+
+
+# ------------------------------------------------------------------ cross entropy
+def xent_args(**kw):
+    a = dict(a=FAKE, lda=64, b=FAKE, ldb=64, M=8, N=100, K=64, sa=FAKE, sb=FAKE, rows=0, t=FAKE, bits=64, loss=FAKE, lse=FAKE,
+             mean=FAKE, ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return a
+
+
+COMMON = [
+    (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(K=24, lda=32, ldb=32), UNSUP),
+    (dict(K=65552, lda=65552, ldb=65552), UNSUP), (dict(M=(1 << 20) + 1), UNSUP), (dict(M=1 << 20, K=1024, lda=1024, ldb=1024), UNSUP),
+    (dict(N=1 << 31), UNSUP), (dict(bits=16), ENUM), (dict(a=None), NULL), (dict(b=None), NULL), (dict(t=None), NULL),
+    (dict(lda=48), SHAPE), (dict(ldb=48), SHAPE), (dict(lda=72), UNSUP), (dict(ldb=72), UNSUP), (dict(lda=(1 << 24) + 16), UNSUP),
+    (dict(a=FAKE + 8), UNSUP), (dict(b=FAKE + 8), UNSUP), (dict(t=FAKE + 4), ARG), (dict(bits=32, t=FAKE + 2), ARG),
+    (dict(sa=FAKE + 2), ARG), (dict(sb=FAKE + 1), ARG), (dict(ws=None), NULL), (dict(wsb=100), ARG), (dict(ws=FAKE + 8), ARG),
+]
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(rows=4), ENUM), (dict(rows=-1), ENUM), (dict(rows=1, sa=None), NULL), (dict(rows=2, sb=None), NULL),
+    (dict(loss=None), NULL), (dict(lse=None), NULL), (dict(loss=FAKE + 2), ARG), (dict(lse=FAKE + 2), ARG), (dict(mean=FAKE + 2), ARG),
+])
+def test_cross_entropy_rejects(L, kw, status):
+    assert L.fp8_cross_entropy(*xent_args(**kw).values(), None) == status
+    assert L.fp8mi_last_error()
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(lse=None), NULL), (dict(dloss=None), NULL), (dict(dloss=FAKE + 2), ARG), (dict(lse=FAKE + 1), ARG), (dict(drows=2), ENUM),
+    (dict(ld_da=63), SHAPE), (dict(ld_db=63), SHAPE), (dict(da=FAKE + 1), ARG), (dict(db=FAKE + 1), ARG),
+])
+def test_cross_entropy_grad_rejects(L, kw, status):
+    a = xent_args(dloss=FAKE, drows=0, da=FAKE, ld_da=64, db=FAKE, ld_db=64)
+    a.update(kw)
+    order = ("a", "lda", "b", "ldb", "M", "N", "K", "sa", "sb", "t", "bits", "lse", "dloss", "drows", "da", "ld_da", "db", "ld_db",
+             "ws", "wsb")
+    assert L.fp8_cross_entropy_grad(*[a[k] for k in order], None) == status
+
+
+def test_cross_entropy_workspaces(L):
+    """Pure host functions: 0 where nothing runs, bounded by what they hold."""
+    for f in (L.fp8_cross_entropy_workspace_bytes, L.fp8_cross_entropy_grad_workspace_bytes):
+        assert f(0, 100, 64) == 0 and f(-1, 100, 64) == 0 and f(8, 0, 64) == 0 and f(8, 100, 24) == 0
+        assert 0 < f(1, 1, 16) < 1 << 20
+        for M, N, K in ((1, 32768, 1536), (4096, 65536, 1536), (8192, 131072, 4096), (100000, 1000, 64)):
+            assert f(M, N, K) < 3 << 30
+    assert L.fp8_cross_entropy_workspace_bytes(1, 32768, 1536) < 1 << 20  # a token's score needs no 16-bit operands
+
+
+def test_binding_refuses_cross_entropy():
+    a, b, t = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(9, 32, dtype=torch.uint8), torch.zeros(4, dtype=torch.int64)
+    one = torch.ones(1)
+    for args, kw, text in [
+        ((a.float(), b, t), {}, "1-byte"), ((a, b[:, :16], t), {}, "K mismatch"), ((a, b, t[:3]), {}, "targets must be"),
+        ((a, b, t.float()), {}, "targets must be"), ((a, b, t), dict(a_scale_inv=torch.ones(3)), "a_scale_inv"),
+        ((a, b, t), dict(b_scale_inv=torch.ones(4)), "b_scale_inv"), ((a, b, t), dict(loss=torch.zeros(3)), "loss must be"),
+        ((a, b, t), dict(lse=torch.zeros(4, dtype=torch.float64)), "lse must be"), ((a, b, t), dict(mean_out=one), "mean_out"),
+        ((a.t(), b, t), {}, "unit column stride"),
+    ]:
+        with pytest.raises(ValueError, match=text):
+            fp8mi.fp8_cross_entropy(*args, **kw)
+    lse = torch.zeros(4)
+    for kw, text in [
+        (dict(a_scale_inv=torch.ones(4)), "no row scales"), (dict(b_scale_inv=torch.ones(9)), "no row scales"),
+        (dict(da=torch.zeros(4, 32)), "da must be"), (dict(db=torch.zeros(9, 16, dtype=torch.bfloat16)), "db has shape"),
+        (dict(dloss=torch.ones(3)), "dloss must be"), (dict(lse=torch.zeros(5)), "lse must be"),
+    ]:
+        args = dict(lse=lse, dloss=one)
+        args.update(kw)
+        with pytest.raises(ValueError, match=text):
+            fp8mi.fp8_cross_entropy_grad(a, b, t, **args)

@@ -79,6 +79,34 @@ def grid(y):
     return k, y / step - k, step
 
 
+def adamw8_fp32(codes_m, scales_m, codes_v, scales_v, g, seed, step, tensor, b1, b2, c=None):
+    """The new codes and scales of an 8-bit step, operation by operation in IEEE
+    fp32: (codes of |m| with its sign, scales, codes of sqrt(v), scales)."""
+    f = np.float32
+    n = len(g)
+    ms, vs = (np.repeat(x.astype(f), 256)[:n] for x in (scales_m, scales_v))
+    g = g.astype(f) if c is None else g.astype(f) * f(c)
+    m = f(b1) * (decode_e4m3(codes_m).astype(f) * ms) + f(1 - b1) * g
+    q = decode_e4m3(codes_v).astype(f) * vs
+    r = np.sqrt(f(b2) * (q * q) + f(1 - b2) * g * g)
+    out = []
+    for x, u, root in ((m, uniforms(n, seed, step, tensor)[0].astype(f), False),
+                       (r, uniforms(n, seed, step, tensor)[1].astype(f), True)):
+        pad = np.zeros(-(-n // 256) * 256, f)
+        pad[:n] = np.abs(x)
+        s = pad.reshape(-1, 256).max(1) * (f(1) / f(448))
+        s = np.where(s < f(2.0 ** -100), f(0), s)
+        per = np.repeat(s, 256)[:n]
+        y = np.minimum(np.abs(x) / np.where(per > 0, per, f(np.inf)), f(448))
+        e = np.maximum(np.frexp(y)[1] - 1, -6)
+        unit = np.exp2((e - 3).astype(f))
+        k = np.floor(y / unit)
+        t = y / unit - k
+        up = (u * (2 * k + 1) < t * (2 * k + t)) | ((k == 0) & (t > 0)) if root else u < t
+        out += [np.copysign((k + up) * unit, x), s]
+    return out
+
+
 # ------------------------------------------------------------------ cross entropy
 def logits(a_codes, b_codes, sa, sb):
     a, b = decode_e4m3(a_codes) * np.reshape(sa, (-1, 1)), decode_e4m3(b_codes) * np.reshape(sb, (-1, 1))
