@@ -661,8 +661,8 @@ static fp8mi_status check_xent(const XentCall& c, int target_bits, const void* w
   if (!c.a || !c.b || !c.targets) return fail(FP8MI_ERR_NULL, "a, b or targets is NULL");
   if (c.lda < c.K || c.ldb < c.K)
     return fail(FP8MI_ERR_SHAPE, "lda %lld / ldb %lld < K %lld", (long long)c.lda, (long long)c.ldb, (long long)c.K);
-  if (c.lda > (1 << 24) || c.ldb > (1 << 24))
-    return fail(FP8MI_ERR_UNSUPPORTED, "lda %lld / ldb %lld above 2^24", (long long)c.lda, (long long)c.ldb);
+  if (c.lda > (1 << 22) || c.ldb > (1 << 22))
+    return fail(FP8MI_ERR_UNSUPPORTED, "lda %lld / ldb %lld above 2^22", (long long)c.lda, (long long)c.ldb);
   if ((c.lda % 16) || (c.ldb % 16) || (reinterpret_cast<uintptr_t>(c.a) & 15u) || (reinterpret_cast<uintptr_t>(c.b) & 15u))
     return fail(FP8MI_ERR_UNSUPPORTED, "a and b must be 16-byte aligned, lda and ldb multiples of 16");
   if (reinterpret_cast<uintptr_t>(c.targets) % (target_bits / 8)) return fail(FP8MI_ERR_ARG, "targets not aligned to their size");

@@ -5,35 +5,38 @@
 //   loss_i = lse_i - l_{i, t_i}
 //   G_ij = d_i (exp(l_ij - lse_i) - [j = t_i])   dA = sb G B   dB = sa G^T A
 //
-// The vocabulary is taken in pieces.  Forward: a piece's codes become fp16 (their
-// exact values) in the workspace, and the product's epilogue (xent_mm.h) leaves
-// each row's largest logit and sum of exponentials per tile of columns; one more
-// kernel joins them.  Backward: the piece's logits once more, G / d in fp16, then
-// G B into fp32 sums and G^T A straight to its rows of dB.  So 2 M N K flop forward
-// and 6 M N K backward, at 16 bits' rate; what is written besides is M times a
-// piece's columns.
+// The products are fp16's: A's codes become fp16 (their exact values) in the
+// workspace, B's as a tile's fragments are read from LDS (v_cvt_scalef32 beside the
+// MFMAs: 4096 x 65536 x 1536 658 -> 683 us, where writing them out first took 55, and
+// 333 x 50001 x 1536 76 -> 79 against 37).  Forward: the product's epilogue
+// (xent_mm.h) leaves each row's largest logit and sum of exponentials per tile of
+// columns, and one more kernel joins them.  Backward, the vocabulary in pieces: the
+// piece's logits once more, G / d in fp16, then G B into fp32 sums and G^T A straight
+// to its rows of dB.  So 2 M N K flop forward and 6 M N K backward, at 16 bits' rate;
+// what is written besides is M times a piece's columns.
 #include "xent_mm.h"
 
 namespace fp8mi {
 
 namespace {
 
-constexpr int64_t kPieceElements = (int64_t)128 << 20;  // of a piece's weights or of G: 256 MiB in fp16
+constexpr int64_t kPieceElements = (int64_t)128 << 20;  // of G: 256 MiB
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // Leading dimension of n fp16 values: rows whose distance is a multiple of 1 KiB
-// fall on few of the memory's channels, so such rows get 128 bytes more
-// (4096 x 1536 x 16384, G B with rows 32 KiB apart: MEASURE).
+// fall on few of the memory's channels, so such rows get 128 bytes more (4096 x 1536
+// x 16384, G B with rows 32 KiB apart: 261 -> 237 us).
 int64_t padded(int64_t n) { return n % 512 == 0 ? n + 64 : n; }
 
-// Columns of a piece, a multiple of 256: so many that neither the piece's weights
-// nor (with rows) its G are above kPieceElements, in pieces of about one size.
-int64_t piece_columns(int64_t N, int64_t K, int64_t rows) {
-  const int64_t most = kPieceElements / (K > rows ? K : rows);
-  const int64_t p = most < 256 ? 256 : (most > (1 << 20) ? 1 << 20 : most / 256 * 256);
-  return up((N + (N + p - 1) / p - 1) / ((N + p - 1) / p), 256);
+// Columns of a piece, a multiple of 256: at most `most`, in pieces of about one size.
+int64_t even_pieces(int64_t N, int64_t most) {
+  most = most < 256 ? 256 : (most > (1 << 20) ? 1 << 20 : most / 256 * 256);
+  const int64_t pieces = (N + most - 1) / most;
+  return up((N + pieces - 1) / pieces, 256);
 }
+// So many that a piece's codes stay within a buffer's 32-bit offsets (ldb <= 2^22).
+int64_t offset_columns(int64_t ldb) { return (INT64_C(1) << 30) / ldb; }
 
 struct Carve {
   int64_t at = 0;
@@ -57,33 +60,27 @@ int64_t rows_tile(int64_t N) { return N >= 8192 ? 32 : 16; }
 int join_rows(int64_t M) { return M >= 128 ? 16 : (M >= 16 ? 4 : 1); }
 
 struct ForwardPlan {
-  int64_t cols, ld, tile, ticket, slots, parts, logit, a16, b16, bytes;
+  int64_t ld, tile, ticket, slots, parts, logit, a16, bytes;
   bool rows;
   ForwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
     rows = few_rows(M, N);
-    cols = rows ? N : piece_columns(N, K, 0);
     ld = padded(K);
     tile = rows ? rows_tile(N) : xent_lse_tile(M, N);
     ticket = c.take(4);
     slots = c.take((M + join_rows(M) - 1) / join_rows(M) * 16);
-    parts = c.take((N + cols - 1) / cols * ((cols + tile - 1) / tile) * M * 8);
+    parts = c.take((N + tile - 1) / tile * M * 8);
     logit = c.take(M * 4);
-    if (rows) {
-      bytes = c.at;
-      return;
-    }
-    a16 = c.take(M * ld * 2);
-    b16 = c.take(cols * ld * 2);
+    a16 = c.take(rows ? 0 : M * ld * 2);
     bytes = c.at;
   }
 };
 
 struct BackwardPlan {
-  int64_t cols, splits, ld, ld_g, scale, a16, a16d, b16, g, sums, bytes;
+  int64_t cols, splits, ld, ld_g, scale, a16, a16d, g, sums, bytes;
   BackwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
-    cols = piece_columns(N, K, M);
+    cols = even_pieces(N, kPieceElements / M);
     // K splits of G B: about a tile for each of 256 CUs, steps of at least 512 columns
     const int64_t tiles = (M + 255) / 256 * ((K + 191) / 192);
     splits = 256 / tiles;
@@ -94,21 +91,19 @@ struct BackwardPlan {
     scale = c.take(4);
     a16 = c.take(M * ld * 2);
     a16d = c.take(M * ld * 2);
-    b16 = c.take(cols * ld * 2);
     g = c.take(M * ld_g * 2);
     sums = c.take(splits * M * K * 4);
     bytes = c.at;
   }
 };
 
-// Codes [R, C] of up to two matrices (A, and the first piece of B) as fp16, 32 codes
-// to a thread: C % 16 == 0, whole 16-byte chunks.  Bound by HBM: 3 bytes per code.
+// Codes [R, C] as fp16, 32 codes to a thread: C % 16 == 0, whole 16-byte chunks.
 // With targets, the rows of ignored ones are zeros (a NaN among their codes would
 // reach dB as 0 * NaN); with row factors, out_scaled receives each row times its own.
 struct Widen {
   const uint8_t* x;
   uint16_t* out;
-  int64_t ld, ld_out, chunks;  // chunks of 16 codes, in all
+  int64_t ld, ld_out, chunks;  // of 16 codes, in all
   int32_t row_chunks;
   int target_bits;
   const void* targets;
@@ -116,12 +111,9 @@ struct Widen {
   const float* rows_by;
   uint16_t* out_scaled;
 };
-__device__ __forceinline__ void widen_group(const Widen& a, const Widen& b, int64_t group) {
+__device__ __forceinline__ void widen_group(const Widen& m, int64_t group) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const int64_t groups_a = (a.chunks + 511) / 512;
-  const bool first = group < groups_a;
-  const Widen& m = first ? a : b;
-  const int64_t at = (group - (first ? 0 : groups_a)) * 512 + threadIdx.x;
+  const int64_t at = group * 512 + threadIdx.x;
   u32x4 v[2];
   int64_t out[2], row[2];
 #pragma unroll
@@ -163,17 +155,17 @@ __device__ __forceinline__ void widen_group(const Widen& a, const Widen& b, int6
   }
 }
 
-__global__ void __launch_bounds__(256) widen_codes(Widen a, Widen b, uint32_t* ticket) {
-  if (ticket && threadIdx.x + blockIdx.x == 0) *ticket = 0u;  // for the join, launches on
-  widen_group(a, b, blockIdx.x);
+__global__ void __launch_bounds__(256) widen_codes(Widen a, uint32_t* ticket) {
+  if (ticket && threadIdx.x + blockIdx.x == 0) *ticket = 0u;  // for the join, two launches on
+  widen_group(a, blockIdx.x);
 }
-int64_t widen_groups(const Widen& a, const Widen& b) { return (a.chunks + 511) / 512 + (b.chunks + 511) / 512; }
+int64_t widen_groups(const Widen& a) { return (a.chunks + 511) / 512; }
 
 Widen widen(const uint8_t* x, int64_t ld, int64_t R, int64_t C, uint16_t* out, int64_t ld_out) {
   return {x, out, ld, ld_out, R * (C / 16), (int32_t)(C / 16), 0, nullptr, nullptr, nullptr, nullptr};
 }
-hipError_t launch_widen(const Widen& a, const Widen& b, uint32_t* ticket, hipStream_t st) {
-  hipLaunchKernelGGL(widen_codes, dim3((unsigned)widen_groups(a, b)), dim3(256), 0, st, a, b, ticket);
+hipError_t launch_widen(const Widen& a, uint32_t* ticket, hipStream_t st) {
+  hipLaunchKernelGGL(widen_codes, dim3((unsigned)widen_groups(a)), dim3(256), 0, st, a, ticket);
   return hipGetLastError();
 }
 
@@ -202,9 +194,9 @@ __global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const vo
 // alike, so that a load instruction reads 64 contiguous bytes of a row.  The
 // waves' sums meet in LDS, and wave i finishes strip i.  (1 x 32768 x 1536, widened
 // and in 128 x 128 tiles: 60 us; this: MEASURE.)
-struct RowsGrad {  // what the gradient's form does besides: the operands' 16-bit forms, for the products after it
+struct RowsGrad {  // what the gradient's form does besides: A in fp16, for the products after it
   static constexpr bool kGrad = true;
-  Widen a, b;
+  Widen a;
 };
 struct RowsStats {
   static constexpr bool kGrad = false;
@@ -214,7 +206,7 @@ template <int TI, int TJ, class G>
 __global__ void __launch_bounds__(256) xent_rows(XentArgs p, G extra, uint32_t col_blocks, uint32_t blocks) {
   if constexpr (G::kGrad) {
     if (blockIdx.x >= blocks) {
-      widen_group(extra.a, extra.b, blockIdx.x - blocks);
+      widen_group(extra.a, blockIdx.x - blocks);
       return;
     }
   }
@@ -505,16 +497,21 @@ __global__ void __launch_bounds__(256) zero_rows(uint16_t* p, int64_t rows, int6
     if (e != hipSuccess) return e;       \
   } while (0)
 
-void fill_logits(XentArgs& p, const XentCall& c, const uint16_t* a16, const uint16_t* b16, int64_t ld,
-                 int64_t v0, int64_t n) {
+// The logits of columns v0 .. v0 + n - 1, A's codes in fp16 at a16.
+void fill_logits(XentArgs& p, const XentCall& c, const uint16_t* a16, int64_t ld, int64_t v0, int64_t n) {
   p.a = reinterpret_cast<const uint8_t*>(a16);
-  p.b = reinterpret_cast<const uint8_t*>(b16);
-  p.lda = p.ldb = 2 * ld;
+  p.b = c.b + v0 * c.ldb;
+  p.lda = 2 * ld; p.ldb = c.ldb;
   p.K = p.k_total = 2 * c.K;
   p.M = c.M; p.N = n; p.batch = 1;
   p.a_scale_inv = c.a_scale_inv; p.b_scale_inv = c.b_scale_inv && c.b_rows ? c.b_scale_inv + v0 : c.b_scale_inv;
   p.a_rows = c.a_rows; p.b_rows = c.b_rows;
   p.targets = c.targets; p.target_bits = c.target_bits; p.v0 = v0; p.vocab = c.N;
+}
+// The same from A's codes (xent_rows).
+void fill_rows(XentArgs& p, const XentCall& c, int64_t v0, int64_t n) {
+  fill_logits(p, c, nullptr, 0, v0, n);
+  p.a = c.a; p.lda = c.lda; p.K = c.K;
 }
 
 }  // namespace
@@ -546,26 +543,21 @@ hipError_t launch_xent_forward(const XentCall& c, hipStream_t st) {
   uint32_t* const ticket = reinterpret_cast<uint32_t*>(c.ws + plan.ticket);
   float2* const parts = reinterpret_cast<float2*>(c.ws + plan.parts);
   float* const logit = reinterpret_cast<float*>(c.ws + plan.logit);
-  int64_t tiles = 0;
+  const int64_t tiles = (c.N + plan.tile - 1) / plan.tile;
   if (plan.rows) {
     XentArgs p;
-    fill_logits(p, c, nullptr, nullptr, 0, 0, c.N);
-    p.a = c.a; p.b = c.b; p.lda = c.lda; p.ldb = c.ldb; p.K = c.K;
+    fill_rows(p, c, 0, c.N);
     p.parts = parts;
     p.target_logit = logit;
-    tiles = (c.N + plan.tile - 1) / plan.tile;
     FP8MI_TRY(launch_rows(p, RowsStats{ticket}, 0, st));
   } else {
     uint16_t* const a16 = reinterpret_cast<uint16_t*>(c.ws + plan.a16);
-    uint16_t* const b16 = reinterpret_cast<uint16_t*>(c.ws + plan.b16);
-    for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
-      const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-      FP8MI_TRY(launch_widen(widen(c.a, c.lda, v0 == 0 ? c.M : 0, c.K, a16, plan.ld),
-                             widen(c.b + v0 * c.ldb, c.ldb, n, c.K, b16, plan.ld), v0 == 0 ? ticket : nullptr, st));
+    FP8MI_TRY(launch_widen(widen(c.a, c.lda, c.M, c.K, a16, plan.ld), ticket, st));
+    const int64_t cols = even_pieces(c.N, offset_columns(c.ldb));  // a multiple of every tile's
+    for (int64_t v0 = 0; v0 < c.N; v0 += cols) {
       XentLseArgs p;
-      fill_logits(p, c, a16, b16, plan.ld, v0, n);
-      p.tile0 = tiles;
-      tiles += (n + plan.tile - 1) / plan.tile;
+      fill_logits(p, c, a16, plan.ld, v0, c.N - v0 < cols ? c.N - v0 : cols);
+      p.tile0 = v0 / plan.tile;
       p.parts = parts;
       p.target_logit = logit;
       FP8MI_TRY(launch_xent_lse(p, st));
@@ -597,47 +589,48 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
     hipLaunchKernelGGL(dloss_scale, dim3(1), dim3(1024), 0, st, c.dloss, c.targets, c.target_bits, c.M, scale);
     FP8MI_TRY(hipGetLastError());
   }
+  Widen rows = widen(c.a, c.lda, c.M, c.K, at(plan.a16), plan.ld);
+  rows.targets = c.targets;
+  rows.target_bits = c.target_bits;
+  if (scaled) {
+    rows.rows = c.dloss;
+    rows.rows_by = scale;
+    rows.out_scaled = at(plan.a16d);
+  }
+  const int64_t most = offset_columns(c.ldb), cols = plan.cols <= most ? plan.cols : even_pieces(c.N, most);
   // bytes of G's rows per K split, from the first piece (no later one is wider):
   // whole 128-byte steps, so that every split starts on a chunk
-  const int64_t first_cols = up(c.N < plan.cols ? c.N : plan.cols, 8);
+  const int64_t first_cols = up(c.N < cols ? c.N : cols, 8);
   const int64_t k_split = up((2 * first_cols + plan.splits - 1) / plan.splits, 128);
   const int64_t splits = (2 * first_cols + k_split - 1) / k_split;
-  for (int64_t v0 = 0; v0 < c.N; v0 += plan.cols) {
-    const int64_t n = c.N - v0 < plan.cols ? c.N - v0 : plan.cols;
-    Widen rows = widen(c.a, c.lda, v0 == 0 ? c.M : 0, c.K, at(plan.a16), plan.ld);
-    rows.targets = c.targets;
-    rows.target_bits = c.target_bits;
-    if (scaled) {
-      rows.rows = c.dloss;
-      rows.rows_by = scale;
-      rows.out_scaled = at(plan.a16d);
-    }
-    const Widen weights = widen(c.b + v0 * c.ldb, c.ldb, n, c.K, at(plan.b16), plan.ld);
+  for (int64_t v0 = 0; v0 < c.N; v0 += cols) {
+    const int64_t n = c.N - v0 < cols ? c.N - v0 : cols;
     XentGradArgs g;
-    fill_logits(g, c, at(plan.a16), at(plan.b16), plan.ld, v0, n);
     g.lse = c.lse;
     g.d = at(plan.g); g.ld_d = plan.ld_g;
-    if (few_rows(c.M, n)) {  // the logits straight from the codes, beside the widening
-      g.a = c.a; g.b = c.b + v0 * c.ldb; g.lda = c.lda; g.ldb = c.ldb; g.K = c.K;
-      FP8MI_TRY(launch_rows(g, RowsGrad{rows, weights}, widen_groups(rows, weights), st));
+    if (few_rows(c.M, n)) {  // the logits straight from the codes, beside the widening of A
+      if (v0 > 0) rows.chunks = 0;
+      fill_rows(g, c, v0, n);
+      FP8MI_TRY(launch_rows(g, RowsGrad{rows}, widen_groups(rows), st));
     } else {
-      FP8MI_TRY(launch_widen(rows, weights, nullptr, st));
+      if (v0 == 0) FP8MI_TRY(launch_widen(rows, nullptr, st));
+      fill_logits(g, c, at(plan.a16), plan.ld, v0, n);
       FP8MI_TRY(launch_xent_grad(g, st));
     }
-    AddArgs add;  // G by rows, the piece's weights K-major
+    AddArgs add;  // G by rows, the piece's codes K-major
     add.a = reinterpret_cast<const uint8_t*>(at(plan.g));
-    add.b = reinterpret_cast<const uint8_t*>(at(plan.b16));
-    add.lda = 2 * plan.ld_g; add.ldb = 2 * plan.ld;
+    add.b = c.b + v0 * c.ldb;
+    add.lda = 2 * plan.ld_g; add.ldb = c.ldb;
     add.M = c.M; add.N = c.K;
     add.k_total = 2 * up(n, 8);
     add.k_major_rows = n;
     add.K = k_split;
     add.batch = (add.k_total + k_split - 1) / k_split;
     add.stride_a = k_split;
-    add.stride_b = k_split / 2 * add.ldb;
+    add.stride_b = k_split / 2 * c.ldb;
     add.sums = sums;
     add.first = v0 == 0;
-    Mm16Args km;  // both K-major
+    KmArgs km;  // both K-major
     km.a = reinterpret_cast<const uint8_t*>(at(plan.g));
     km.b = reinterpret_cast<const uint8_t*>(at(scaled ? plan.a16d : plan.a16));
     km.lda = 2 * plan.ld_g; km.ldb = 2 * plan.ld;

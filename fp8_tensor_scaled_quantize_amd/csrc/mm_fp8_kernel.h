@@ -117,11 +117,13 @@ __device__ __forceinline__ float load_bias(const MmArgs& p, int64_t j, float bsc
 // Operands of 16 bits (fp16), for products whose sums fp8's in-group truncation
 // (below) would spoil: the same tile in bytes, a step of 128 bytes being 64 k,
 // with leading dimensions, K and strides in bytes too.
-constexpr int kOpF16 = 8;
+// B may be E4M3 codes beside an fp16 A (kOpCodes): its tile rows are 64 bytes, and a
+// fragment's 16 codes become fp16 as they are read from LDS.
+constexpr int kOpF16 = 8, kOpCodes = 9;
 template <int W> struct Width {
   static constexpr int value = W;
 };
-template <int F> constexpr int kOpBytes = F == kOpF16 ? 2 : 1;
+template <int F> constexpr int kOpBytes = F >= kOpF16 ? 2 : 1;  // of the values that the product sees
 
 // K-major tiles of 16-bit operands: 64 k-rows of 2 W bytes.  A fragment's 16
 // columns are 32 contiguous bytes, so 32-byte granules are rotated: a half-wave of
@@ -163,6 +165,43 @@ __device__ __forceinline__ v4f mfma_f16(const v8i& bfrag, const v8i& afrag, v4f 
   return c;
 }
 
+// Tiles of codes beside fp16 ones: the 16-byte chunk c of a 64-byte row r sits at
+// position c ^ ((r >> 2) & 3), which puts the 16 rows that one lane group reads on the
+// 16 chunks of the 64 banks.
+__device__ __forceinline__ v8i lds_frag_codes(const uint8_t* S, int row, int g) {
+  const uint4 c = *reinterpret_cast<const uint4*>(S + row * 64 + ((g ^ ((row >> 2) & 3)) << 4));
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  v8i r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    r[2 * e] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[e], 1.0f, false));
+    r[2 * e + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[e], 1.0f, true));
+  }
+  return r;
+}
+
+// The same from a K-major tile of codes, 64 k-rows of W bytes: chunks rotated as in
+// km_pos, by bit 4 of the k-row in bit 5's place (a lane group takes 16 k here).
+template <int CPR> __device__ __forceinline__ int km_codes_pos(int c, int kr) {
+  return (c + (kr & 7) + (((kr >> 4) & 1) << 3)) % CPR;
+}
+template <int W> __device__ __forceinline__ v8i lds_frag_km_codes(const uint8_t* S, int rb, int lane) {
+  const int g = lane >> 4, a = lane & 15, j = a >> 1, h = a & 1;
+  v8i r;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int kr = 16 * g + 8 * q + j;
+    const v2i d = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        (lds_v2i_ptr)(S + kr * W + km_codes_pos<W / 16>(rb >> 4, kr) * 16 + 8 * h));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      r[4 * q + 2 * e] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)d[e], 1.0f, false));
+      r[4 * q + 2 * e + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)d[e], 1.0f, true));
+    }
+  }
+  return r;
+}
+
 template <int FA, int FB>
 __device__ __forceinline__ v4f mfma_nt(const v8i& bfrag, const v8i& afrag, const v4f& c) {
   // first operand: B rows (format FB -> cbsz), second: A rows (format FA -> blgp).
@@ -199,7 +238,7 @@ __device__ __forceinline__ v8i spread_dword(const v8i& f, int s) {
 
 template <int FA, int FB, bool PREC>
 __device__ __forceinline__ v4f mma(const v8i& bfrag, const v8i& afrag, v4f c) {
-  if constexpr (FA == kOpF16) {
+  if constexpr (FA >= kOpF16) {
     return mfma_f16(bfrag, afrag, c);
   } else if constexpr (!PREC) {
     return mfma_nt<FA, FB>(bfrag, afrag, c);
@@ -352,7 +391,9 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
                                         uint8_t* pool) {
   constexpr bool KMA = (LAY & 1) != 0, KMB = (LAY & 2) != 0;
   constexpr int EB = kOpBytes<FA>;  // bytes per operand element
-  static_assert(FA == FB || EB == kOpBytes<FB>, "operands of one width");
+  constexpr bool BC = FB == kOpCodes;
+  static_assert(EB == kOpBytes<FB>, "operands of one width");
+  static_assert(!BC || FA == kOpF16, "codes as B stand beside fp16");
   constexpr int NWAVES = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   constexpr int TI = WM / 16, TJ = WN / 16;
@@ -364,8 +405,9 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   // box: 4096^3 56.0 -> 55.0 us, 8192^3 420 -> 403 us).
   constexpr int NLW = (BM * BN >= 256 * 192) ? NWAVES / 2 : NWAVES;
   constexpr int LA = BM / 8 / NLW;            // 1 KiB load instructions per loading wave for A
-  constexpr int LB = BN / 8 / NLW;            // ... and for B
-  static_assert(LA >= 1 && LB >= 1 && LA * 8 * NLW == BM && LB * 8 * NLW == BN, "tile / wave mismatch");
+  constexpr int BR = BC ? 16 : 8;             // B rows per load instruction
+  constexpr int LB = BN / BR / NLW;           // ... and for B
+  static_assert(LA >= 1 && LB >= 1 && LA * 8 * NLW == BM && LB * BR * NLW == BN, "tile / wave mismatch");
   static_assert(TI >= 1 && TJ >= 1, "wave tile below one MFMA tile");
   constexpr int CROW = BN + 8;                // bf16 per LDS row of the staged C tile (16 B pad)
   // LDS stages: two for the big tiles (2 x 64 KiB at 256 x 256); the small
@@ -386,16 +428,22 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
   int ext_b = (int)(KMB ? p.b_extent_km(n0) : p.b_extent_from(n0));
   if constexpr (EB == 2) {  // a K-major operand of 16 bits: whole rows of this batch's k
     if constexpr (KMA) ext_a = (int)(P::k_rows(p, bz) * p.lda - 2 * m0);
-    if constexpr (KMB) ext_b = (int)(P::k_rows(p, bz) * p.ldb - 2 * n0);
+    if constexpr (KMB && !BC) ext_b = (int)(P::k_rows(p, bz) * p.ldb - 2 * n0);
+    // codes are the caller's: their last row ends with its columns
+    if constexpr (KMB && BC) ext_b = (int)((P::k_rows(p, bz) - 1) * p.ldb + p.N - n0);
+    if constexpr (!KMB && BC) ext_b = (int)((p.N - 1 - n0) * p.ldb + p.K / 2);
   }
   const v4i rsa = buffer_rsrc(p.a + bz * p.stride_a + (KMA ? EB * m0 : m0 * p.lda), ext_a);
-  const v4i rsb = buffer_rsrc(p.b + bz * p.stride_b + (KMB ? EB * n0 : n0 * p.ldb), ext_b);
+  const v4i rsb = buffer_rsrc(p.b + bz * p.stride_b + (KMB ? (BC ? 1 : EB) * n0 : n0 * p.ldb), ext_b);
   // Lane l of a 1 KiB load fills LDS row r0 + l/8 (r0 a multiple of 8) at
   // chunk position l%8, so it fetches logical chunk (l%8) ^ swz(l/8).
   const int lr = lane >> 3, lc = (lane & 7) ^ swz(lr);
   // unsigned: offsets of rows past the edge may wrap; those rows' outputs are never stored
   const uint32_t lda = (uint32_t)p.lda, ldb = (uint32_t)p.ldb;
   const uint32_t va = lr * lda + 16 * lc, vb = lr * ldb + 16 * lc;
+  // codes beside fp16: lane l fills position l%4 of row r0 + l/4 (r0 a multiple of 16)
+  const int cc = (lane & 3) ^ (lane >> 4);
+  const uint32_t vc = (uint32_t)(lane >> 2) * ldb + 16 * cc;
   const int K = (int)P::k_bytes(p, bz);
   // K-major operands: load instruction ii fills LDS chunks 64 ii .. 64 ii + 63
   // of the stage; lane l's chunk q = 64 ii + l is position q % CPR of k-row
@@ -412,6 +460,13 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     const int rot = ((kr & 3) + (((kr >> 4) & 1) << 2)) % G;
     const uint32_t c = (uint32_t)((pos + G - rot) % G);
     return k0 / 2 + kr >= k_rows ? (uint32_t)ext : (uint32_t)kr * ld + 32 * c + 16 * (qq & 1);
+  };
+
+  auto km_codes_offset = [&](int qq, int k0) -> uint32_t {
+    constexpr int CPR = BN / 16;
+    const int kr = qq / CPR, pos = qq % CPR;
+    const uint32_t c = (uint32_t)((pos + CPR - km_codes_pos<CPR>(0, kr)) % CPR);
+    return k0 / 2 + kr >= k_rows ? (uint32_t)ext_b : (uint32_t)kr * ldb + 16 * c;
   };
 
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
@@ -470,7 +525,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
         }
       }
       if (q < LB) {
-        if constexpr (KMB && EB == 2) {
+        if constexpr (KMB && BC) {
+          dma16(rsb, bs + (wid * LB + q) * 1024, (int)km_codes_offset((wid * LB + q) * 64 + lane, k0),
+                (int)((uint32_t)(k0 / 2) * ldb));
+        } else if constexpr (KMB && EB == 2) {
           dma16(rsb, bs + (wid * LB + q) * 1024, (int)km16_offset(Width<BN>{}, (wid * LB + q) * 64 + lane, k0, ldb, ext_b),
                 (int)((uint32_t)(k0 / 2) * ldb));
         } else if constexpr (KMB) {
@@ -480,6 +538,9 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
           const uint32_t c = (uint32_t)((pos + CPR_B - rot) % CPR_B);  // inverse of km_pos
           dma16(rsb, bs + (wid * LB + q) * 1024, k0 + kr >= K ? ext_b : (int)((uint32_t)kr * ldb + 16 * c),
                 (int)((uint32_t)k0 * ldb));
+        } else if constexpr (BC) {
+          const int r0 = (wid * LB + q) * 16;
+          dma16(rsb, bs + r0 * 64, k0 / 2 + 16 * cc >= K / 2 ? ext_b : (int)(vc + (uint32_t)r0 * ldb), k0 / 2);
         } else {
           const int r0 = (wid * LB + q) * 8;
           dma16(rsb, bs + r0 * kBK, past ? ext_b : (int)(vb + (uint32_t)r0 * ldb), k0);
@@ -515,7 +576,10 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
         }
       } else {
         const int qb = q - LA;
-        if constexpr (KMB && EB == 2) {
+        if constexpr (KMB && BC) {
+          dma16(rsb, bs + (wid * LB + qb) * 1024, (int)km_codes_offset((wid * LB + qb) * 64 + lane, k0),
+                (int)((uint32_t)(k0 / 2) * ldb));
+        } else if constexpr (KMB && EB == 2) {
           dma16(rsb, bs + (wid * LB + qb) * 1024, (int)km16_offset(Width<BN>{}, (wid * LB + qb) * 64 + lane, k0, ldb, ext_b),
                 (int)((uint32_t)(k0 / 2) * ldb));
         } else if constexpr (KMB) {
@@ -525,6 +589,9 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
           const uint32_t c2 = (uint32_t)((pos + CPR_B - rot) % CPR_B);
           dma16(rsb, bs + (wid * LB + qb) * 1024, k0 + kr >= K ? ext_b : (int)((uint32_t)kr * ldb + 16 * c2),
                 (int)((uint32_t)k0 * ldb));
+        } else if constexpr (BC) {
+          const int r0 = (wid * LB + qb) * 16;
+          dma16(rsb, bs + r0 * 64, k0 / 2 + 16 * cc >= K / 2 ? ext_b : (int)(vc + (uint32_t)r0 * ldb), k0 / 2);
         } else {
           const int r0 = (wid * LB + qb) * 8;
           dma16(rsb, bs + r0 * kBK, past ? ext_b : (int)(vb + (uint32_t)r0 * ldb), k0);
@@ -546,7 +613,9 @@ __device__ __forceinline__ void mm_tile(const P& p, const int64_t m0, const int6
     else return KMA ? lds_frag_km<BM>(As, wm * WM + 16 * i, lane) : lds_frag(As, wm * WM + 16 * i + r16, g);
   };
   auto frag_b = [&](const uint8_t* Bs, int j) -> v8i {
-    if constexpr (KMB && EB == 2) return lds_frag_km16<BN>(Bs, wn * WN + 16 * j, lane);
+    if constexpr (KMB && BC) return lds_frag_km_codes<BN>(Bs, wn * WN + 16 * j, lane);
+    else if constexpr (BC) return lds_frag_codes(Bs, wn * WN + 16 * j + r16, g);
+    else if constexpr (KMB && EB == 2) return lds_frag_km16<BN>(Bs, wn * WN + 16 * j, lane);
     else return KMB ? lds_frag_km<BN>(Bs, wn * WN + 16 * j, lane) : lds_frag(Bs, wn * WN + 16 * j + r16, g);
   };
   if constexpr (STAGES == 2) {

@@ -27,10 +27,11 @@ __device__ __forceinline__ int tile_target(int64_t t, int64_t v0, int64_t n) {
 
 constexpr float kGScale = 16384.0f;
 
-// fp16 operands: leading dimensions, K and strides in bytes.  Batch z takes bytes
-// z K .. of a row-major operand's rows (the last batch fewer), and the rows z K / 2 ..
-// of a K-major one's k_major_rows.
+// A in fp16, B's codes as they are (kOpB; or fp16): fp16 leading dimensions, and K and
+// strides of A, in bytes.  Batch z takes bytes z K .. of a row-major A's rows (the last
+// batch fewer), and the rows z K / 2 .. of a K-major operand's k_major_rows.
 struct Mm16Args : MmArgs {
+  static constexpr int kOpB = kOpCodes;
   int64_t k_total = 0, k_major_rows = 0;
   __host__ __device__ static int64_t k_bytes(const Mm16Args& p, int64_t bz) {
     const int64_t left = p.k_total - bz * p.K;
@@ -234,6 +235,11 @@ struct XentGradArgs : XentArgs {
   }
 };
 
+// G^T A: both operands K-major in fp16, the plain epilogue.
+struct KmArgs : Mm16Args {
+  static constexpr int kOpB = kOpF16;
+};
+
 // fp32 sums over several launches and K splits: out[z] (+)= A B^T.  N % 16 == 0.
 struct AddArgs : Mm16Args {
   static constexpr bool kTail = true;
@@ -274,7 +280,7 @@ static hipError_t launch_mm16_tile(const P& p0, hipStream_t st) {
   P p = p0;
   // several rounds of tiles, or long sums (a K split of G B is 128 steps and more: 237 -> 214 us)
   p.early_loads = tiles_m * tiles_n * p0.batch > (int64_t)device_cu_count() || p0.K >= 64 * kBK;
-  hipLaunchKernelGGL((mm_fp8_dma<kOpF16, kOpF16, BM, BN, WM_, WN_, MINB, -1, LAY, false, DEEP, P>),
+  hipLaunchKernelGGL((mm_fp8_dma<kOpF16, P::kOpB, BM, BN, WM_, WN_, MINB, -1, LAY, false, DEEP, P>),
                      dim3((unsigned)(tiles_m * tiles_n), 1, (unsigned)p0.batch), dim3(64 * WM_ * WN_), 0, st, p, tiles_m,
                      tiles_n, 4);
   return hipGetLastError();
@@ -298,9 +304,8 @@ static inline int pick16(int64_t M, int64_t N, int64_t batch, bool narrow) {
 // one epilogue each
 hipError_t launch_xent_lse(const XentLseArgs& p, hipStream_t st);
 hipError_t launch_xent_grad(const XentGradArgs& p, hipStream_t st);
-// G B into fp32 sums (A by rows, B K-major) and G^T A (both K-major, plain epilogue);
-// either may be null.
-hipError_t launch_mm16_grads(const AddArgs* add, const Mm16Args* km, hipStream_t st);
+// G B into fp32 sums (G by rows, the codes K-major) and G^T A; either may be null.
+hipError_t launch_mm16_grads(const AddArgs* add, const KmArgs* km, hipStream_t st);
 int64_t xent_lse_tile(int64_t M, int64_t N);  // columns that share a row's statistics
 
 }  // namespace fp8mi

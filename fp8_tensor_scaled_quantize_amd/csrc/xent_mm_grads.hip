@@ -15,7 +15,7 @@ template <int LAY, class P> static hipError_t launch_grads(const P& p, hipStream
 // Both products in one launch, 64 x 64 tiles, where neither fills the chip: the
 // first workgroups take G B (the longer sums), the others G^T A (64 x 1000 x 512:
 // 6.3 + 4.0 us and a launch between, together MEASURE).
-__global__ void __launch_bounds__(256, 2) mm16_both(AddArgs a, Mm16Args b, int64_t tiles_am, int64_t tiles_an,
+__global__ void __launch_bounds__(256, 2) mm16_both(AddArgs a, KmArgs b, int64_t tiles_am, int64_t tiles_an,
                                                     int64_t wgs_a, int64_t tiles_bm, int64_t tiles_bn) {
   using Lds = TileLds<64, 64, 4, 0>;
   __shared__ __align__(16) uint8_t pool[Lds::kBytes];
@@ -23,14 +23,14 @@ __global__ void __launch_bounds__(256, 2) mm16_both(AddArgs a, Mm16Args b, int64
   if ((int64_t)blockIdx.x < wgs_a) {
     const uint32_t tiles = (uint32_t)(tiles_am * tiles_an);
     tile_coords(blockIdx.x % tiles, tiles_am, tiles_an, 4, tm, tn);
-    mm_tile<kOpF16, kOpF16, 64, 64, 1, 4, -1, 2, false, 0>(a, tm * 64, tn * 64, (int64_t)(blockIdx.x / tiles), pool);
+    mm_tile<kOpF16, kOpCodes, 64, 64, 1, 4, -1, 2, false, 0>(a, tm * 64, tn * 64, (int64_t)(blockIdx.x / tiles), pool);
   } else {
     tile_coords((int64_t)blockIdx.x - wgs_a, tiles_bm, tiles_bn, 4, tm, tn);
     mm_tile<kOpF16, kOpF16, 64, 64, 1, 4, -1, 3, false, 0>(b, tm * 64, tn * 64, 0, pool);
   }
 }
 
-hipError_t launch_mm16_grads(const AddArgs* add, const Mm16Args* km, hipStream_t st) {
+hipError_t launch_mm16_grads(const AddArgs* add, const KmArgs* km, hipStream_t st) {
   if (add && km && pick16(add->M, add->N, add->batch, true) == 64 && pick16(km->M, km->N, 1, true) == 64) {
     const int64_t am = (add->M + 63) / 64, an = (add->N + 63) / 64, bm = (km->M + 63) / 64, bn = (km->N + 63) / 64;
     hipLaunchKernelGGL(mm16_both, dim3((unsigned)(am * an * add->batch + bm * bn)), dim3(256), 0, st, *add, *km, am, an,

@@ -474,7 +474,7 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
  *            which fp16 holds exactly, with fp32 sums)
  *   lse_i  = log sum_j exp l(i,j)         loss_i = lse_i - l(i, t_i)
  *   a, b       device E4M3 codes of the rows [M, K] and of the vocabulary's weights
- *              [N, K]; K (a multiple of 16, at most 65536), lda, ldb (at most 2^24) multiples
+ *              [N, K]; K (a multiple of 16, at most 65536), lda, ldb (at most 2^22) multiples
  *              of 16, 16-byte aligned.
  *   a_scale_inv, b_scale_inv, scale_rows   as fp8_mm_act.
  *   targets    device int32 or int64 [M] (target_bits).  Negative: the row is ignored,

@@ -76,6 +76,28 @@ def test_forms(M, N, K):
     assert not da[::5].any()
 
 
+@pytest.mark.parametrize("M,N,K", [(40, 600, 48), (300, 5000, 208), (2100, 3000, 336), (300, 33000, 80)])
+def test_nothing_beside_the_operands_is_used(M, N, K):
+    """Rows of a wider buffer that ends with the last row's last code: what lies
+    between the rows (NaN codes) and behind them stays out."""
+    a, b, t, sa, sb, g = operands(M, N, K, seed=7)
+    d = torch.rand(M, generator=g, device=DEV)
+    loss, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb)
+    da, db = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
+
+    def wide(x):
+        ld = x.shape[1] + 48
+        buf = torch.full((x.shape[0] * ld - 48,), 0x7F, dtype=torch.uint8, device=DEV)
+        view = torch.as_strided(buf, x.shape, (ld, 1))
+        view.copy_(x)
+        return view
+
+    a2, b2 = wide(a), wide(b)
+    loss2, lse2 = fp8mi.fp8_cross_entropy(a2, b2, t, sa, sb)
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    assert all(torch.equal(x, y) for x, y in zip((da, db), fp8mi.fp8_cross_entropy_grad(a2, b2, t, lse, d, sa, sb)))
+
+
 def test_the_same_whatever_the_workspace_holds():
     a, b, t, sa, sb, g = operands(1500, 20011, 528, 3)
     d = torch.ones(1, device=DEV)

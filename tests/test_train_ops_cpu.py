@@ -129,7 +129,7 @@ COMMON = [
     (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(K=24, lda=32, ldb=32), UNSUP),
     (dict(K=65552, lda=65552, ldb=65552), UNSUP), (dict(M=(1 << 20) + 1), UNSUP), (dict(M=1 << 20, K=1024, lda=1024, ldb=1024), UNSUP),
     (dict(N=1 << 31), UNSUP), (dict(bits=16), ENUM), (dict(a=None), NULL), (dict(b=None), NULL), (dict(t=None), NULL),
-    (dict(lda=48), SHAPE), (dict(ldb=48), SHAPE), (dict(lda=72), UNSUP), (dict(ldb=72), UNSUP), (dict(lda=(1 << 24) + 16), UNSUP),
+    (dict(lda=48), SHAPE), (dict(ldb=48), SHAPE), (dict(lda=72), UNSUP), (dict(ldb=72), UNSUP), (dict(lda=(1 << 22) + 16), UNSUP), (dict(ldb=(1 << 22) + 16), UNSUP),
     (dict(a=FAKE + 8), UNSUP), (dict(b=FAKE + 8), UNSUP), (dict(t=FAKE + 4), ARG), (dict(bits=32, t=FAKE + 2), ARG),
     (dict(sa=FAKE + 2), ARG), (dict(sb=FAKE + 1), ARG), (dict(ws=None), NULL), (dict(wsb=100), ARG), (dict(ws=FAKE + 8), ARG),
 ]
