@@ -28,8 +28,10 @@ class Fp8Head:
 
     def __init__(self, norm_weight: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, hist_len: int = 16):
         d = norm_weight.shape[0]
-        if weight.dim() != 2 or weight.shape[1] != d:
+        if weight.dim() != 2 or weight.shape[1] != d or weight.shape[0] < 1:
             raise ValueError(f"weight {tuple(weight.shape)} does not fit a width of {d}")
+        if d % 16:
+            raise ValueError(f"the width must be a multiple of 16, got {d}")
         self.norm_weight, self.weight, self.eps, self.hist_len = norm_weight, weight, eps, hist_len
         dev = norm_weight.device
         self.rings = {k: new_ring(hist_len, 1.0, dev) for k in ("n", "w")}
@@ -44,9 +46,14 @@ class Fp8Head:
             raise ValueError(f"x and residual must be [..., {d}], got {tuple(x.shape)}"
                              + ("" if residual is None else f" and {tuple(residual.shape)}"))
         x2, r2 = x.reshape(-1, d), None if residual is None else residual.reshape(-1, d)
-        if targets is not None and targets.numel() != x2.shape[0]:
+        if targets is None:
+            return x2, r2, None
+        # before a ring moves
+        if targets.dtype not in (torch.int64, torch.int32):
+            raise ValueError(f"targets must be int64 or int32, got {targets.dtype}")
+        if targets.numel() != x2.shape[0]:
             raise ValueError(f"{targets.numel()} targets for {x2.shape[0]} rows")
-        return x2, r2, None if targets is None else targets.reshape(-1)
+        return x2, r2, targets.reshape(-1).contiguous()
 
     def seed(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Seed the rings from the weight and a first batch, so that the first

@@ -19,8 +19,10 @@ class AdamW:
     get fp32 weights that the step updates and rounds to them.  state_bits 8: the
     states are E4M3 codes with a scale per 256 elements.  weight_decay: a number,
     or one per param.  max_norm: the gradients are scaled to at most that norm,
-    and a step whose gradients are not finite is skipped.  capturable: the step's
-    number and lr are device words (lr_word), so that a captured step goes on."""
+    and a step whose gradients are not finite is skipped (without a look from the
+    host: `steps` counts it all the same, the device's count does not).
+    capturable: the step's number and lr are device words (lr_word), so that a
+    captured step goes on."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
                  state_bits: int = 32, masters: bool = True, max_norm: float | None = None, capturable: bool = False,

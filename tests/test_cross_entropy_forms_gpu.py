@@ -45,7 +45,7 @@ def exact(a, b, t, sa, sb, d):
 # 64-wide, 128-wide, 256-wide tiles with and without edges, one and more pieces, K from a step to long
 SHAPES = [(2048, 20000, 512), (1111, 33001, 640), (4100, 9000, 1040), (600, 70001, 256), (96, 50001, 512), (64, 40000, 768),
           (33, 8200, 2048), (17, 8191, 4096), (200, 3000, 4112), (300, 300, 8192), (5000, 700, 96), (129, 131072, 64),
-          (8000, 33000, 32)]
+          (8000, 33000, 32), (1500, 2000, 16), (150, 9000, 16)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

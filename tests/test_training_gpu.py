@@ -97,8 +97,12 @@ def test_head_refuses():
             hd.forward(bad, t)
     with pytest.raises(ValueError, match="targets for"):
         hd.forward(x, t[:3])
+    rings = [r.clone() for r in hd.rings.values()]
     with pytest.raises(ValueError, match="targets must be"):
         hd.forward(x, t.float())
+    assert all(torch.equal(a, b) for a, b in zip(rings, hd.rings.values()))  # refused before a ring has moved
+    with pytest.raises(ValueError, match="multiple of 16"):
+        Fp8Head(rand(40), rand(10, 40))
     with pytest.raises(ValueError, match="does not fit"):
         Fp8Head(hd.norm_weight, rand(10, 32))
     for change in (lambda: x.add_(1), lambda: t.add_(1), lambda: hd.norm_weight.add_(1)):
@@ -110,6 +114,18 @@ def test_head_refuses():
     hd.forward(x, t)
     with pytest.raises(RuntimeError, match="another forward"):
         a.backward()
+
+
+def test_no_rows_strided_targets_and_one_token():
+    hd = head()
+    hd.freeze()
+    loss = hd.forward(rand(0, 64), torch.zeros(0, dtype=torch.int64, device=DEV))
+    g = hd.backward(torch.ones((), device=DEV))
+    assert float(loss) == 0 and g["x"].shape == (0, 64) and not g["weight"].any() and not g["norm_weight"].any()
+    x, t = rand(6, 64, seed=3), torch.arange(12, device=DEV)
+    assert torch.equal(hd.score(x, t[::2]), hd.score(x, t[::2].contiguous()))
+    one = hd.score(x[0], t[4])
+    assert one.shape == () and torch.equal(one, hd.score(x[:1], t[4:5])[0])
 
 
 def test_score_in_a_graph_and_after_a_new_freeze():
