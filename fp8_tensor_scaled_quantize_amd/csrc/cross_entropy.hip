@@ -48,11 +48,11 @@ struct Carve {
 };
 
 // Few rows, or few logits: xent_rows, 64 rows by 16 or 32 columns to a workgroup.
-// Graph replay, widened and in tiles -> xent_rows (us), 50001 x 1536: 16 rows 88 -> 37,
-// 64 rows 88 -> 54, 96 rows 88 -> 81, 128 rows 88 -> 91, 192 rows 88 -> 123; 32768 x 4096:
-// 128 rows 158 -> 106, 256 rows 186 -> 195; 8000 x 1024: 192 rows 32 -> 29, 384 rows
-// 40 -> 44; 1000 x 512: 512 rows 21 -> 18.
-bool few_rows(int64_t M, int64_t N) { return M <= 128 || M * N <= (1 << 20); }
+// Graph replay, in tiles -> xent_rows (us): 50001 x 1536 16 rows 53 -> 29, 64 rows 53 -> 53,
+// 96 rows 53 -> 79; 32768 x 4096 64 rows 60 -> 60, 96 rows 60 -> 96; 8000 x 1024 96 rows 24 ->
+// 23, 192 rows 25 -> 29; 4000 x 1536 192 rows 26 -> 25, 256 rows 26 -> 28; 1000 x 512 512
+// rows 23 -> 19.
+bool few_rows(int64_t M, int64_t N) { return M <= 64 || M * N <= (3 << 18); }
 int64_t rows_tile(int64_t N) { return N >= 8192 ? 32 : 16; }
 
 // Rows of a workgroup of the join: 16 fill the lines that it reads, fewer while there
@@ -192,8 +192,10 @@ __global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const vo
 // cycles for two values and a wave, is what a wider workgroup saves on the rows').
 // Lane group g takes k = 16 g .. + 15 and 64 + 16 g .. + 15 of a step, A and B
 // alike, so that a load instruction reads 64 contiguous bytes of a row.  The
-// waves' sums meet in LDS, and wave i finishes strip i.  (1 x 32768 x 1536, widened
-// and in 128 x 128 tiles: 60 us; this: MEASURE.)
+// waves' sums meet in LDS, and wave i finishes strip i.  One row of 32768 x 1536: 12 us,
+// 4.3 TB/s; 16 rows of 50001 x 1536: 20 us, 3.8 TB/s.  64 rows (45 us) wait for the loads
+// of U = 2 steps twice, three waves a SIMD; held to four the compiler spills 100
+// registers.
 struct RowsGrad {  // what the gradient's form does besides: A in fp16, for the products after it
   static constexpr bool kGrad = true;
   Widen a;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(256) xent_rows(XentArgs p, G extra, uint32_t c
 // by returning device-scope atomics and wait for them before they take a ticket
 // (0 before the launch), as the ring's fold does.  (Plain stores behind a
 // device-scope fence, whose L2 write-back every workgroup pays for: 29 us instead
-// of MEASURE at 4096 rows.)
+// of 8.6 at 4096 rows.)
 __device__ __forceinline__ uint64_t swap64(uint64_t* p, uint64_t v) {
   return __hip_atomic_exchange(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }

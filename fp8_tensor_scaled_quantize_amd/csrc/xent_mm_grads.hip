@@ -14,7 +14,7 @@ template <int LAY, class P> static hipError_t launch_grads(const P& p, hipStream
 
 // Both products in one launch, 64 x 64 tiles, where neither fills the chip: the
 // first workgroups take G B (the longer sums), the others G^T A (64 x 1000 x 512:
-// 6.3 + 4.0 us and a launch between, together MEASURE).
+// 6.3 + 4.0 us and a launch between, together 6.0).
 __global__ void __launch_bounds__(256, 2) mm16_both(AddArgs a, KmArgs b, int64_t tiles_am, int64_t tiles_an,
                                                     int64_t wgs_a, int64_t tiles_bm, int64_t tiles_bn) {
   using Lds = TileLds<64, 64, 4, 0>;
