@@ -605,12 +605,15 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const int64_t first_cols = up(c.N < cols ? c.N : cols, 8);
   const int64_t k_split = up((2 * first_cols + plan.splits - 1) / plan.splits, 128);
   const int64_t splits = (2 * first_cols + k_split - 1) / k_split;
+  // by the whole vocabulary, as in the forward pass: a narrow last piece's logits
+  // then add up in the order of the others, and of those that made lse
+  const bool from_codes = few_rows(c.M, c.N);
   for (int64_t v0 = 0; v0 < c.N; v0 += cols) {
     const int64_t n = c.N - v0 < cols ? c.N - v0 : cols;
     XentGradArgs g;
     g.lse = c.lse;
     g.d = at(plan.g); g.ld_d = plan.ld_g;
-    if (few_rows(c.M, n)) {  // the logits straight from the codes, beside the widening of A
+    if (from_codes) {  // the logits straight from the codes, beside the widening of A
       if (v0 > 0) rows.chunks = 0;
       fill_rows(g, c, v0, n);
       FP8MI_TRY(launch_rows(g, RowsGrad{rows}, widen_groups(rows), st));

@@ -98,6 +98,25 @@ def test_nothing_beside_the_operands_is_used(M, N, K):
     assert all(torch.equal(x, y) for x, y in zip((da, db), fp8mi.fp8_cross_entropy_grad(a2, b2, t, lse, d, sa, sb)))
 
 
+def test_rows_as_far_apart_as_allowed():
+    """ldb = 2^22: a buffer's offsets hold 256 such rows, so the vocabulary is taken in pieces."""
+    M, N, K, ld = 3000, 300, 64, 1 << 22
+    a, b, t, sa, sb, g = operands(M, N, K, seed=9)
+    far = torch.as_strided(torch.empty((N - 1) * ld + K, dtype=torch.uint8, device=DEV), (N, K), (ld, 1))
+    far.copy_(b)
+    d = torch.rand(M, generator=g, device=DEV)
+    loss, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb)
+    loss2, lse2 = fp8mi.fp8_cross_entropy(a, far, t, sa, sb)
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    da, db = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
+    da2, db2 = fp8mi.fp8_cross_entropy_grad(a, far, t, lse, d, sa, sb)
+    assert torch.equal(db, db2)
+    # da's sums are split elsewhere: each side is off by its own bf16 rounding
+    assert (da.double() - da2.double()).norm() <= 2 * HALF * da.double().norm()
+    few, flse = fp8mi.fp8_cross_entropy(a[:9], far, t[:9], sa, sb)
+    assert (few - loss[:9]).abs().max() < 1e-5
+
+
 def test_the_same_whatever_the_workspace_holds():
     a, b, t, sa, sb, g = operands(1500, 20011, 528, 3)
     d = torch.ones(1, device=DEV)
