@@ -641,13 +641,14 @@ fp8mi_status fp8_rmsnorm_grad(const void* dy, int dtype, int64_t rows, int64_t c
                   "rmsnorm gradient launch");
 }
 
-// Sizes that the cross entropy's kernels and 32-bit offsets cover.
+// Sizes that the cross entropy's kernels, 32-bit offsets and grids (below 2^32 threads)
+// cover.
 static fp8mi_status check_xent_size(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 1 || K < 1)
     return fail(FP8MI_ERR_SHAPE, "M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
-  if (K % 16 || K > 65536 || M > (1 << 20) || M >= (INT64_C(1) << 30) / (K + 64) || N > INT64_C(0x7FFFFFFF))
+  if (K % 16 || K > 65536 || M > (1 << 20) || M >= (INT64_C(1) << 30) / (K + 64) || N > (1 << 28))
     return fail(FP8MI_ERR_UNSUPPORTED, "M=%lld N=%lld K=%lld: K is a multiple of 16 up to 65536, M at most 2^20, M (K + 64) "
-                "below 2^30, N below 2^31", (long long)M, (long long)N, (long long)K);
+                "below 2^30, N at most 2^28", (long long)M, (long long)N, (long long)K);
   return FP8MI_OK;
 }
 
@@ -726,10 +727,14 @@ fp8mi_status fp8_cross_entropy_grad(const uint8_t* a, int64_t lda, const uint8_t
   return from_hip(launch_xent_backward(c, static_cast<hipStream_t>(stream)), "cross entropy gradient launch");
 }
 
-// One tensor of a list: n elements of dtype at p.
-static fp8mi_status check_elements(const char* name, int i, const void* p, int64_t n, int dt) {
+// What grids of 2^31 threads cover: 1024 elements of a tensor, 32768 of all gradients, to
+// a workgroup of 256.
+constexpr int64_t kAdamWElements = INT64_C(1) << 33, kNormElements = INT64_C(1) << 38;
+
+// One tensor of a list: n elements of dtype at p, at most `most`.
+static fp8mi_status check_elements(const char* name, int i, const void* p, int64_t n, int dt, int64_t most) {
   if (!valid_dtype(dt)) return fail(FP8MI_ERR_ENUM, "tensor %d: %s dtype %d is not F32/F16/BF16", i, name, dt);
-  if (n < 0 || n > (INT64_C(1) << 42)) return fail(FP8MI_ERR_SHAPE, "tensor %d: %lld elements", i, (long long)n);
+  if (n < 0 || n > most) return fail(FP8MI_ERR_SHAPE, "tensor %d: %lld elements", i, (long long)n);
   if (n > 0 && !p) return fail(FP8MI_ERR_NULL, "tensor %d: %s is NULL", i, name);
   if (reinterpret_cast<uintptr_t>(p) % dtype_bytes(dt))
     return fail(FP8MI_ERR_ARG, "tensor %d: %s not aligned to its element size", i, name);
@@ -751,8 +756,8 @@ fp8mi_status fp8_adamw_step(const fp8mi_adamw_tensor* tensors, int32_t count, co
     return fail(FP8MI_ERR_ARG, "device words must be 4-byte aligned");
   for (int i = 0; i < count; ++i) {
     const fp8mi_adamw_tensor& t = tensors[i];
-    fp8mi_status s = check_elements("param", i, t.param, t.n, t.param_dtype);
-    if (s == FP8MI_OK) s = check_elements("grad", i, t.grad, t.n, t.grad_dtype);
+    fp8mi_status s = check_elements("param", i, t.param, t.n, t.param_dtype, kAdamWElements);
+    if (s == FP8MI_OK) s = check_elements("grad", i, t.grad, t.n, t.grad_dtype, kAdamWElements);
     if (s != FP8MI_OK) return s;
     if (t.state_bits != 32 && t.state_bits != 8)
       return fail(FP8MI_ERR_ENUM, "tensor %d: state_bits %d is not 32/8", i, t.state_bits);
@@ -784,7 +789,7 @@ fp8mi_status fp8_adamw_step(const fp8mi_adamw_tensor* tensors, int32_t count, co
 size_t fp8_grad_norm_workspace_bytes(const fp8mi_norm_tensor* tensors, int32_t count) {
   if (!tensors || count <= 0) return 0;
   for (int i = 0; i < count; ++i)
-    if (tensors[i].n < 0 || tensors[i].n > (INT64_C(1) << 42)) return 0;
+    if (tensors[i].n < 0 || tensors[i].n > kNormElements) return 0;
   return (size_t)grad_norm_workspace_bytes(tensors, count);
 }
 
@@ -796,10 +801,10 @@ fp8mi_status fp8_grad_norm(const fp8mi_norm_tensor* tensors, int32_t count, cons
   if (!aligned4(norm_out) || !aligned4(clip_out)) return fail(FP8MI_ERR_ARG, "fp32 outputs must be 4-byte aligned");
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
-    const fp8mi_status s = check_elements("grad", i, tensors[i].grad, tensors[i].n, tensors[i].dtype);
+    const fp8mi_status s = check_elements("grad", i, tensors[i].grad, tensors[i].n, tensors[i].dtype, kNormElements);
     if (s != FP8MI_OK) return s;
     total += tensors[i].n;
-    if (total > (INT64_C(1) << 42)) return fail(FP8MI_ERR_SHAPE, "more than 2^42 elements");
+    if (total > kNormElements) return fail(FP8MI_ERR_SHAPE, "more than 2^38 elements");
   }
   const size_t need = fp8_grad_norm_workspace_bytes(tensors, count);
   if (need > 0 && !workspace) return fail(FP8MI_ERR_NULL, "workspace is NULL (%zu bytes needed)", need);

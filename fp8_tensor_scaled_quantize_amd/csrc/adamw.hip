@@ -358,11 +358,11 @@ hipError_t launch_adamw(const fp8mi_adamw_tensor* tensors, int count, const Adam
     a.base = i;
     int64_t wgs = 0;
     int k = 0;
-    // a launch ends where the table is full or its grid would pass 2^30
-    // workgroups; an empty tensor takes an entry and no workgroup
+    // a launch ends where the table is full or its grid would pass 2^31 threads (a
+    // grid holds fewer than 2^32); an empty tensor takes an entry and no workgroup
     for (; k < kAdamWTensors && i + k < count; ++k) {
       const int64_t need = (tensors[i + k].n + kChunk - 1) / kChunk;
-      if (k > 0 && wgs + need > (1 << 30)) break;
+      if (k > 0 && wgs + need > (1 << 23)) break;
       a.tab.t[k] = tensors[i + k];
       a.tab.first[k] = (int32_t)wgs;
       wgs += need;

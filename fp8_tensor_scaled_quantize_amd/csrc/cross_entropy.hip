@@ -555,7 +555,9 @@ hipError_t launch_xent_forward(const XentCall& c, hipStream_t st) {
   } else {
     uint16_t* const a16 = reinterpret_cast<uint16_t*>(c.ws + plan.a16);
     FP8MI_TRY(launch_widen(widen(c.a, c.lda, c.M, c.K, a16, plan.ld), ticket, st));
-    const int64_t cols = even_pieces(c.N, offset_columns(c.ldb));  // a multiple of every tile's
+    // 256 x 256 tiles of 512 threads: at most 2^31 of them in a grid
+    const int64_t most = offset_columns(c.ldb), grid = (INT64_C(1) << 38) / c.M;
+    const int64_t cols = even_pieces(c.N, most < grid ? most : grid);  // a multiple of every tile's
     for (int64_t v0 = 0; v0 < c.N; v0 += cols) {
       XentLseArgs p;
       fill_logits(p, c, a16, plan.ld, v0, c.N - v0 < cols ? c.N - v0 : cols);

@@ -53,6 +53,8 @@ class Fp8Head:
             raise ValueError(f"targets must be int64 or int32, got {targets.dtype}")
         if targets.numel() != x2.shape[0]:
             raise ValueError(f"{targets.numel()} targets for {x2.shape[0]} rows")
+        if targets.device != x.device:
+            raise ValueError(f"targets are on {targets.device}, x on {x.device}")
         return x2, r2, targets.reshape(-1).contiguous()
 
     def seed(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:

@@ -485,7 +485,7 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
  *              fixed order.
  *   workspace  device scratch of fp8_cross_entropy_workspace_bytes bytes, 16-byte
  *              aligned, no initialisation; calls in flight on one workspace race.
- * M is at most 2^20, M (K + 64) below 2^30, N below 2^31.  M == 0 writes the mean alone.
+ * M is at most 2^20, M (K + 64) below 2^30, N at most 2^28.  M == 0 writes the mean alone.
  * A logit that is infinite or NaN makes the row's loss NaN.
  */
 FP8MI_API fp8mi_status fp8_cross_entropy(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M,
@@ -548,7 +548,7 @@ FP8MI_API size_t fp8_cross_entropy_grad_workspace_bytes(int64_t M, int64_t N, in
  *   lr_device  NULL, or (with step_device) device fp32 in lr's place.
  *   grad_scale NULL, or device fp32 c (fp8_grad_norm's clip).  Not finite: the step
  *              is skipped -- parameters, masters, states and step_device stay.
- * Tensors of n == 0 are allowed.  No two tensors may share memory.
+ * Tensors of n == 0 are allowed; n is at most 2^33.  No two tensors may share memory.
  */
 #define FP8MI_ADAMW_STEP_WORDS 4
 typedef struct {
@@ -587,7 +587,8 @@ FP8MI_API fp8mi_status fp8_adamw_step(const fp8mi_adamw_tensor* tensors, int32_t
  *              finite (fp8_adamw_step skips such a step).
  *   workspace  device scratch of fp8_grad_norm_workspace_bytes bytes, 8-byte aligned,
  *              no initialisation; calls in flight on one workspace race.
- * Two launches (one more for each further 128 tensors).  No gradients: norm 0.
+ * Two launches (one more for each further 128 tensors).  No gradients: norm 0.  At most
+ * 2^38 elements in all.
  */
 typedef struct {
   const void* grad;

@@ -361,3 +361,19 @@ def test_norm_without_a_limit_and_in_a_graph():
         torch.cuda.synchronize()
         got = out.clone(), clip.clone()
         assert torch.equal(got[0], fp8mi.fp8_grad_norm(g, 2.0, clip_out=clip)) and torch.equal(got[1], clip)
+
+
+def test_more_elements_than_a_grid_holds():
+    """Five tensors of 2^31 elements: four to a launch.  All weights go from 0 to -lr, a power of two, which bf16 holds
+    (fp32's few roundings are far below its half step), and every code of m and sqrt(v) is its block's largest."""
+    n, lr = 1 << 31, 2.0 ** -9
+    params = [torch.zeros(n, dtype=torch.bfloat16, device=DEV) for _ in range(5)]
+    m, v = ([torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(5)] for _ in range(2))
+    ms, vs = ([torch.zeros(n // 256, device=DEV) for _ in range(5)] for _ in range(2))
+    grad = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    fp8mi.fp8_adamw_step(params, [grad] * 5, m, v, 1, lr, (0.9, 0.95), 1e-8, 0.0, None, ms, vs)
+    for t, want in (*((p, -lr) for p in params), *((c, 0x7E) for c in (*m, *v))):
+        lo, hi = torch.aminmax(t)
+        assert lo == want and hi == want
+    norm = fp8mi.fp8_grad_norm([grad] * 5)
+    assert abs(float(norm) - (5 * n) ** 0.5) <= 2.0 ** -23 * (5 * n) ** 0.5

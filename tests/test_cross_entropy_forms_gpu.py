@@ -128,3 +128,23 @@ def test_the_same_whatever_the_workspace_holds():
         out.append((loss, lse, *fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb, workspace=ws[1])))
     for o in out[1:]:
         assert all(torch.equal(x, y) for x, y in zip(o, out[0]))
+
+
+def test_more_logits_than_a_grid_holds():
+    """2^39 logits: two launches.  Rows of A are 0 or (1, 0, ...), B's are (1, 0, ...) or (2, 0, ...)."""
+    M, N, K = 1 << 20, 1 << 19, 16
+    one, two = (int(torch.tensor(x).to(E4M3).view(torch.uint8)) for x in (1.0, 2.0))
+    a, b = torch.zeros(M, K, dtype=torch.uint8, device=DEV), torch.zeros(N, K, dtype=torch.uint8, device=DEV)
+    a[::3, 0] = one
+    b[:, 0] = one
+    b[1::2, 0] = two
+    t = torch.arange(M, device=DEV) % N
+    loss, lse = fp8mi.fp8_cross_entropy(a, b, t)
+    on = a[:, 0] == one
+    e = torch.tensor(1.0, dtype=torch.float64, device=DEV).exp()
+    want = torch.where(on, (N / 2 * (e + e * e)).log(), torch.tensor(float(N), device=DEV).double().log())
+    logit = torch.where(on, 1.0 + (t % 2).double(), 0.0)
+    # a sum's terms pass fewer than 256 roundings (64 in a tile, 128 tiles to a segment of the join, 16 segments), each
+    # of 2^-23 with its exponential's; lse and loss, below 16, round by 2^-21 at most
+    for got, w in ((lse, want), (loss, want - logit)):
+        assert (got.double() - w).abs().max() <= 256 * 2.0 ** -23 + 2 * 2.0 ** -21

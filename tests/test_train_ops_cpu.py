@@ -79,6 +79,20 @@ def test_grad_norm_rejects(L):
     assert call(ws=None) == NULL and call(ws=FAKE + 4) == ARG and call(nbytes=8) == ARG
 
 
+def test_sizes_beyond_a_grid(L):
+    """A grid holds fewer than 2^32 threads: sizes that would need more are refused before anything is read."""
+    assert L.fp8_adamw_step(tensor(n=(1 << 33) + 1), 1, hyper(), None) == SHAPE
+
+    def norm(*sizes):
+        table = b"".join(struct.pack("@Pqi4x", FAKE, n, 2) for n in sizes)
+        return L.fp8_grad_norm(table, len(sizes), None, FAKE, FAKE, None, 0, None)
+
+    assert norm((1 << 38) + 1) == SHAPE and norm(1 << 37, (1 << 37) + 1) == SHAPE
+    assert norm(1 << 37, 1 << 37) == NULL  # allowed: only the workspace is missing
+    for f in (L.fp8_cross_entropy_workspace_bytes, L.fp8_cross_entropy_grad_workspace_bytes):
+        assert f(1, (1 << 28) + 1, 16) == 0 and f(1, 1 << 28, 16) > 0
+
+
 def test_binding_refuses_lists():
     f32 = lambda n=4: torch.zeros(n)  # noqa: E731
 

@@ -116,6 +116,14 @@ def test_head_refuses():
         a.backward()
 
 
+def test_targets_elsewhere_are_refused_before_a_ring_moves():
+    hd = head()
+    rings = [r.clone() for r in hd.rings.values()]
+    with pytest.raises(ValueError, match="targets are on"):
+        hd.forward(rand(4, 64), torch.zeros(4, dtype=torch.int64))
+    assert all(torch.equal(a, b) for a, b in zip(rings, hd.rings.values()))
+
+
 def test_no_rows_strided_targets_and_one_token():
     hd = head()
     hd.freeze()
