@@ -178,14 +178,12 @@ __device__ __forceinline__ uint32_t grid_steps(float y, float& k, float& f) {
 }
 
 // y >= 0 rounded to the grid point above with the probability of its place between
-// the two: h16 / 2^16 against the 20 bits below a code's mantissa.  Adding to the
-// value's bits carries into the exponent as the codes' order does; subnormals (the
-// grid 2^-9 below 2^-6) go one binade up, where that is the grid.
+// the two: h16 / 2^16 against the 20 bits below a code's mantissa.  2^-120 takes E4M3's
+// exponents, its subnormals too, to fp32's, so that a code is the bits above those 20,
+// and a carry goes into the exponent as the codes' order does.
 __device__ __forceinline__ uint32_t round_code(float y, uint32_t h16) {
-  y = fminf(y, 448.0f);
-  const bool small = y < 0.015625f;
-  const uint32_t bits = __float_as_uint(small ? y + 0.015625f : y);
-  return ((bits + (0xFFFF7u - 16u * h16)) >> 20) - (small ? 968u : 960u);
+  const uint32_t bits = __float_as_uint(fminf(y, 448.0f) * 7.52316384526264e-37f);
+  return (bits + (~(16u * h16) & 0xFFFF0u) + 7u) >> 20;
 }
 
 // Correctly rounded square root of a normal x (or 0, or one that is not finite) and
@@ -193,15 +191,20 @@ __device__ __forceinline__ uint32_t round_code(float y, uint32_t h16) {
 // of what it rounds, and so does the next step; with these the codes are the
 // formula's, operation by operation, in IEEE arithmetic.
 __device__ __forceinline__ float exact_root(float x) {
-  const float s = __builtin_amdgcn_sqrtf(x);  // within an ulp
+  const float s = __builtin_amdgcn_sqrtf(x);  // within an ulp; at 0, infinity and NaN both comparisons are false
   const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
-  float r = fmaf(-below, s, x) <= 0.0f ? below : s;
-  r = fmaf(-above, s, x) > 0.0f ? above : r;
-  return x > 0.0f && x <= 3.40282347e38f ? r : s;
+  const float r = fmaf(-below, s, x) <= 0.0f ? below : s;
+  return fmaf(-above, s, x) > 0.0f ? above : r;
 }
 __device__ __forceinline__ float exact_quotient(float x, float s, float r) {
   const float q = x * r;
   return fmaf(fmaf(-q, s, x), r, q);
+}
+// Correctly rounded 1 / s for s of 2^-100 to 2^120 (compared with the division for every
+// mantissa); 0 for 0.
+__device__ __forceinline__ float exact_reciprocal(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return s != 0.0f ? fmaf(fmaf(-s, r, 1.0f), r, r) : 0.0f;
 }
 
 // A 32-bit integer hash (two multiplications between shifts).
@@ -276,7 +279,7 @@ __device__ __forceinline__ void adamw_block(const fp8mi_adamw_tensor& t, const A
       rr = umax(rr, __float_as_uint(r[e]));
     }
     const float sm = block_scale(__uint_as_float(wave_umax(mm))), sr = block_scale(__uint_as_float(wave_umax(rr)));
-    const float im = sm != 0.0f ? 1.0f / sm : 0.0f, ir = sr != 0.0f ? 1.0f / sr : 0.0f;
+    const float im = exact_reciprocal(sm), ir = exact_reciprocal(sr);
     const uint64_t group = (uint64_t)i >> 2;
     uint32_t x = mix32((uint32_t)group ^ key ^ mix32((uint32_t)(group >> 32))) | 1u, cm = 0u, cv = 0u;
 #pragma unroll
@@ -325,7 +328,8 @@ __global__ void __launch_bounds__(kNT) adamw_kernel(AdamWTable a) {
   if (at >= t.n) return;
   const StepNumbers s = step_numbers(a.h);
   if (t.state_bits == 8) {
-    const uint32_t key = mix32(mix32(mix32(a.h.seed) ^ s.t) ^ (uint32_t)(a.base + k));
+    const uint32_t t32 = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.t);  // scalar hashing
+    const uint32_t key = mix32(mix32(mix32(a.h.seed) ^ t32) ^ (uint32_t)(a.base + k));
     adamw_block<true>(t, a.h, s, c, key, at);
   } else {
     adamw_block<false>(t, a.h, s, c, 0u, at);
