@@ -908,14 +908,18 @@ def fp8_cross_entropy_grad(a: torch.Tensor, b: torch.Tensor, targets: torch.Tens
 _ADAMW_TENSOR, _ADAMW_HYPER, _NORM_TENSOR = "7Pq3if", struct.Struct("@4dq3PI4x"), "Pqi4x"
 
 
-# (A step over small tensors is as long as these checks: they are written as
-# comprehensions, and look for the culprit only once one has failed.)
+# (A step over small tensors is as long as these checks: they are maps of the tensors'
+# methods, and look for the culprit only once one has failed.)
+_contiguous, _numel, _data_ptr = torch.Tensor.is_contiguous, torch.Tensor.numel, torch.Tensor.data_ptr
+_get_device, _element_size = torch.Tensor.get_device, torch.Tensor.element_size
+
+
 def _flat(ts, name: str, sizes=None) -> None:
     """Contiguous tensors (elementwise operators read them as flat arrays), of
     the given element counts."""
-    if False in [t.is_contiguous() for t in ts]:
+    if not all(map(_contiguous, ts)):
         raise ValueError(f"{name}[{[t.is_contiguous() for t in ts].index(False)}] must be contiguous")
-    if sizes is not None and [t.numel() for t in ts] != sizes:
+    if sizes is not None and list(map(_numel, ts)) != sizes:
         if len(ts) != len(sizes):
             raise ValueError(f"{len(ts)} {name} for {len(sizes)} params")
         for i, t in enumerate(ts):
@@ -930,13 +934,36 @@ def _dtypes(ts, name: str):
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {[t.dtype for t in ts]}") from None
 
 
+def _all_f32(ts) -> bool:
+    return all([t.dtype is torch.float32 for t in ts])
+
+
 def _all_on_device(*lists) -> None:
     """_on_device for lists of tensors (no None among them)."""
-    here = {t.get_device() for ts in lists for t in ts}
+    here = set()
+    for ts in lists:
+        here.update(map(_get_device, ts))
     if len(here) != 1 or min(here) < 0 or min(here) != _current_device():
         for ts in lists:
             _on_device(*ts)  # says which
         _on_device(*[ts[0] for ts in lists if len(ts)])
+
+
+def _given(ts, n: int):
+    """A list with None where there is no tensor: which entries have one, those
+    tensors, and all addresses (0 without)."""
+    if ts is None:
+        return (), (), (0,) * n
+    if len(ts) != n:
+        raise ValueError("masters and scales: one entry per param (None where there is none)")
+    at = [i for i, t in enumerate(ts) if t is not None]
+    kept = ts if len(at) == n else [ts[i] for i in at]
+    ptrs = list(map(_data_ptr, kept))
+    if len(at) != n:
+        some, ptrs = ptrs, [0] * n
+        for i, p in zip(at, some):
+            ptrs[i] = p
+    return at, kept, ptrs
 
 
 def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch.Tensor = 1e-3, betas=(0.9, 0.999),
@@ -952,32 +979,35 @@ def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch
     a device scalar.  weight_decay: a number, or one per tensor.  A grad_scale
     (device scalar) that is not finite skips the step."""
     n = len(params)
-    sizes = [p.numel() for p in params]
+    sizes = list(map(_numel, params))
     _flat(params, "params")
     _flat(grads, "grads", sizes)
     _flat(exp_avgs, "exp_avgs", sizes)
     _flat(exp_avg_sqs, "exp_avg_sqs", sizes)
-    none = [None] * n
-    masters = none if masters is None else masters
-    ms = none if exp_avg_scales is None else exp_avg_scales
-    vs = none if exp_avg_sq_scales is None else exp_avg_sq_scales
-    if len(masters) != n or len(ms) != n or len(vs) != n:
-        raise ValueError("masters and scales: one entry per param (None where there is none)")
-    kept = [m for m in masters if m is not None]
+    at_w, kept, wptr = _given(masters, n)
+    at_m, m_scales, mptr = _given(exp_avg_scales, n)
+    at_v, v_scales, vptr = _given(exp_avg_sq_scales, n)
     if kept:
-        _flat(kept, "masters", [k for m, k in zip(masters, sizes) if m is not None])
-        if [m for m in kept if m.dtype is not torch.float32]:
+        _flat(kept, "masters", sizes if len(kept) == n else [sizes[i] for i in at_w])
+        if not _all_f32(kept):
             raise ValueError(f"masters must be float32, got {[m.dtype for m in kept]}")
-    scales = [a for a in (*ms, *vs) if a is not None]
-    if scales:
-        for i, (m, v, a, b, k) in enumerate(zip(exp_avgs, exp_avg_sqs, ms, vs, sizes)):
-            if a is None and b is None:
-                continue
-            if a is None or b is None or m.element_size() != 1 or v.element_size() != 1:
-                raise ValueError(f"8-bit states of params[{i}] need 1-byte codes and scales for both")
-            _typed_vector(a, -(-k // ADAMW_BLOCK), "scales", _F32_ONLY)
-            _typed_vector(b, -(-k // ADAMW_BLOCK), "scales", _F32_ONLY)
-    if [1 for m, a in zip((*exp_avgs, *exp_avg_sqs), (*ms, *vs)) if a is None and m.dtype is not torch.float32]:
+    bits, scales = [32] * n, []
+    wide = [*exp_avgs, *exp_avg_sqs]
+    if at_m or at_v:
+        codes = [t[i] for t in (exp_avgs, exp_avg_sqs) for i in at_m]
+        if at_m != at_v or set(map(_element_size, codes)) != {1}:
+            i = next(i for i in sorted({*at_m, *at_v}) if (i in at_m) != (i in at_v) or
+                     exp_avgs[i].element_size() != 1 or exp_avg_sqs[i].element_size() != 1)
+            raise ValueError(f"8-bit states of params[{i}] need 1-byte codes and scales for both")
+        scales = [*m_scales, *v_scales]
+        blocks = [-(-sizes[i] // ADAMW_BLOCK) for i in at_m]
+        if list(map(_numel, scales)) != blocks + blocks or not all(map(_contiguous, scales)) or not _all_f32(scales):
+            for t, k in zip(scales, blocks + blocks):
+                _typed_vector(t.flatten() if t.is_contiguous() else t, k, "scales", _F32_ONLY)
+        for i in at_m:
+            bits[i] = 8
+        wide = [t[i] for t in (exp_avgs, exp_avg_sqs) for i in range(n) if bits[i] == 32] if len(at_m) < n else ()
+    if not _all_f32(wide):
         raise ValueError("states must be float32, or codes with their scales")
     pdt, gdt = _dtypes(params, "params"), _dtypes(grads, "grads")
     decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
@@ -998,20 +1028,21 @@ def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch
         return
     words = [t for t in (grad_scale, step if step_ptr else None, lr if lr_ptr else None) if t is not None]
     _all_on_device(params, grads, exp_avgs, exp_avg_sqs, kept, scales, words)
-    at = [p.data_ptr() for p in params]
+    at = list(map(_data_ptr, params))
     if len(set(at)) != n and len({p for p, k in zip(at, sizes) if k}) != len([k for k in sizes if k]):
         raise ValueError("the same param is there twice")
-    wptr, mptr, vptr = ([0 if t is None else t.data_ptr() for t in ts] for ts in (masters, ms, vs))
-    rows = zip(at, [g.data_ptr() for g in grads], wptr, [t.data_ptr() for t in exp_avgs],
-               [t.data_ptr() for t in exp_avg_sqs], mptr, vptr, sizes, pdt, gdt, [32 if a is None else 8 for a in ms], decay)
-    flat = [x for row in rows for x in row]
+    flat = [0] * (12 * n)  # a tensor's words, column by column
+    columns = (at, map(_data_ptr, grads), wptr, map(_data_ptr, exp_avgs), map(_data_ptr, exp_avg_sqs), mptr, vptr, sizes,
+               pdt, gdt, bits, decay)
+    for i, column in enumerate(columns):
+        flat[i::12] = column
     hyper = _ADAMW_HYPER.pack(0.0 if lr_ptr else float(lr), betas[0], betas[1], eps, 0 if step_ptr else step, step_ptr or 0,
                               lr_ptr or 0, 0 if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF)
     status = lib().fp8_adamw_step(struct.pack("@" + _ADAMW_TENSOR * n, *flat), n, hyper,
                                   _stream(params[0] if n else step))
     if status:
         _check(status)
-    _changed_in_place(params + kept if isinstance(params, list) else [*params, *kept])
+    _changed_in_place([*params, *kept])
 
 
 def fp8_grad_norm(grads, max_norm: float | None = None, out: torch.Tensor | None = None,
@@ -1027,8 +1058,8 @@ def fp8_grad_norm(grads, max_norm: float | None = None, out: torch.Tensor | None
         out = torch.empty(1, dtype=torch.float32, device=grads[0].device)
     _scalar(out, "out")
     _scalar(clip_out, "clip_out")
-    rows = zip([t.data_ptr() for t in grads], [t.numel() for t in grads], _dtypes(grads, "grads"))
-    flat = [x for row in rows for x in row]
+    flat = [0] * (3 * n)
+    flat[::3], flat[1::3], flat[2::3] = map(_data_ptr, grads), map(_numel, grads), _dtypes(grads, "grads")
     table = struct.pack("@" + _NORM_TENSOR * n, *flat)
     L = lib()
     if workspace is None:
