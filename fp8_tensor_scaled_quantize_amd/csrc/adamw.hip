@@ -23,7 +23,10 @@ constexpr int kBlock = 256;        // elements of an 8-bit state that share a sc
 constexpr int kAdamWTensors = 44, kNormTensors = 128;  // of one launch: its arguments are at most 4 KiB
 // Elements per workgroup: a block per wave.  With four blocks per wave in flight
 // (88 registers instead of 38) 24 small tensors took 6.9 us instead of 4.7, ragged
-// 8-bit ones 26.1 instead of 24.2, and only fp32 states gained (96 -> 94).
+// 8-bit ones 26.1 instead of 24.2, and only fp32 states gained (96 -> 94); with two, the
+// second read before the first is worked on (56 registers), 5.0 instead of 4.5, 30.3
+// instead of 27.2, one block of fp32 states 112.6 instead of 110.4, and only eight of
+// 8-bit ones gained (541 -> 517).
 constexpr int kChunk = kNT / 64 * kBlock;
 
 // ------------------------------------------------------------------ the table
