@@ -240,23 +240,59 @@ struct KmArgs : Mm16Args {
   static constexpr int kOpB = kOpF16;
 };
 
-// fp32 sums over several launches and K splits: out[z] (+)= A B^T.  N % 16 == 0.
-struct AddArgs : Mm16Args {
+// What becomes of a gradient's sums: bf16(scale by_i / kGScale * sum), 0 in ignored rows
+// (without targets there are none).
+struct Finish {
+  uint16_t* out = nullptr;
+  int64_t ld = 0;
+  const float* scale = nullptr;  // one word, or none
+  const float* by = nullptr;     // one word, or one per row
+  int by_rows = 0, target_bits = 0;
+  const void* targets = nullptr;
+};
+__device__ __forceinline__ bool finish_row(const Finish& f, int64_t row, float& factor) {
+  factor = (f.scale ? *f.scale : 1.0f) * f.by[f.by_rows ? row : 0] * (1.0f / kGScale);
+  return !f.targets || load_target(f.targets, f.target_bits, row) >= 0;
+}
+__device__ __forceinline__ void finish4(const Finish& f, int64_t row, int64_t col, v4f v, bool counted, float factor) {
+  v = counted ? v * factor : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint2 w = bf16x4_rne(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<u32x2_any*>(f.out + row * f.ld + col) = u32x2_any{w.x, w.y};
+}
+
+// fp32 sums over several launches and K splits: out[z] (+)= A B^T, N % 16 == 0; without
+// `sums` they are all of it and finished here.
+template <int B> struct SumArgs : Mm16Args {
+  static constexpr int kOpB = B;
   static constexpr bool kTail = true;
   float* sums = nullptr;  // [batch][M, N]
   int first = 0;
+  Finish fin;
   template <int BM, int BN> static constexpr int extra_bytes() { return 0; }
-  template <int BM, int BN> __device__ static __forceinline__ void fetch(const AddArgs&, Rows&, int, int64_t, int64_t) {}
-  template <int BM, int BN> __device__ static __forceinline__ void park(const AddArgs&, const Rows&, int, uint8_t*) {}
+  template <int BM, int BN> __device__ static __forceinline__ void fetch(const SumArgs&, Rows&, int, int64_t, int64_t) {}
+  template <int BM, int BN> __device__ static __forceinline__ void park(const SumArgs&, const Rows&, int, uint8_t*) {}
   template <int BM, int BN, int WAVES_M, int WAVES_N, int TI, int TJ>
-  __device__ static __forceinline__ void tail(const AddArgs& p, const v4f (&acc)[TI][TJ], uint8_t*, const uint8_t*,
+  __device__ static __forceinline__ void tail(const SumArgs& p, const v4f (&acc)[TI][TJ], uint8_t*, const uint8_t*,
                                               int64_t m0, int64_t n0, int64_t bz) {
     constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wid / WAVES_N, wn = wid % WAVES_N;
-    float* const base = p.sums + bz * p.M * p.N + n0 + wn * WN + 4 * g;
     const int64_t cl = p.N - n0 - wn * WN;
     const int cols_in = cl < WN ? (int)cl : WN;
+    if (!p.sums) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        const int64_t row = m0 + wm * WM + 16 * i + r16;
+        if (row >= p.M) continue;
+        float factor;
+        const bool counted = finish_row(p.fin, row, factor);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          if (16 * j < cols_in) finish4(p.fin, row, n0 + wn * WN + 16 * j + 4 * g, acc[i][j], counted, factor);
+      }
+      return;
+    }
+    float* const base = p.sums + bz * p.M * p.N + n0 + wn * WN + 4 * g;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int64_t row = m0 + wm * WM + 16 * i + r16;
@@ -273,6 +309,9 @@ struct AddArgs : Mm16Args {
     }
   }
 };
+
+using AddArgs = SumArgs<kOpCodes>;   // G by rows, the codes K-major
+using KmSumArgs = SumArgs<kOpF16>;   // both K-major in fp16
 
 template <int BM, int BN, int WM_, int WN_, int MINB, int LAY, int DEEP, class P>
 static hipError_t launch_mm16_tile(const P& p0, hipStream_t st) {
@@ -304,8 +343,8 @@ static inline int pick16(int64_t M, int64_t N, int64_t batch, bool narrow) {
 // one epilogue each
 hipError_t launch_xent_lse(const XentLseArgs& p, hipStream_t st);
 hipError_t launch_xent_grad(const XentGradArgs& p, hipStream_t st);
-// G B into fp32 sums (G by rows, the codes K-major) and G^T A; either may be null.
-hipError_t launch_mm16_grads(const AddArgs* add, const KmArgs* km, hipStream_t st);
+// G B, and G^T A straight to its rows or, in K splits, into fp32 sums; any may be null.
+hipError_t launch_mm16_grads(const AddArgs* add, const KmArgs* km, const KmSumArgs* km_sums, hipStream_t st);
 int64_t xent_lse_tile(int64_t M, int64_t N);  // columns that share a row's statistics
 
 }  // namespace fp8mi

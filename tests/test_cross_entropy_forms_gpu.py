@@ -148,3 +148,54 @@ def test_more_logits_than_a_grid_holds():
     # of 2^-23 with its exponential's; lse and loss, below 16, round by 2^-21 at most
     for got, w in ((lse, want), (loss, want - logit)):
         assert (got.double() - w).abs().max() <= 256 * 2.0 ** -23 + 2 * 2.0 ** -21
+
+
+# many rows of few codes: G^T A in K splits, over one and over several pieces; sums that are complete at once
+SPLIT_SHAPES = [(300000, 1000, 32), (6000, 60, 1024), (3000, 300, 512), (1500, 1500, 768), (100000, 2, 16), (70000, 65, 48),
+                (1024, 1000, 16), (4097, 129, 272), (1023, 1, 16), (1025, 1500, 1040)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT_SHAPES)
+def test_splits_over_the_rows(M, N, K):
+    if N > 1:
+        return test_forms(M, N, K)
+    # A vocabulary of one: G = exp(l - lse) - 1 is 0 in truth, as are the gradients.  lse is l times ln 2 and is taken
+    # times log2 e again: with the two constants' roundings and the exponential's, fewer than 16 half steps of 1 + |l|, and
+    # |l| <= |a| |b|.  G's rounding to fp16 adds 2^-11 of it, the outputs' 2^-8 (together below a hundredth), dA is d G b and
+    # dB at most the sum of d |G| |a|.
+    a, b, t, sa, sb, g = operands(M, N, K, seed=M + N)
+    d = torch.rand(M, generator=g, device=DEV) + 0.1
+    loss, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb)
+    da, db = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
+    na = (a.view(E4M3).double() * sa.double()).norm(dim=1)
+    nb = (b.view(E4M3).double() * sb.double()).norm()
+    most = d.double() * 1.01 * 16 * U32 * (1 + na * nb)
+    assert (da.double().norm(dim=1) <= most * nb).all() and db.double().norm() <= (most * na).sum()
+
+
+@pytest.mark.parametrize("M,N,K", [(6000, 60, 1024), (1500, 1500, 768), (512, 2000, 1024), (100, 20000, 512)])
+def test_each_gradient_alone(M, N, K):
+    """Alone, a product may run in other tiles than beside the other: the sums' order is the same."""
+    a, b, t, sa, sb, g = operands(M, N, K, seed=5)
+    d = torch.rand(M, generator=g, device=DEV)
+    _, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb)
+    for dloss in (d, d[:1].clone()):
+        da, db = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, dloss, sa, sb)
+        assert torch.equal(da, fp8mi.fp8_cross_entropy_grad(a, b, t, lse, dloss, sa, sb, need_db=False)[0])
+        assert torch.equal(db, fp8mi.fp8_cross_entropy_grad(a, b, t, lse, dloss, sa, sb, need_da=False)[1])
+        wide = [torch.full((x.shape[0], K + 3), 7.0, dtype=torch.bfloat16, device=DEV) for x in (da, db)]
+        fp8mi.fp8_cross_entropy_grad(a, b, t, lse, dloss, sa, sb, da=wide[0][:, :K], db=wide[1][:, :K])
+        assert torch.equal(wide[0][:, :K], da) and torch.equal(wide[1][:, :K], db)
+        assert all((w[:, K:] == 7).all() for w in wide)
+
+
+def test_ignored_rows_of_complete_sums():
+    """A dloss that is NaN where the row is ignored, with sums finished by the product itself."""
+    a, b, t, sa, sb, g = operands(700, 200, 64, seed=6)
+    _, lse = fp8mi.fp8_cross_entropy(a, b, t, sa, sb)
+    d = torch.rand(700, generator=g, device=DEV)
+    want = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
+    d[t < 0] = float("nan")
+    a[t < 0] = 0x7F
+    got = fp8mi.fp8_cross_entropy_grad(a, b, t, lse, d, sa, sb)
+    assert all(torch.equal(x, y) for x, y in zip(want, got)) and not got[0][t < 0].any()
