@@ -184,8 +184,20 @@ hipError_t launch_widen(const Widen& a, uint32_t* ticket, hipStream_t st) {
 __global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const void* targets, int bits, int64_t M, float* out) {
   __shared__ float red[16];
   float m = 0.0f;
-  for (int64_t i = threadIdx.x; i < M; i += 1024)
-    if (load_target(targets, bits, i) >= 0) m = __builtin_elementwise_maximum(m, fabsf(dloss[i]));  // a NaN kept
+  constexpr int U = 8;  // rows in flight
+  for (int64_t i = threadIdx.x; i < M; i += U * 1024) {
+    int64_t t[U];
+    float d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = i + u * 1024;
+      t[u] = r < M ? load_target(targets, bits, r) : -1;
+      d[u] = r < M ? dloss[r] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t[u] >= 0) m = __builtin_elementwise_maximum(m, fabsf(d[u]));  // a NaN kept
+  }
   for (int off = 32; off > 0; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
