@@ -85,14 +85,19 @@ struct BackwardPlan {
     const int64_t tiles = (M + 255) / 256 * ((K + 191) / 192);
     splits = 256 / tiles;
     if (splits > cols / 512) splits = cols / 512;
+    // where those fill less than three quarters of the CUs, 256 tiles of 128 x 128, which
+    // run beside G^T A's in one round (the gradient of 2000 x 5000 x 256 71 -> 55 us, of 5536
+    // x 2680 x 192 84 -> 56)
+    const int64_t tiles128 = (M + 127) / 128 * ((K + 127) / 128);
+    if (tiles * splits < 192 && splits > 256 / tiles128) splits = 256 / tiles128;
     if (splits < 1) splits = 1;
-    // of G^T A over many rows, where a small vocabulary gives few tiles, to 256 workgroups
-    // and at least 512 rows each: 3000 x 300 x 512 both products 23.9 -> 11.1 us; the whole
+    // of G^T A over many rows, where a small vocabulary gives few tiles (of 64 x 64, or of
+    // 128 x 128 from 64 of those on), to 256 workgroups of at least 512 rows: 3000 x 300 x 512 both products 23.9 -> 11.1 us; the whole
     // gradient of 6000 x 60 x 1024 74 -> 34, of 1500 x 1500 x 768 (144 tiles of 128 x 128 for
     // 72) 60.8 -> 53.7
     const int64_t widest = N < cols ? N : cols, tiles_db = (widest + 63) / 64 * ((K + 63) / 64);
     const int64_t tiles_db128 = (widest + 127) / 128 * ((K + 127) / 128);
-    splits_db = tiles_db < 128 ? 256 / tiles_db : (tiles_db128 < 128 ? 256 / tiles_db128 : 1);
+    splits_db = tiles_db < 64 ? 256 / tiles_db : (tiles_db128 < 128 ? 256 / tiles_db128 : 1);
     if (splits_db > M / 512) splits_db = M / 512;
     if (splits_db < 1) splits_db = 1;
     ld = padded(K);

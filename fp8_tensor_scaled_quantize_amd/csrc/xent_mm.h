@@ -327,13 +327,15 @@ static hipError_t launch_mm16_tile(const P& p0, hipStream_t st) {
 
 // Tiles as pick_tile's: 256 x 256, or 256 x 192 where that needs less time, from
 // 60% of the CUs on, below that 128 x 128, then 64 x 64 (whose eight-stage form is no
-// faster here: 64 x 1000 x 512 logits 7.7 against 8.0 us, G B 6.8 against 6.3).
+// faster here: 64 x 1000 x 512 logits 7.7 against 8.0 us, G B 6.8 against 6.3).  The
+// gradients' products (`narrow`) of up to 128 rows take 128 x 128 at most: G B of 6 x 21489
+// x 2976 26.5 -> 22.0.
 static inline int pick16(int64_t M, int64_t N, int64_t batch, bool narrow) {
   // of an MI355X, not of the current device: the workspace's size goes by the tiles
   constexpr int64_t ncu = 256;
   const int64_t tm = (M + 255) / 256;
   const int64_t t256 = tm * ((N + 255) / 256) * batch, t192 = tm * ((N + 191) / 192) * batch;
-  if (10 * t256 >= 6 * ncu || (narrow && 10 * t192 >= 6 * ncu)) {
+  if ((!narrow || M > 128) && (10 * t256 >= 6 * ncu || (narrow && 10 * t192 >= 6 * ncu))) {
     if (!narrow) return 256;
     return (t192 + ncu - 1) / ncu * 230 < (t256 + ncu - 1) / ncu * 256 ? 192 : 256;
   }

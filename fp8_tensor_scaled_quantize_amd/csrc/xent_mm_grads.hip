@@ -46,7 +46,7 @@ template <class KM> static hipError_t launch_pair(const AddArgs* add, const KM* 
   if (add && km) {
     const int ta = pick16(add->M, add->N, add->batch, true);
     int tb = pick16(km->M, km->N, 1, true);
-    if (KM::kTail) tb = (km->M + 63) / 64 * ((km->N + 63) / 64) < 128 ? 64 : 128;  // as splits_db goes by
+    if (KM::kTail) tb = (km->M + 63) / 64 * ((km->N + 63) / 64) < 64 ? 64 : 128;  // as splits_db goes by
     if (ta == 64 && tb == 64) return launch_both<64>(*add, *km, st);
     if (ta <= 128 && tb <= 128) return launch_both<128>(*add, *km, st);
   }
