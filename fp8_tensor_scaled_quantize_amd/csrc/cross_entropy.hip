@@ -92,9 +92,9 @@ struct BackwardPlan {
     if (tiles * splits < 192 && splits > 256 / tiles128) splits = 256 / tiles128;
     if (splits < 1) splits = 1;
     // of G^T A over many rows, where a small vocabulary gives few tiles (of 64 x 64, or of
-    // 128 x 128 from 64 of those on), to 256 workgroups of at least 512 rows: 3000 x 300 x 512 both products 23.9 -> 11.1 us; the whole
-    // gradient of 6000 x 60 x 1024 74 -> 34, of 1500 x 1500 x 768 (144 tiles of 128 x 128 for
-    // 72) 60.8 -> 53.7
+    // 128 x 128 from 64 of those on), to 256 workgroups of at least 512 rows: 3000 x 300 x
+    // 512 both products 23.9 -> 11.1 us; the whole gradient of 6000 x 60 x 1024 74 -> 34, of
+    // 1500 x 1500 x 768 (144 tiles of 128 x 128 for 72) 60.8 -> 53.7
     const int64_t widest = N < cols ? N : cols, tiles_db = (widest + 63) / 64 * ((K + 63) / 64);
     const int64_t tiles_db128 = (widest + 127) / 128 * ((K + 127) / 128);
     splits_db = tiles_db < 64 ? 256 / tiles_db : (tiles_db128 < 128 ? 256 / tiles_db128 : 1);
