@@ -21,7 +21,8 @@ __all__ = ["E4M3", "E5M2", "F32", "F16", "BF16", "Fp8Error", "fp8_quantize", "fp
            "fp8_quantize_dynamic", "DYNAMIC_WORKSPACE_BYTES", "fp8_amax_fold", "fp8_mm", "fp8_mm_ex", "FP8_E4M3", "FP8_E5M2", "fp8_bias_grad", "fp8_bias_grad_workspace_bytes", "fp8_ring_seed", "new_ring", "ring_words", "version",
            "fp8_rmsnorm", "fp8_rmsnorm_grad", "fp8_rmsnorm_grad_workspace_bytes", "fp8_mm_act", "fp8_act_grad",
            "fp8_cross_entropy", "fp8_cross_entropy_grad", "fp8_cross_entropy_workspace_bytes",
-           "fp8_cross_entropy_grad_workspace_bytes", "fp8_adamw_step", "fp8_grad_norm", "ADAMW_BLOCK", "ADAMW_STEP_WORDS",
+           "fp8_cross_entropy_grad_workspace_bytes", "fp8_adamw_step", "fp8_grad_norm", "adamw_step", "grad_norm",
+           "ADAMW_BLOCK", "ADAMW_STEP_WORDS",
            "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_SILU", "interleave_gated"]
 
 E4M3, E5M2 = 0, 1
@@ -1071,3 +1072,8 @@ def fp8_grad_norm(grads, max_norm: float | None = None, out: torch.Tensor | None
     if status:
         _check(status)
     return out
+
+
+# The optimizer's calls take no fp8 operand (32-bit states, any gradients), and are
+# there without the prefix too.
+adamw_step, grad_norm = fp8_adamw_step, fp8_grad_norm
