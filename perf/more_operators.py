@@ -336,15 +336,15 @@ def _own_ce_grad(s):
 def _own_adamw(s):
     import fp8_tensor_scaled_quantize_amd as fp8mi
     s["steps"] += 1
-    fp8mi.fp8_adamw_step(s["params"], s["grads"], s["m"], s["v"], s["steps"], lr=LR, betas=(BETA1, BETA2), eps=EPS,
-                         weight_decay=DECAY, masters=s["masters"], exp_avg_scales=s["m_scales"],
-                         exp_avg_sq_scales=s["v_scales"], grad_scale=s["scale"], seed=SEED)
+    fp8mi.adamw_step(s["params"], s["grads"], s["m"], s["v"], s["steps"], lr=LR, betas=(BETA1, BETA2), eps=EPS,
+                     weight_decay=DECAY, masters=s["masters"], exp_avg_scales=s["m_scales"],
+                     exp_avg_sq_scales=s["v_scales"], grad_scale=s["scale"], seed=SEED)
     return _adamw_outputs(s)
 
 
 def _own_grad_norm(s):
     import fp8_tensor_scaled_quantize_amd as fp8mi
-    fp8mi.fp8_grad_norm(s["grads"], max_norm=MAX_NORM, out=s["norm"], clip_out=s["clip"])
+    fp8mi.grad_norm(s["grads"], max_norm=MAX_NORM, out=s["norm"], clip_out=s["clip"])
     return {"norm": s["norm"], "clip": s["clip"]}
 
 
