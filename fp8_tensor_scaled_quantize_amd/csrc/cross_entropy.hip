@@ -447,9 +447,11 @@ __global__ void __launch_bounds__(256) xent_join(const float2* parts, int64_t ti
   float l = 0.0f;
   if (seg == 0 && row < M) {
     const float2 all = red[0][r];
-    const float l2 = (all.x > -3.0e38f ? all.x : 0.0f) + log2f(all.y);
-    l = t < 0 ? 0.0f : (t < vocab ? (l2 - own) * kLn2 : __builtin_nanf(""));
-    lse[row] = l2 * kLn2;
+    // the loss from the largest logit's distance to the target's, which is exact, not from
+    // lse: a loss of 10^-5 beside logits of some hundreds would be lost in lse's rounding
+    const float top = all.x > -3.0e38f ? all.x : 0.0f, more = log2f(all.y);
+    l = t < 0 ? 0.0f : (t < vocab ? ((top - own) + more) * kLn2 : __builtin_nanf(""));
+    lse[row] = (top + more) * kLn2;
     loss[row] = l;
   }
   if (!mean) return;
