@@ -77,7 +77,7 @@ struct ForwardPlan {
 };
 
 struct BackwardPlan {
-  int64_t cols, splits, splits_db, ld, ld_g, scale, a16, a16d, g, sums, sums_db, bytes;
+  int64_t cols, splits, splits_db, ld, ld_g, unit, a16, a16d, g, sums, sums_db, bytes;
   BackwardPlan(int64_t M, int64_t N, int64_t K) {
     Carve c;
     cols = even_pieces(N, kPieceElements / M);
@@ -102,7 +102,7 @@ struct BackwardPlan {
     if (splits_db < 1) splits_db = 1;
     ld = padded(K);
     ld_g = padded(cols);
-    scale = c.take(4);
+    unit = c.take(4);
     a16 = c.take(M * ld * 2);
     a16d = c.take(M * ld * 2);
     g = c.take(M * ld_g * 2);
@@ -122,7 +122,7 @@ struct Widen {
   int32_t row_chunks;
   int target_bits;
   const void* targets;
-  const float* rows;           // [R], times 1 / *rows_by
+  const float* rows;           // [R], in units of *rows_by (row_lift)
   const float* rows_by;
   uint16_t* out_scaled;
 };
@@ -154,7 +154,7 @@ __device__ __forceinline__ void widen_group(const Widen& m, int64_t group) {
     q[1] = u32x4{w[4], w[5], w[6], w[7]};
     if (m.out_scaled) {
       const bool counted = load_target(m.targets, m.target_bits, row[u]) >= 0;
-      const float f = counted ? m.rows[row[u]] / *m.rows_by : 0.0f;
+      const float d = counted ? m.rows[row[u]] : 0.0f, f = d / *m.rows_by * row_lift(d, *m.rows_by);
       float t[16];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -184,9 +184,10 @@ hipError_t launch_widen(const Widen& a, uint32_t* ticket, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The power of two at or above the largest |dloss| of the counted rows: dB's rows of
-// A carry dloss over it, which fp16 holds (1 where that is no normal number).
-__global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const void* targets, int bits, int64_t M, float* out) {
+// The unit of the rows' loss gradients (row_lift): the power of two that puts the largest
+// |dloss| of the counted rows into [2^6, 2^7), 2^-100 at least (a smaller one would leave
+// fp32 in dB's factor), 1 where the largest is not finite.
+__global__ void __launch_bounds__(1024) dloss_unit(const float* dloss, const void* targets, int bits, int64_t M, float* out) {
   __shared__ float red[16];
   float m = 0.0f;
   constexpr int U = 8;  // rows in flight
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(1024) dloss_scale(const float* dloss, const vo
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int k = 1; k < 16; ++k) m = __builtin_elementwise_maximum(m, red[k]);
-  const uint32_t exp = __float_as_uint(m) & 0x7F800000u;
-  *out = exp > 0u && exp < 0x7F000000u ? __uint_as_float(exp + 0x00800000u) : 1.0f;
+  const uint32_t exp = __float_as_uint(m) >> 23;
+  *out = exp < 255u ? __uint_as_float((exp < 33u ? 27u : exp - 6u) << 23) : 1.0f;
 }
 
 // Few rows (scoring while serving): bound by reading the weights once.  A workgroup
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(256) xent_rows(XentArgs p, G extra, uint32_t c
   }
   if constexpr (G::kGrad) {  // as XentGradArgs: groups of eight columns, those past the vocabulary as zeros
     if (!in) return;
-    const float lse = t < p.vocab ? p.lse[row] * kLog2e : __builtin_nanf("");
+    const float lse = t < p.vocab ? p.lse[row] * kLog2e : __builtin_nanf(""), scale = XentArgs::g_scale(p, row);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int64_t at = n0 + 16 * j + 4 * g;
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(256) xent_rows(XentArgs p, G extra, uint32_t c
       for (int e = 0; e < 4; ++e) {
         float q = __builtin_amdgcn_exp2f(x[j][e] - lse);
         if (p.v0 + at + e == t) q -= 1.0f;
-        v[e] = t < 0 || at + e >= p.N ? 0.0f : q * kGScale;
+        v[e] = t < 0 || at + e >= p.N ? 0.0f : q * scale;
       }
       uint32_t w[2];
       pack_f16<4>(w, v);
@@ -637,11 +638,12 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   const BackwardPlan plan(c.M, c.N, c.K);
   const auto at = [&](int64_t off) { return reinterpret_cast<uint16_t*>(c.ws + off); };
   float* const sums = reinterpret_cast<float*>(c.ws + plan.sums);
-  // with a loss gradient per row, dB takes A's rows times theirs
+  // with a loss gradient per row, dB takes A's rows times theirs, and G's rows share their
+  // range (dA alone too: it is the same with dB and without)
   const bool scaled = c.db && c.dloss_rows;
-  float* const scale = reinterpret_cast<float*>(c.ws + plan.scale);
-  if (scaled) {
-    hipLaunchKernelGGL(dloss_scale, dim3(1), dim3(1024), 0, st, c.dloss, c.targets, c.target_bits, c.M, scale);
+  float* const unit = reinterpret_cast<float*>(c.ws + plan.unit);
+  if (c.dloss_rows) {
+    hipLaunchKernelGGL(dloss_unit, dim3(1), dim3(1024), 0, st, c.dloss, c.targets, c.target_bits, c.M, unit);
     FP8MI_TRY(hipGetLastError());
   }
   Widen rows = widen(c.a, c.lda, c.M, c.K, at(plan.a16), plan.ld);
@@ -649,7 +651,7 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   rows.target_bits = c.target_bits;
   if (scaled) {
     rows.rows = c.dloss;
-    rows.rows_by = scale;
+    rows.rows_by = unit;
     rows.out_scaled = at(plan.a16d);
   }
   const int64_t most = offset_columns(c.ldb), cols = plan.cols <= most ? plan.cols : even_pieces(c.N, most);
@@ -665,6 +667,7 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
   sum_a.sums = sums; sum_a.splits = splits;
   sum_a.fin.out = c.da; sum_a.fin.ld = c.ld_da;
   sum_a.fin.scale = c.b_scale_inv; sum_a.fin.by = c.dloss; sum_a.fin.by_rows = c.dloss_rows;
+  sum_a.fin.unit = c.dloss_rows ? unit : nullptr;
   sum_a.fin.targets = c.targets; sum_a.fin.target_bits = c.target_bits;
   // by the whole vocabulary, as in the forward pass: a narrow last piece's logits
   // then add up in the order of the others, and of those that made lse
@@ -674,6 +677,7 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
     XentGradArgs g;
     g.lse = c.lse;
     g.d = at(plan.g); g.ld_d = plan.ld_g;
+    g.dloss = c.dloss_rows ? c.dloss : nullptr; g.unit = unit;
     if (from_codes) {  // the logits straight from the codes, beside the widening of A
       if (v0 > 0) rows.chunks = 0;
       fill_rows(g, c, v0, n);
@@ -720,13 +724,13 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t st) {
       if (c.db) {
         sum_b.sums = km.sums; sum_b.splits = km.batch; sum_b.count = n * c.K;
         sum_b.fin.out = c.db + v0 * c.ld_db; sum_b.fin.ld = c.ld_db;
-        sum_b.fin.scale = c.a_scale_inv; sum_b.fin.by = scaled ? scale : c.dloss;
+        sum_b.fin.scale = c.a_scale_inv; sum_b.fin.by = scaled ? unit : c.dloss;
       }
     } else {
       KmArgs km;
       fill_km(km);
       km.a_scale_inv = c.a_scale_inv;
-      km.b_scale_inv = scaled ? scale : c.dloss;
+      km.b_scale_inv = scaled ? unit : c.dloss;
       km.c = c.db + v0 * c.ld_db; km.ldc = c.ld_db; km.stride_c = 0;
       FP8MI_TRY(launch_mm16_grads(c.da ? &add : nullptr, c.db ? &km : nullptr, nullptr, st));
     }

@@ -27,6 +27,19 @@ __device__ __forceinline__ int tile_target(int64_t t, int64_t v0, int64_t n) {
 
 constexpr float kGScale = 16384.0f;
 
+// With a loss gradient per row, G^T A takes A's rows times theirs over `unit`, the power of
+// two that puts the largest |dloss| of the batch into [2^6, 2^7) (448 of that is below
+// fp16's 65504).  A row below 2^-14 of the unit, 2^-20 of the largest, would leave fp16's
+// normal numbers: up to 2^8 of it go to A's row, and G's row is that much smaller (its
+// entries' rounding, 2^-39 of 1 in all, 2^-31 at most) until dA's sums are finished.  So a
+// row of 2^-28 of the largest still enters dB with 11 bits of a code of 1.  (Without either
+// a row of 10^-8 of the largest was zero in dB up to codes of 4.)
+__device__ __forceinline__ float row_lift(float dloss, float unit) {  // 2^0 .. 2^8
+  const int e = (int)((__float_as_uint(dloss) >> 23) & 255u) - (int)(__float_as_uint(unit) >> 23);  // exponent of dloss / unit
+  const int up = -14 - e;
+  return __uint_as_float((uint32_t)(127 + (up < 0 ? 0 : (up > 8 ? 8 : up))) << 23);
+}
+
 // A in fp16, B's codes as they are (kOpB; or fp16): fp16 leading dimensions, and K and
 // strides of A, in bytes.  Batch z takes bytes z K .. of a row-major A's rows (the last
 // batch fewer), and the rows z K / 2 .. of a K-major operand's k_major_rows.
@@ -59,12 +72,17 @@ struct XentArgs : Mm16Args {
   const float* lse = nullptr;       // [M]
   uint16_t* d = nullptr;            // fp16 [M, ld_d]
   int64_t ld_d = 0;
+  const float* dloss = nullptr;     // [M] where rows have their own (row_lift), else null
+  const float* unit = nullptr;
+  __device__ static __forceinline__ float g_scale(const XentArgs& p, int64_t row) {
+    return p.dloss ? kGScale / row_lift(p.dloss[row], *p.unit) : kGScale;
+  }
 
   struct Rows {
-    float col = 1.0f, row = 1.0f;
+    float col = 1.0f, row = 1.0f, scale = kGScale;
     int target = kTargetElsewhere;
   };
-  template <int BM, int BN> static constexpr int extra_bytes() { return 4 * BN + 8 * BM; }
+  template <int BM, int BN> static constexpr int extra_bytes() { return 4 * BN + 12 * BM; }
   template <int BM, int BN, bool GRAD>
   __device__ static __forceinline__ void fetch_rows(const XentArgs& p, Rows& r, int tid, int64_t m0, int64_t n0) {
     if (p.b_scale_inv && tid < BN) r.col = p.b_scale_inv[p.b_rows ? (n0 + tid < p.N ? n0 + tid : n0) : 0];
@@ -73,17 +91,19 @@ struct XentArgs : Mm16Args {
     r.target = tile_target(t, p.v0 + n0, p.N - n0 < BN ? p.N - n0 : BN);
     if constexpr (GRAD) {
       r.row = t < p.vocab ? p.lse[m0 + tid] * kLog2e : __builtin_nanf("");
+      r.scale = g_scale(p, m0 + tid);
     } else {
       if (p.a_rows) r.row = p.a_scale_inv[m0 + tid];
     }
   }
-  // extra: column scales [BN], row words [BM], targets [BM]
+  // extra: column scales [BN], row words [BM], targets [BM], G's scales [BM]
   template <int BM, int BN> __device__ static __forceinline__ void park(const XentArgs&, const Rows& r, int tid, uint8_t* extra) {
     float* f = reinterpret_cast<float*>(extra);
     if (tid < BN) f[tid] = r.col;
     if (tid < BM) {
       f[BN + tid] = r.row;
       reinterpret_cast<int*>(f)[BN + BM + tid] = r.target;
+      f[BN + 2 * BM + tid] = r.scale;
     }
   }
 };
@@ -181,7 +201,7 @@ struct XentLseArgs : XentArgs {
   }
 };
 
-// kGScale (exp(l - lse) - [target]) in fp16, rows of the gradient's two products.
+// g_scale (exp(l - lse) - [target]) in fp16, rows of the gradient's two products.
 struct XentGradArgs : XentArgs {
   template <int BM, int BN>
   __device__ static __forceinline__ void fetch(const XentArgs& p, Rows& r, int tid, int64_t m0, int64_t n0) {
@@ -204,7 +224,7 @@ struct XentGradArgs : XentArgs {
     for (int i = 0; i < TI; ++i) {
       const int lr = wm * WM + 16 * i + r16;
       const bool in = m0 + lr < p.M;
-      const float lse = rows[lr];
+      const float lse = rows[lr], scale = rows[2 * BM + lr];
       const int own = tgt[lr] - wn * WN;
       const bool ignored = tgt[lr] == kTargetIgnored;
       uint16_t* const out = p.d + (m0 + lr) * p.ld_d + n0 + wn * WN;
@@ -217,7 +237,7 @@ struct XentGradArgs : XentArgs {
         for (int e = 0; e < C; ++e) {
           float q = __builtin_amdgcn_exp2f(fmaf(t[e], s, -lse));
           if (own == at + e) q -= 1.0f;
-          t[e] = ignored ? 0.0f : q * kGScale;
+          t[e] = ignored ? 0.0f : q * scale;
         }
         if (cols_in < WN) {
 #pragma unroll
@@ -241,17 +261,20 @@ struct KmArgs : Mm16Args {
 };
 
 // What becomes of a gradient's sums: bf16(scale by_i / kGScale * sum), 0 in ignored rows
-// (without targets there are none).
+// (without targets there are none); with `unit` by_i are loss gradients whose rows of G
+// row_lift made smaller.
 struct Finish {
   uint16_t* out = nullptr;
   int64_t ld = 0;
   const float* scale = nullptr;  // one word, or none
   const float* by = nullptr;     // one word, or one per row
+  const float* unit = nullptr;
   int by_rows = 0, target_bits = 0;
   const void* targets = nullptr;
 };
 __device__ __forceinline__ bool finish_row(const Finish& f, int64_t row, float& factor) {
-  factor = (f.scale ? *f.scale : 1.0f) * f.by[f.by_rows ? row : 0] * (1.0f / kGScale);
+  const float by = f.by[f.by_rows ? row : 0], lift = f.unit ? row_lift(by, *f.unit) : 1.0f;
+  factor = (f.scale ? *f.scale : 1.0f) * (by * (lift / kGScale));
   return !f.targets || load_target(f.targets, f.target_bits, row) >= 0;
 }
 __device__ __forceinline__ void finish4(const Finish& f, int64_t row, int64_t col, v4f v, bool counted, float factor) {

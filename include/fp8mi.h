@@ -500,8 +500,12 @@ FP8MI_API size_t fp8_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t
  *   G(i,j) = exp(l(i,j) - lse_i) - [j = t_i]      rounded to fp16 (2^-11, or 2^-39 in all);
  *            0 for an ignored row, NaN for one whose target is N or more
  *   da(i,k) = sb dloss_i sum_j G(i,j) dec(B(j,k))         fp32 sums, one bf16 rounding
- *   db(j,k) = sa sum_i dloss_i G(i,j) dec(A(i,k))         (dloss_i A rounded to fp16 where
- *            there is one per row); the codes and dloss of ignored rows are not used
+ *   db(j,k) = sa sum_i dloss_i G(i,j) dec(A(i,k))         the codes and dloss of ignored rows
+ *            are not used
+ * With one dloss per row, dloss_i dec(A) is rounded to fp16 for db: by 2^-11, or by 2^-39 of
+ * the largest |dloss| of the counted rows (per unit of a code, sa apart) in all, so a row of
+ * 10^-8 of that keeps its precision and one of 10^-12 is lost; G of a row below 2^-20 of it
+ * is rounded by up to 2^-31 in all, in da too.
  * Arguments as fp8_cross_entropy, with one scale per operand (the two factors leave the
  * sums), and
  *   lse        device fp32 [M]: the forward call's.

@@ -8,7 +8,7 @@ import train_ref as R
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-U32 = 2.0 ** -24
+HALF, U32 = 2.0 ** -8, 2.0 ** -24
 
 
 def code(x):
@@ -53,3 +53,63 @@ def test_loss_of_a_confident_token(M, N, top):
     assert (np.abs(f64(loss) - want) <= err).all(), (np.abs(f64(loss) - want) / err).max()
     assert abs(float(mean[0]) - want.mean()) <= err.max() + U32
     assert (np.abs(f64(lse) - (own + want)) <= 8 * U32 * (own + 1) + err).all()
+
+
+# rows straight from the codes, the same in K splits of G^T A, tiles, tiles in K splits
+@pytest.mark.parametrize("M,N", [(40, 300), (1030, 700), (300, 3000), (1500, 600)])
+@pytest.mark.parametrize("size", [1.0, 1e-25, 1e25])
+def test_rows_of_little_weight(M, N, size):
+    """Vocabulary rows whose gradient comes from a single row of small dloss: each is
+    the formula's by itself, whatever the batch's largest dloss."""
+    ratios = [1e-5, 1e-7, 1e-8, 1e-9]
+    Q, S, K = len(ratios), 16, 128
+    rng = np.random.default_rng(M)
+    a, b = (torch.from_numpy(rng.integers(0x28, 0x70, (n, K)) | (rng.integers(0, 2, (n, K)) << 7)).to(torch.uint8)
+            for n in (M, N))  # magnitudes of 2^-2 to 2^7
+    low, high = int(code(-448.0)), int(code(448.0))
+    # S columns of K for each small row q: only it has no -448 there, and only the vocabulary's row q has 448
+    a[:, :Q * S] = low
+    b[:, :Q * S] = 0
+    for q in range(Q):
+        a[5 + q, q * S:(q + 1) * S] = 0
+        b[9 + q] = 0
+        b[9 + q, q * S:(q + 1) * S] = high
+    t = torch.randint(9 + Q, N, (M,))
+    t[5:5 + Q] = 9 + torch.arange(Q)
+    sa, sb = np.float32(2.0 ** -7), np.float32(2.0 ** -7)  # those columns: -196 elsewhere
+    d = torch.rand(M) * 0.5 + 0.5
+    d[5:5 + Q] = torch.tensor(ratios)
+    d *= size
+    args = [x.to(DEV) for x in (a, b, t)]
+    scales = [torch.tensor([s], device=DEV) for s in (sa, sb)]
+    _, lse = fp8mi.fp8_cross_entropy(*args, *scales)
+    da, db = fp8mi.fp8_cross_entropy_grad(*args, lse, d.to(DEV), *scales)
+    A, B = R.decode_e4m3(a.numpy()), R.decode_e4m3(b.numpy())
+    l = (A @ B.T) * (float(sa) * float(sb))
+    el = (np.abs(A) @ np.abs(B).T) * float(sa) * float(sb) * K * 2 * U32 + 4 * U32 * np.abs(l)
+    p = np.exp(l - f64(lse)[:, None])
+    G = p.copy()
+    G[np.arange(M), t.numpy()] -= 1
+    w, most = d.double().numpy(), float(d.max())
+    # G before its rounding (the argument's errors), then fp16's half step or the smallest one, which a row of little
+    # weight has up to 2^8 times larger
+    eg = p * (el + 4 * U32 * (np.abs(l) + np.abs(f64(lse))[:, None]) + 4 * U32) + 2 * U32 * np.abs(G)
+    eg = eg + 2.0 ** -11 * (np.abs(G) + eg) + np.where(w < most * 2.0 ** -20, 2.0 ** -31, 2.0 ** -39)[:, None]
+    for q in range(Q):
+        i, j = 5 + q, 9 + q
+        rest = np.delete(p[:, j], i).max()
+        assert rest < 1e-30  # the row is alone
+        x = w[i] * float(sa) * A[i]
+        want = G[i, j] * x
+        # dloss A in fp16: half a step, or 2^-39 of the largest dloss per unit of a code
+        ex = 2.0 ** -11 * np.abs(x) + 2.0 ** -39 * most * float(sa)
+        err = np.abs(G[i, j]) * ex + eg[i, j] * (np.abs(x) + ex) + (M + 8) * 2 * U32 * np.abs(want)
+        got = f64(db[j])
+        assert (np.abs(got - want) <= err + HALF * (np.abs(want) + err)).all(), (q, np.abs(got - want).max() / np.abs(want).max())
+        assert np.linalg.norm(got - want) <= 0.02 * np.linalg.norm(want)
+    dwant = w[:, None] * float(sb) * (G @ B)
+    derr = w[:, None] * float(sb) * (eg @ np.abs(B) + (N + 8) * 2 * U32 * (np.abs(G) @ np.abs(B)))
+    assert (np.abs(f64(da) - dwant) <= derr + HALF * (np.abs(dwant) + derr)).all()
+    # alone, each is the same
+    assert torch.equal(da, fp8mi.fp8_cross_entropy_grad(*args, lse, d.to(DEV), *scales, need_db=False)[0])
+    assert torch.equal(db, fp8mi.fp8_cross_entropy_grad(*args, lse, d.to(DEV), *scales, need_da=False)[1])
