@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from . import ADAMW_BLOCK, ADAMW_STEP_WORDS, fp8_adamw_step, fp8_grad_norm
+from . import (ADAMW_BLOCK, ADAMW_STEP_WORDS, _all_on_device, _dtypes, _flat, _numel, fp8_adamw_step, fp8_grad_norm)
 
 
 class AdamW:
@@ -22,7 +22,11 @@ class AdamW:
     and a step whose gradients are not finite is skipped (without a look from the
     host: `steps` counts it all the same, the device's count does not).
     capturable: the step's number and lr are device words (lr_word), so that a
-    captured step goes on."""
+    captured step goes on.
+
+    Each param counts its own steps, those that had a gradient for it, and its bias
+    corrections go by them.  Params that had theirs in the same steps are updated in
+    one call, and any others in a call for each such group."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
                  state_bits: int = 32, masters: bool = True, max_norm: float | None = None, capturable: bool = False,
@@ -45,8 +49,12 @@ class AdamW:
         self.exp_avg_scale, self.exp_avg_sq_scale = (
             [torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=dev) if state_bits == 8 else None for p in self.params]
             for _ in range(2))
-        self.steps = 0
-        self.step_words = torch.zeros(ADAMW_STEP_WORDS, dtype=torch.int32, device=dev) if capturable else None
+        # groups of params with one count, ascending: it is at the first param's place
+        self._groups = [list(range(n))]
+        self._counts = [0] * n  # steps issued from the host
+        self._words = torch.zeros(n, ADAMW_STEP_WORDS, dtype=torch.int32, device=dev) if capturable else None
+        self.step_words = None if self._words is None else self._words[0]  # the first param's
+        self._captured = set()  # the groups of captured steps, by their first params: they stay together
         self.lr_word = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)  # of the latest step's gradients, with max_norm
         self._clip = torch.empty_like(self.norm)
@@ -55,31 +63,89 @@ class AdamW:
         for p in self.params:
             p.grad = None
 
+    @property
+    def steps(self) -> int:
+        """The most steps that a param has had."""
+        return max(self._counts)
+
+    @steps.setter
+    def steps(self, count: int) -> None:
+        self._set_counts([int(count)] * len(self.params))
+
+    def _regroup(self, counts) -> list:
+        """The groups for new counts."""
+        kept = [g for g in self._groups if g[0] in self._captured]
+        rest = sorted(i for g in self._groups if g[0] not in self._captured for i in g)
+        if any(len({counts[i] for i in g}) > 1 for g in kept):
+            raise ValueError("these step counts differ among params that a captured step counts together")
+        return kept + [[i for i in rest if counts[i] == c] for c in dict.fromkeys(counts[i] for i in rest)]
+
+    def _set_counts(self, counts) -> None:
+        self._groups, self._counts = self._regroup(counts), list(counts)
+        if self._words is not None:
+            self._words.copy_(torch.tensor([[c] + [0] * (ADAMW_STEP_WORDS - 1) for c in counts], dtype=torch.int32))
+
+    def _parted(self, have):
+        """The groups, those parted of which some params have a gradient and some have
+        none, and where such parts' counts come from and go to."""
+        parts, moved = [], []
+        for g in self._groups:
+            yes, no = [i for i in g if i in have], [i for i in g if i not in have]
+            parts += [p for p in (yes, no) if p]
+            if yes and no:
+                moved.append((g[0], no[0] if yes[0] == g[0] else yes[0]))
+                # (a count of 0 needs no copy, so a first step may be captured with some gradients missing)
+                if self._words is not None and self._counts[g[0]] and (g[0] in self._captured or
+                                                                       torch.cuda.is_current_stream_capturing()):
+                    raise RuntimeError("a captured step keeps the params that were updated together: these gradients "
+                                       "are there for a part of them (run one such step before the capture)")
+        return parts, moved
+
     def step(self, grads=None) -> None:
         """One step with the given gradients, or the params' own; a param whose
-        gradient is None is left as it is."""
+        gradient is None is left as it is, and does not count the step."""
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
         at = [i for i, g in enumerate(grads) if g is not None]
         if not at:
             return
-        grads = [grads[i].contiguous() for i in at]
-
-        def pick(ts):
-            return [ts[i] for i in at]
-
+        for i in at:
+            grads[i] = grads[i].contiguous()
+        given, have = [grads[i] for i in at], set(at)
+        groups, moved = (self._groups, ()) if len(at) == len(grads) else self._parted(have)
+        active = [g for g in groups if g[0] in have]
+        if len(active) > 1:  # several calls: what one of them would refuse, before the first has run
+            params = [self.params[i] for i in at]
+            _flat(params, "params")
+            _flat(given, "grads", list(map(_numel, params)))
+            _dtypes(params, "params"), _dtypes(given, "grads")
+            _all_on_device(params, given)
+            filled = [p.data_ptr() for p in params if p.numel()]
+            if len(set(filled)) != len(filled):
+                raise ValueError("the same param is there twice")
         scale = None
         if self.max_norm is not None:
-            fp8_grad_norm(grads, self.max_norm, out=self.norm, clip_out=self._clip)
+            fp8_grad_norm(given, self.max_norm, out=self.norm, clip_out=self._clip)
             scale = self._clip
-        device = self.step_words is not None
-        fp8_adamw_step(pick(self.params), grads, pick(self.exp_avg), pick(self.exp_avg_sq),
-                       self.step_words if device else self.steps + 1, self.lr_word if device else self.lr, self.betas,
-                       self.eps, pick(self.weight_decay), pick(self.masters), pick(self.exp_avg_scale),
-                       pick(self.exp_avg_sq_scale), scale, self.seed)
-        if not device:
-            self.steps += 1
+        for a, b in moved:
+            if self._counts[a] and self._words is not None:
+                self._words[b].copy_(self._words[a])
+            self._counts[b] = self._counts[a]
+        self._groups = groups
+        device = self._words is not None
+        for g in active:
+            def pick(ts):
+                return ts if len(g) == len(ts) else [ts[i] for i in g]
+
+            fp8_adamw_step(pick(self.params), pick(grads), pick(self.exp_avg), pick(self.exp_avg_sq),
+                           self._words[g[0]] if device else self._counts[g[0]] + 1, self.lr_word if device else self.lr,
+                           self.betas, self.eps, pick(self.weight_decay), pick(self.masters),
+                           pick(self.exp_avg_scale), pick(self.exp_avg_sq_scale), scale, self.seed)
+            if device and torch.cuda.is_current_stream_capturing():
+                self._captured.add(g[0])
+            for i in g:
+                self._counts[i] += 1
 
     def sync_masters(self) -> None:
         """Take the masters from the params anew (after a param was loaded or set)."""
@@ -88,22 +154,31 @@ class AdamW:
                 m.copy_(p.detach())
 
     def state_dict(self) -> dict:
-        steps = self.steps if self.step_words is None else int(self.step_words[0])
-        return {"steps": steps, "masters": self.masters, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
-                "exp_avg_scale": self.exp_avg_scale, "exp_avg_sq_scale": self.exp_avg_sq_scale}
+        counts = list(self._counts)
+        if self._words is not None:
+            words = self._words[:, 0].tolist()
+            for g in self._groups:
+                for i in g:
+                    counts[i] = words[g[0]]
+        return {"steps": max(counts), "param_steps": counts, "masters": self.masters, "exp_avg": self.exp_avg,
+                "exp_avg_sq": self.exp_avg_sq, "exp_avg_scale": self.exp_avg_scale,
+                "exp_avg_sq_scale": self.exp_avg_sq_scale}
 
     def load_state_dict(self, state: dict) -> None:
         """Fill the states from another optimizer's over the same params (same
-        state_bits and masters), in place."""
+        state_bits and masters), in place.  A state without "param_steps" has one
+        count, "steps", for all."""
         for name in ("masters", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
             mine, theirs = getattr(self, name), state[name]
             if [None if t is None else (t.numel(), t.dtype) for t in mine] != \
                     [None if t is None else (t.numel(), t.dtype) for t in theirs]:
                 raise ValueError(f"the state's {name} do not fit these params")
+        counts = [int(c) for c in state.get("param_steps", [state["steps"]] * len(self.params))]
+        if len(counts) != len(self.params):
+            raise ValueError("the state's param_steps do not fit these params")
+        self._regroup(counts)  # refuses what it refuses before anything is written
         for name in ("masters", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
             for a, b in zip(getattr(self, name), state[name]):
                 if a is not None:
                     a.copy_(b.reshape(a.shape))
-        self.steps = int(state["steps"])
-        if self.step_words is not None:
-            self.step_words[0] = self.steps
+        self._set_counts(counts)
