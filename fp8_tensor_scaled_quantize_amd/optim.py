@@ -37,6 +37,7 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
         self.lr, self.betas, self.eps, self.max_norm, self.seed = lr, betas, eps, max_norm, seed
+        self.state_bits = state_bits
         n = len(self.params)
         self.weight_decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
         if len(self.weight_decay) != n:
@@ -55,6 +56,7 @@ class AdamW:
         self._words = torch.zeros(n, ADAMW_STEP_WORDS, dtype=torch.int32, device=dev) if capturable else None
         self.step_words = None if self._words is None else self._words[0]  # the first param's
         self._captured = set()  # the groups of captured steps, by their first params: they stay together
+        self._none = torch.empty(0, dtype=torch.float32, device=dev)  # stands for a param without a gradient
         self.lr_word = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)  # of the latest step's gradients, with max_norm
         self._clip = torch.empty_like(self.norm)
@@ -135,13 +137,20 @@ class AdamW:
         self._groups = groups
         device = self._words is not None
         for g in active:
-            def pick(ts):
-                return ts if len(g) == len(ts) else [ts[i] for i in g]
+            inside = set(g)
+
+            def pick(ts, other=self._none):
+                if len(g) == len(ts):
+                    return ts
+                if self.state_bits == 32:
+                    return [ts[i] for i in g]
+                # 8-bit states are rounded by a tensor's place: those of other groups keep theirs
+                return [t if i in inside else other for i, t in enumerate(ts)]
 
             fp8_adamw_step(pick(self.params), pick(grads), pick(self.exp_avg), pick(self.exp_avg_sq),
                            self._words[g[0]] if device else self._counts[g[0]] + 1, self.lr_word if device else self.lr,
-                           self.betas, self.eps, pick(self.weight_decay), pick(self.masters),
-                           pick(self.exp_avg_scale), pick(self.exp_avg_sq_scale), scale, self.seed)
+                           self.betas, self.eps, pick(self.weight_decay, 0.0), pick(self.masters, None),
+                           pick(self.exp_avg_scale, None), pick(self.exp_avg_sq_scale, None), scale, self.seed)
             if device and torch.cuda.is_current_stream_capturing():
                 self._captured.add(g[0])
             for i in g:

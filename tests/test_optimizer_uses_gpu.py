@@ -43,9 +43,10 @@ def test_a_late_param_counts_its_own_steps(bits, capturable):
     assert opt.state_dict()["param_steps"] == [204, 3, 4] and other.state_dict()["param_steps"] == [204, 3, 4]
 
 
-@pytest.mark.parametrize("bits", [32])
+@pytest.mark.parametrize("bits", [32, 8])
 def test_each_param_as_if_it_were_alone(bits):
-    """Whether the others have gradients changes nothing in a param's own steps."""
+    """Whether the others have gradients changes nothing in a param's own steps, the
+    8-bit states' random numbers among them."""
     pattern = [(0, 1, 2), (1, 2), (0, 2), (2,), (1,), (0, 1, 2), (0, 1)]
     p = [rand(700 + i, i, torch.bfloat16) for i in range(3)]
     opt = AdamW(p, lr=1e-2, state_bits=bits, seed=5)
