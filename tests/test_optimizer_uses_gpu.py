@@ -1,7 +1,9 @@
-"""AdamW over params whose gradients are not always there."""
+"""AdamW over params whose gradients are not always there, and a captured step's
+8-bit states."""
 import pytest
 import torch
 
+import fp8_tensor_scaled_quantize_amd as fp8mi
 from fp8_tensor_scaled_quantize_amd.optim import AdamW
 
 pytestmark = pytest.mark.gpu
@@ -134,3 +136,44 @@ def test_a_bad_gradient_of_one_group_stops_all():
         with pytest.raises(ValueError):
             opt.step([rand(300, 3), bad])
         assert torch.equal(p[0], kept[0]) and opt.state_dict()["param_steps"] == [1, 0]
+
+
+def test_captured_8_bit_states_are_the_eager_ones():
+    """Codes and scales go by the gradients, the seed, the step and the clip alone: a
+    replayed step's are an eager one's, bit for bit.  Weights: lr's quotient
+    and the corrections in fp32 from the device's or the host's fp64, a rounding or
+    two of the update apart."""
+    def make():
+        w = [rand(n, 7 + n) * 0.05 for n in (5000, 77)]
+        return dict(w=w, p=[t.to(torch.bfloat16) for t in w], g=[rand(t.numel(), 9, torch.bfloat16) for t in w],
+                    m=[torch.zeros(t.numel(), dtype=torch.uint8, device=DEV) for t in w],
+                    v=[torch.zeros(t.numel(), dtype=torch.uint8, device=DEV) for t in w],
+                    ms=[torch.zeros(-(-t.numel() // 256), device=DEV) for t in w],
+                    vs=[torch.zeros(-(-t.numel() // 256), device=DEV) for t in w])
+
+    def run(s, step, lr, clip):
+        fp8mi.fp8_adamw_step(s["p"], s["g"], s["m"], s["v"], step, lr=lr, betas=(0.9, 0.95), weight_decay=0.1,
+                             masters=s["w"], exp_avg_scales=s["ms"], exp_avg_sq_scales=s["vs"], grad_scale=clip, seed=3)
+
+    a, b = make(), make()
+    words = torch.zeros(fp8mi.ADAMW_STEP_WORDS, dtype=torch.int32, device=DEV)
+    lr, clip = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(a, words, lr, clip)
+    for t in range(1, 5):
+        lr.fill_(3e-3 * t)
+        clip.fill_(0.5 if t % 2 else 2.0)
+        before = [w.clone() for w in b["w"]]
+        graph.replay()
+        torch.cuda.synchronize()
+        run(b, t, float(lr), clip)
+        assert int(words[0]) == t
+        for name in ("m", "v", "ms", "vs"):
+            assert all(torch.equal(x, y) for x, y in zip(a[name], b[name])), name
+        for x, y, w, px, py in zip(a["w"], b["w"], before, a["p"], b["p"]):
+            assert not torch.equal(y, w)  # there was a step
+            # the step's factors differ by a half step each on either side, its update by 4 with the product's and the sum's
+            assert ((x - y).abs() <= t * (4 * 2.0 ** -24 * (3 * float(lr) + w.abs()) + 2.0 ** -24 * w.abs())).all()
+            assert torch.equal(px, x.to(torch.bfloat16)) and torch.equal(py, y.to(torch.bfloat16))
