@@ -821,12 +821,23 @@ def fp8_cross_entropy_grad_workspace_bytes(M: int, N: int, K: int) -> int:
 
 _TARGET_BITS = {torch.int64: 64, torch.int32: 32}
 
+# What may hold E4M3 codes, where a call takes no other format: bytes or torch's type of
+# that format (another fp8 type's values would be read as this one's).
+_E4M3_CODES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+
+
+def _e4m3_codes(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype is torch.uint8:
+        return t
+    if t.dtype not in _E4M3_CODES:
+        if t.element_size() != 1:
+            return _as_codes(t, name)  # says so
+        raise ValueError(f"{name} must hold E4M3 codes (uint8, int8 or float8_e4m3fn), got {t.dtype}")
+    return t.view(torch.uint8)
+
 
 def _xent_operands(a, b, targets):
-    if a.dtype is not torch.uint8:
-        a = _as_codes(a, "a")
-    if b.dtype is not torch.uint8:
-        b = _as_codes(b, "b")
+    a, b = _e4m3_codes(a, "a"), _e4m3_codes(b, "b")
     _, M, K, lda = _rows2d(a, "a")
     _, N, Kb, ldb = _rows2d(b, "b")
     if K != Kb:

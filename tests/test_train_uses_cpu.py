@@ -1,5 +1,8 @@
 """Uses of the operators that end a training step which need no GPU: names, and
 refusals of the binding and of the objects before anything is launched."""
+import pytest
+import torch
+
 import fp8_tensor_scaled_quantize_amd as fp8mi
 
 
@@ -8,3 +11,25 @@ def test_the_optimizers_names():
     for name in ("adamw_step", "grad_norm"):
         assert name in fp8mi.__all__ and "fp8_" + name in fp8mi.__all__
         assert getattr(fp8mi, name) is getattr(fp8mi, "fp8_" + name)
+
+
+OTHERS = [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.bool]
+
+
+def test_cross_entropy_refuses_other_formats():
+    """Operands are E4M3 codes: tensors of another fp8 type have other values."""
+    a, b, t = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(9, 32, dtype=torch.uint8), torch.zeros(4, dtype=torch.int64)
+    f = torch.zeros(4)
+
+    def calls(x, y):
+        return (lambda: fp8mi.fp8_cross_entropy(x, y, t), lambda: fp8mi.fp8_cross_entropy_grad(x, y, t, f, f))
+
+    for dtype in OTHERS:
+        for x, y in ((a.view(dtype), b), (a, b.view(dtype))):
+            for call in calls(x, y):
+                with pytest.raises(ValueError, match="E4M3 codes"):
+                    call()
+    for dtype in (torch.int8, torch.float8_e4m3fn):  # only the device is wrong here
+        for call in calls(a.view(dtype), b.view(dtype)):
+            with pytest.raises(ValueError, match="host tensor"):
+                call()
