@@ -1011,6 +1011,9 @@ def fp8_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr: float | torch
             i = next(i for i in sorted({*at_m, *at_v}) if (i in at_m) != (i in at_v) or
                      exp_avgs[i].element_size() != 1 or exp_avg_sqs[i].element_size() != 1)
             raise ValueError(f"8-bit states of params[{i}] need 1-byte codes and scales for both")
+        if not all([t.dtype in _E4M3_CODES for t in codes]):
+            raise ValueError("8-bit states must hold E4M3 codes (uint8, int8 or float8_e4m3fn), got "
+                             f"{sorted({str(t.dtype) for t in codes if t.dtype not in _E4M3_CODES})}")
         scales = [*m_scales, *v_scales]
         blocks = [-(-sizes[i] // ADAMW_BLOCK) for i in at_m]
         if list(map(_numel, scales)) != blocks + blocks or not all(map(_contiguous, scales)) or not _all_f32(scales):

@@ -33,3 +33,19 @@ def test_cross_entropy_refuses_other_formats():
         for call in calls(a.view(dtype), b.view(dtype)):
             with pytest.raises(ValueError, match="host tensor"):
                 call()
+
+
+def test_eight_bit_states_refuse_other_formats():
+    w, one = torch.zeros(4), torch.zeros(1)
+
+    def step(m, v):
+        fp8mi.fp8_adamw_step([w], [w], [m], [v], 1, exp_avg_scales=[one], exp_avg_sq_scales=[one])
+
+    codes = torch.zeros(4, dtype=torch.uint8)
+    for dtype in OTHERS:
+        for m, v in ((codes.view(dtype), codes), (codes, codes.view(dtype))):
+            with pytest.raises(ValueError, match="E4M3 codes"):
+                step(m, v)
+    for dtype in (torch.int8, torch.float8_e4m3fn):  # only the device is wrong here
+        with pytest.raises(ValueError, match="host tensor"):
+            step(codes.view(dtype), codes.view(dtype))
