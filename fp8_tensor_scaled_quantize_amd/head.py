@@ -115,12 +115,13 @@ class Fp8Head:
     def freeze(self) -> None:
         """Quantize the weight for score (current scaling).  Called again, it fills
         the same storage, so that a captured score has the new weight."""
-        if self._frozen is None:
+        kept = self._frozen
+        if kept is None:
             w = self.weight
-            self._frozen = (torch.empty(w.shape, dtype=torch.uint8, device=w.device),
-                            torch.empty(1, dtype=torch.float32, device=w.device))
-        codes, inv = self._frozen
-        fp8_quantize_dynamic(self.weight, E4M3, LAYOUT_ROW, out_row=codes, scale_inv_out=inv)
+            kept = (torch.empty(w.shape, dtype=torch.uint8, device=w.device),
+                    torch.empty(1, dtype=torch.float32, device=w.device))
+        fp8_quantize_dynamic(self.weight, E4M3, LAYOUT_ROW, out_row=kept[0], scale_inv_out=kept[1])
+        self._frozen = kept
 
     def score(self, x: torch.Tensor, targets: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         """Loss of each target (0 where it is negative), fp32 of targets' shape;

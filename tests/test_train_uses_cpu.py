@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import fp8_tensor_scaled_quantize_amd as fp8mi
+from fp8_tensor_scaled_quantize_amd.head import Fp8Head
 
 
 def test_the_optimizers_names():
@@ -49,3 +50,12 @@ def test_eight_bit_states_refuse_other_formats():
     for dtype in (torch.int8, torch.float8_e4m3fn):  # only the device is wrong here
         with pytest.raises(ValueError, match="host tensor"):
             step(codes.view(dtype), codes.view(dtype))
+
+
+def test_a_freeze_that_fails_leaves_nothing_to_score_with():
+    head = Fp8Head(torch.ones(32), torch.zeros(9, 32))
+    for _ in range(2):
+        with pytest.raises(ValueError, match="host tensor"):
+            head.freeze()
+        with pytest.raises(RuntimeError, match="freeze"):
+            head.score(torch.zeros(2, 32), torch.zeros(2, dtype=torch.int64))
