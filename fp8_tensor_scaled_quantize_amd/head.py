@@ -18,8 +18,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (E4M3, LAYOUT_ROW, fp8_cross_entropy, fp8_cross_entropy_grad, fp8_quantize, fp8_quantize_dynamic,
-               fp8_ring_seed, fp8_rmsnorm, fp8_rmsnorm_grad, new_ring)
+from . import (E4M3, LAYOUT_ROW, fp8_cross_entropy, fp8_cross_entropy_grad, fp8_cross_entropy_workspace_bytes,
+               fp8_quantize, fp8_quantize_dynamic, fp8_ring_seed, fp8_rmsnorm, fp8_rmsnorm_grad, new_ring)
 from .mlp import _version
 
 
@@ -57,6 +57,18 @@ class Fp8Head:
             raise ValueError(f"targets are on {targets.device}, x on {x.device}")
         return x2, r2, targets.reshape(-1).contiguous()
 
+    def _check_weight(self, x2) -> None:
+        """What the weight's quantize and the loss would refuse, before the norm's ring moves."""
+        w, (rows, d) = self.weight, x2.shape
+        if w.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+            raise ValueError(f"weight must be bfloat16, float16 or float32, got {w.dtype}")
+        if w.dim() != 2 or w.shape[1] != d or w.stride(1) != 1:
+            raise ValueError(f"weight must be [vocabulary, {d}] with unit column stride, got {tuple(w.shape)}")
+        if w.device != x2.device:
+            raise ValueError(f"weight is on {w.device}, x on {x2.device}")
+        if rows and not fp8_cross_entropy_workspace_bytes(rows, w.shape[0], d):
+            raise ValueError(f"{rows} rows of {d} over a vocabulary of {w.shape[0]}: more than fp8_cross_entropy takes")
+
     def seed(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> None:
         """Seed the rings from the weight and a first batch, so that the first
         step has the tensors' own scales (a fresh ring holds scale 1)."""
@@ -74,6 +86,7 @@ class Fp8Head:
         loss over the targets that are not negative, an fp32 scalar (0 without
         any)."""
         x2, r2, t = self._rows(x, residual, targets)
+        self._check_weight(x2)
         s, dev = self.scale_inv, x.device
         h = x2 if r2 is None else torch.empty_like(x2)
         rstd = torch.empty(x2.shape[0], dtype=torch.float32, device=dev)
