@@ -486,7 +486,9 @@ FP8MI_API fp8mi_status fp8_act_grad(const void* dy, int dy_dtype, int64_t rows, 
  *   workspace  device scratch of fp8_cross_entropy_workspace_bytes bytes, 16-byte
  *              aligned, no initialisation; calls in flight on one workspace race.
  * M is at most 2^20, M (K + 64) below 2^30, N at most 2^28.  M == 0 writes the mean alone.
- * A logit that is infinite or NaN makes the row's loss NaN.
+ * A logit of -inf is a probability of zero, and a loss of +inf at the target; one of +inf or NaN, or
+ * nothing but -inf, makes the row's loss NaN.  The loss is taken from the largest logit's
+ * distance to the target's, so a small one is as precise beside large logits.
  */
 FP8MI_API fp8mi_status fp8_cross_entropy(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t M,
                                          int64_t N, int64_t K, const float* a_scale_inv, const float* b_scale_inv,
@@ -497,8 +499,12 @@ FP8MI_API size_t fp8_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t
 /*
  * fp8_cross_entropy_grad -- gradient of sum_i dloss_i loss_i with respect to the
  * head's operands, the logits computed once more:
- *   G(i,j) = exp(l(i,j) - lse_i) - [j = t_i]      rounded to fp16 (2^-11, or 2^-39 in all);
- *            0 for an ignored row, NaN for one whose target is N or more
+ *   G(i,j) = exp(l(i,j) - lse_i) - [j = t_i]      0 for an ignored row, NaN for one whose
+ *            target is N or more.  The exponential is fp32's: lse's rounding and its own
+ *            arithmetic make it a few 2^-24 (1 + |lse_i|) of itself, which is what the target's
+ *            entry of a confident row is off by.  Then G is rounded to fp16: by 2^-11 of
+ *            itself, or by 2^-39, so probabilities below 2^-28 lose bits and those below 2^-39
+ *            give no gradient
  *   da(i,k) = sb dloss_i sum_j G(i,j) dec(B(j,k))         fp32 sums, one bf16 rounding
  *   db(j,k) = sa sum_i dloss_i G(i,j) dec(A(i,k))         the codes and dloss of ignored rows
  *            are not used

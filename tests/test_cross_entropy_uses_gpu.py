@@ -55,6 +55,43 @@ def test_loss_of_a_confident_token(M, N, top):
     assert (np.abs(f64(lse) - (own + want)) <= 8 * U32 * (own + 1) + err).all()
 
 
+@pytest.mark.parametrize("M,N", [(8, 300), (300, 3000), (500, 9000), (300, 50000)])
+def test_infinite_logits(M, N):
+    """-inf is a probability of zero (a loss of +inf at the target), +inf and NaN make
+    the row's loss NaN, as does a row of nothing but -inf."""
+    K = 16
+    a, b = torch.zeros(M, K), torch.zeros(N, K)
+    a[:, 0] = 1.0
+    a[:, 1] = 448.0
+    b[:, 0] = (torch.arange(N) % 3).float() - 1
+    sb = torch.ones(N)
+    sb[7] = 1e38  # 448 * 448 * 1e38 is beyond fp32
+    b[7, 1] = -448.0
+    t = torch.arange(M) % 5
+    t[3] = 7
+    sb, t = sb.to(DEV), t.to(DEV)
+    loss, lse = fp8mi.fp8_cross_entropy(code(a).to(DEV), code(b).to(DEV), t, None, sb)
+    l = b[:, 0].double().numpy()
+    l[7] = -np.inf
+    all_ = np.log(np.exp(l).sum())
+    err = 200 * U32 * (1 + all_)
+    for i in range(M):
+        want = np.inf if int(t[i]) == 7 else all_ - l[int(t[i])]
+        assert (float(loss[i]) == want) if np.isinf(want) else abs(float(loss[i]) - want) <= err
+    assert (np.abs(f64(lse) - all_) <= err).all()
+    b[7, 1] = 448.0  # +inf
+    loss, lse = fp8mi.fp8_cross_entropy(code(a).to(DEV), code(b).to(DEV), t, None, sb)
+    assert torch.isnan(loss).all()
+    a[:, 1] = 0.0
+    a[2, 1] = 448.0  # row 2's logits are all -inf: its own scale as well as the columns'
+    b[:, 1] = -448.0
+    sb.fill_(1e38)
+    sa = torch.zeros(M, device=DEV)
+    sa[2] = 1.0
+    loss, lse = fp8mi.fp8_cross_entropy(code(a).to(DEV), code(b).to(DEV), t, sa, sb)
+    assert torch.isnan(loss[2]) and int(torch.isnan(loss).sum()) == 1
+
+
 # rows straight from the codes, the same in K splits of G^T A, tiles, tiles in K splits
 @pytest.mark.parametrize("M,N", [(40, 300), (1030, 700), (300, 3000), (1500, 600)])
 @pytest.mark.parametrize("size", [1.0, 1e-25, 1e25])
