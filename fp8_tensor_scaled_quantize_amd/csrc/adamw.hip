@@ -183,16 +183,20 @@ __device__ __forceinline__ uint32_t grid_steps(float y, float& k, float& f) {
 // y >= 0 rounded to the grid point above with the probability of its place between
 // the two: h16 / 2^16 against the 20 bits below a code's mantissa.  2^-120 takes E4M3's
 // exponents, its subnormals too, to fp32's, so that a code is the bits above those 20,
-// and a carry goes into the exponent as the codes' order does.
+// and a carry goes into the exponent as the codes' order does.  Exact from y = 2^-6 on;
+// below, the product is one of fp32's subnormals and is rounded first, by 2^-30 at most, so
+// that a y which is that near to its place takes the neighbouring code (44 of 10^8).
 __device__ __forceinline__ uint32_t round_code(float y, uint32_t h16) {
   const uint32_t bits = __float_as_uint(fminf(y, 448.0f) * 7.52316384526264e-37f);
   return (bits + (~(16u * h16) & 0xFFFF0u) + 7u) >> 20;
 }
 
-// Correctly rounded square root of a normal x (or 0, or one that is not finite) and
-// quotient x / s, given r = 1 / s correctly rounded: a code depends on the last bit
-// of what it rounds, and so does the next step; with these the codes are the
-// formula's, operation by operation, in IEEE arithmetic.
+// Correctly rounded square root of x (or 0, or one that is not finite), by comparing x with
+// the products of neighbours, and quotient x / s, given r = 1 / s correctly rounded
+// (Markstein's correction), for x from 2^-103 on: below, the remainders can leave fp32 and
+// the results be an ulp off (a v of 2^-103 is that of gradients of 10^-15).  A code depends on
+// the last bit of what it rounds, and so does the next step; with these the codes are
+// the formula's, operation by operation, in IEEE arithmetic, but for what is named here.
 __device__ __forceinline__ float exact_root(float x) {
   const float s = __builtin_amdgcn_sqrtf(x);  // within an ulp; at 0, infinity and NaN both comparisons are false
   const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
@@ -210,7 +214,8 @@ __device__ __forceinline__ float exact_reciprocal(float s) {
   return s != 0.0f ? fmaf(fmaf(-s, r, 1.0f), r, r) : 0.0f;
 }
 
-// A 32-bit integer hash (two multiplications between shifts).
+// A 32-bit integer hash: Appleby's finaliser (two multiplications between shifts).  The
+// elements after a group's first draw from it by Marsaglia's xorshift, 13, 17 and 5.
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
   h = (h ^ (h >> 13)) * 0xC2B2AE35u;
