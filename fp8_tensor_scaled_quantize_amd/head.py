@@ -175,5 +175,7 @@ class _Fp8HeadFn(torch.autograd.Function):
 def fp8_head_loss(x: torch.Tensor, targets: torch.Tensor, head: Fp8Head,
                   residual: torch.Tensor | None = None) -> torch.Tensor:
     """loss = head.forward(x, targets, residual) recorded for autograd: the
-    backward pass fills the gradients of x, residual and the head's weights."""
+    backward pass fills the gradients of x, residual and the head's weights.  (Its
+    backward is captured into a graph only while no eager graph of the same leaves is
+    alive; head.forward and head.backward capture at any time.)"""
     return _Fp8HeadFn.apply(x, residual, head.norm_weight, head.weight, targets, head)
